@@ -254,6 +254,162 @@ ta_status tree_attn_paged(const void* q, const int32_t* q_indptr, const void* pa
                           float sm_scale, const ta_paged_dims* dims, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ---- Serving a paged KV cache ----------------------------------------------
+ * What a decoding loop does to the cache that tree_attn_paged reads, besides
+ * verifying trees over it: append new tokens (norms and RoPE of their queries
+ * and keys in the same pass), attend one new token per sequence, drop the
+ * rejected nodes of a verified tree, copy pages (forking a sequence whose last
+ * page is partly filled).  The pages have no counterpart; the cache layout and
+ * the page table are those of tree_attn_paged:
+ *   pages        [num_pages, 2, h_kv, 16, head_dim] dtype
+ *   page_indptr  [B+1] int32, page_values [nnz_pages] int32,
+ *   length_info  [B] int32 (1..16 when the sequence owns a page)
+ * except that page_values may be longer than the table: page_indptr[B] <=
+ * nnz_pages (nnz_pages is the array's capacity).
+ *   batch_size   B, 1..16384
+ *   h_q, h_kv, head_dim, dtype, num_pages   as in ta_paged_dims
+ *   nnz_pages    entries of page_values (16 * nnz_pages <= INT32_MAX) */
+typedef struct {
+  int32_t batch_size;
+  int32_t h_q;
+  int32_t h_kv;
+  int32_t head_dim;
+  ta_dtype dtype;
+  int32_t num_pages;
+  int32_t nnz_pages;
+} ta_cache_dims;
+
+/* Bytes of device workspace each of the calls below needs for these dims (a
+ * multiple of 256; 0 on invalid or unsupported dims).  It holds the device
+ * status word (tree_attn_device_status) and, for tree_attn_decode_paged, the
+ * partial states of sequences that several CTAs share.  tree_attn's workspace
+ * rules apply: 256-byte aligned, zero-filled once before its first use, left
+ * ready for the next call by every call, one workspace per set of calls that
+ * may overlap on the GPU (two graphs that may replay at once are such calls).
+ * It depends on the dims and the current device's SM count only. */
+size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims);
+
+typedef enum {
+  TA_ROPE_HALF = 1,        /* pairs (j, j + rotary_dim / 2)                   */
+  TA_ROPE_INTERLEAVED = 2  /* pairs (2 j, 2 j + 1)                            */
+} ta_rope_layout;
+
+/* A rotation, filled by tree_attn_rope_init and passed to
+ * tree_attn_append_paged.  Pair j of a token at position p turns by
+ * p * turns[j] / 2^64 full turns (mod 1): the product of a position and a
+ * 64-bit fixed-point frequency keeps its fraction of a turn exactly, so far
+ * positions lose nothing. */
+typedef struct {
+  int32_t layout;       /* ta_rope_layout                                     */
+  int32_t rotary_dim;   /* elements rotated, from the head's first            */
+  float magnitude;      /* factor of cos and sin                              */
+  uint64_t turns[64];
+} ta_rope;
+
+/* Fills ``rope`` on the host.  layout: ta_rope_layout.  rotary_dim: a multiple
+ * of 16 in 16..128.  Pair j (of rotary_dim / 2) turns by
+ *   angle = position * scale * f_j,   f_j = theta^(-2 j / rotary_dim),
+ * or f_j = inv_freq[j] (a host array of rotary_dim / 2 doubles) when inv_freq
+ * is not NULL, which carries any rescaling of frequencies for long contexts.
+ * scale and every f_j finite, theta finite and > 0 (ignored with inv_freq),
+ * magnitude finite (1 for a plain rotation). */
+ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim, double theta,
+                              double scale, float magnitude, const double* inv_freq);
+
+/* Appends tokens to the cache.  The page table describes the cache after the
+ * call: the last n_b = append_indptr[b+1] - append_indptr[b] kv rows of
+ * sequence b receive its n_b new tokens, in order.
+ *   q, k, v        rows of total_new tokens, [h_q, head_dim] and
+ *                  [h_kv, head_dim] contiguous per token; q_stride, k_stride,
+ *                  v_stride elements from one token to the next (multiples of
+ *                  8, at least the row), so that views of one fused
+ *                  projection need no copy
+ *   append_indptr  [B+1] int32, from 0 to total_new
+ *   positions      [total_new] int32, any value (NULL iff rope is NULL)
+ *   q_weight, k_weight  [head_dim] dtype, or NULL for no norm: per head
+ *                  x <- x * w / sqrt(mean(x^2) + norm_eps)
+ *   norm_eps       finite, >= 0
+ *   rope           a filled ta_rope (read during the call), or NULL
+ *   q_out          [total_new, h_q, head_dim] contiguous (written): q after
+ *                  norm and rotation.  It may be q itself (q_stride = h_q *
+ *                  head_dim); otherwise it overlaps none of the inputs.
+ * k after norm and rotation goes to plane 0 of its slot, v as it is to
+ * plane 1.  Norm and rotation are float32, rounded once to dtype; cos and sin
+ * are those of the angle itself, not of an angle rounded to float32 as in
+ * tree_attn's rotary_mode 1 (the two differ by up to position * 2^-23).
+ * Every other slot of the cache keeps its contents.  No two sequences may
+ * share a page that receives tokens.  A token whose sequence's tables are
+ * inconsistent (or whose page is outside the pool) is not written to the
+ * cache, which tree_attn_device_status reports.  Pointers 16-byte aligned.
+ * Asynchronous on stream. */
+ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride,
+                                 int32_t total_new, const int32_t* append_indptr,
+                                 const int32_t* positions, const void* q_weight,
+                                 const void* k_weight, float norm_eps, const ta_rope* rope,
+                                 void* pages, const int32_t* page_indptr,
+                                 const int32_t* page_values, const int32_t* length_info,
+                                 void* q_out, const ta_cache_dims* dims, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Attention of one token per sequence over the paged cache: q [B, h_q,
+ * head_dim], row b attends every kv row of sequence b (its own key and value
+ * were appended before).  Writes out [B, h_q, head_dim] and the base-2 lse
+ * [B, h_q] (a sequence without kv rows gets out = 0 and lse = -inf).  The kv
+ * rows of the whole batch are split evenly over the GPU, whatever the
+ * sequences' lengths, and the parts merged through their lse; the result does
+ * not depend on timing.  A page index outside the pool reads zeros and slots
+ * past a sequence's length are never used, as in tree_attn_paged.
+ * Inconsistent page tables are reported by tree_attn_device_status and
+ * nothing is computed.  h_q / h_kv <= 128; q, pages and out 16-byte aligned.
+ * Asynchronous on stream. */
+ta_status tree_attn_decode_paged(const void* q, const void* pages, const int32_t* page_indptr,
+                                 const int32_t* page_values, const int32_t* length_info,
+                                 void* out, float* lse, float sm_scale,
+                                 const ta_cache_dims* dims, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Keeps the accepted nodes of verified trees and drops the others.  The last
+ * T = mn_indptr[b+1] - mn_indptr[b] kv rows of sequence b are its tree's nodes
+ * (as in tree_attn_paged); of those, accept_nodes[accept_indptr[b] ..
+ * accept_indptr[b+1]-1] -- strictly ascending node indices, a of them -- move
+ * to the first a tree rows: row kv - T + accept_nodes[j] goes to row
+ * kv - T + j, keys and values of every head.  The sequence then has
+ * kv - T + a rows.  Writes the new table (none of these arrays may overlap the
+ * old table):
+ *   new_page_indptr [B+1], new_length_info [B] (0 for a sequence left without
+ *                   pages), new_page_values [nnz_pages]: each sequence's first
+ *                   pages, in order (entries past new_page_indptr[B] keep
+ *                   their contents)
+ *   freed_pages     [nnz_pages]: the pages each sequence no longer needs, in
+ *                   table order; num_freed [1] their number (entries past it
+ *                   keep their contents)
+ * total_accept = accept_indptr[B].  Pages that receive rows belong to one
+ * sequence only.  When an indptr array, a length or a count (0 <= a <= T <= kv)
+ * is inconsistent nothing is written; a sequence whose accept_nodes are not
+ * ascending within [0, T), or reach a page outside the pool, keeps its rows
+ * as they are; tree_attn_device_status reports either.  pages 16-byte
+ * aligned.  Asynchronous on stream. */
+ta_status tree_attn_compact_paged(void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  const int32_t* mn_indptr, const int32_t* accept_indptr,
+                                  const int32_t* accept_nodes, int32_t total_accept,
+                                  int32_t* new_page_indptr, int32_t* new_page_values,
+                                  int32_t* new_length_info, int32_t* freed_pages,
+                                  int32_t* num_freed, const ta_cache_dims* dims,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Copies whole pages within the pool: page dst_pages[i] becomes a copy of page
+ * src_pages[i], i < n (int32 device arrays).  Only the pool's dims are used
+ * (num_pages, h_kv, head_dim).  A pair that names a page outside the pool, or
+ * whose dst_pages[i] is also another pair's source or destination, is not
+ * copied, and tree_attn_device_status reports it; the other pairs are.
+ * src_pages[i] == dst_pages[i] leaves the page as it is.  pages 16-byte
+ * aligned.  Asynchronous on stream. */
+ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int32_t* dst_pages,
+                               int32_t n, const ta_cache_dims* dims, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* ---- Split-KV ------------------------------------------------------------
  * The same tree attention with the kv tiles of long (sequence, q tile) pairs
  * cut into chunks that run as separate work items, so that a batch of few

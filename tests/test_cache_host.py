@@ -1,0 +1,245 @@
+"""CPU tests of the paged-cache calls: the references against other facts, the
+rotation table, and the arguments that the C entry points refuse before they
+launch anything."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+import tree_attention_gb300 as ta
+import workloads as wl
+from oracle import paged_cache_ref as ref
+from tree_attention_gb300 import build as ta_build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ta_build.build()
+    return ta.lib()
+
+
+# --------------------------------------------------------------------------
+# the references
+# --------------------------------------------------------------------------
+
+def test_decode_reference_is_tree_attention_of_single_nodes():
+    """A tree of one node that ends its sequence sees every kv row."""
+    rng = np.random.default_rng(3)
+    w = wl.build_workload("t", [wl.chain_tree(1) for _ in range(4)], h_q=4, h_kv=2, head_dim=64,
+                          dtype="bf16", tensor_seed=1, prefix_lens=[0, 15, 16, 60])
+    pk = wl.paged_from(w, seed=9, fill=0.0)
+    ro, rl = oracle.tree_attention_paged(w.q, w.q_indptr, pk.pages, pk.page_indptr,
+                                         pk.page_values, pk.last_page_len, w.mn_indptr,
+                                         w.tree_order, 0, w.sm_scale)
+    out, lse, mag, smag = ref.decode(w.q.double().numpy(), pk.pages.double().numpy(),
+                                     pk.page_indptr, pk.page_values, pk.last_page_len, w.sm_scale)
+    np.testing.assert_allclose(out, ro, atol=1e-6)
+    np.testing.assert_allclose(lse, rl, atol=1e-6)
+    assert (np.abs(out) <= mag + 1e-12).all() and rng is not None
+
+
+def test_rotation_reference():
+    """Norms are kept, positions only count through their difference, and the
+    two layouts are one rotation in another order of elements."""
+    rng = np.random.default_rng(0)
+    x, y = rng.normal(size=(2, 5, 3, 64))
+    freq = 1e4 ** (-np.arange(16) / 16.0)
+    pos = np.arange(5) + 70000
+    a = ref.rotate(x, pos, "half", 32, freq)
+    np.testing.assert_allclose((a ** 2).sum(-1), (x ** 2).sum(-1))
+    np.testing.assert_array_equal(a[..., 32:], x[..., 32:])
+    dots = [(ref.rotate(x, pos + s, "half", 32, freq)
+             * ref.rotate(y, pos[::-1] + s, "half", 32, freq)).sum(-1) for s in (0, 17)]
+    np.testing.assert_allclose(dots[0], dots[1], atol=1e-9)
+    order = np.arange(32).reshape(2, 16).T.reshape(-1)       # interleave the halves
+    b = ref.rotate(x[..., :32][..., order], pos, "interleaved", 32, freq)
+    np.testing.assert_allclose(b, a[..., :32][..., order], atol=1e-12)
+
+
+def test_compact_reference_keeps_paths():
+    rng = np.random.default_rng(1)
+    pool = rng.normal(size=(6, 2, 1, 16, 4))
+    indptr, values, last = [0, 3, 5], [4, 0, 2, 5, 1], [8, 3]
+    # sequence 0: 40 rows, 30 of them nodes; sequence 1: 19 rows, 19 nodes, nothing kept
+    p, ni, nv, nl, fr = ref.compact(pool, indptr, values, last, [0, 30, 49], [0, 3, 3], [0, 7, 29])
+    rows = lambda q, v, i: np.stack([q[v[r // 16], :, :, r % 16] for r in i])
+    np.testing.assert_array_equal(rows(p, values[:3], range(13)),
+                                  rows(pool, values[:3], list(range(10)) + [10, 17, 39]))
+    assert (ni, nv, nl, fr) == ([0, 1, 1], [4], [13, 0], [0, 2, 5, 1])
+
+
+# --------------------------------------------------------------------------
+# the rotation table
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("theta,scale,rd", [(1e4, 1.0, 128), (5e5, 0.25, 64), (1e4, -1.0, 16)])
+def test_rope_table_turns(lib, theta, scale, rd):
+    """turns / 2^64 is the frequency in turns; the table keeps at least 2^-53 of
+    the value (the doubles it is made from) and 2^-64 of a turn."""
+    r = ta.Rope("half", rd, theta=theta, scale=scale).struct
+    for j in range(rd // 2):
+        want = scale * theta ** (-2.0 * j / rd) / (2 * math.pi)
+        got = r.turns[j] / 2 ** 64
+        got -= 1.0 if want < 0 else 0.0
+        assert abs(got - want) <= 4 * 2.0 ** -53 * abs(want) + 2.0 ** -53
+    assert list(r.turns)[rd // 2:] == [0] * (64 - rd // 2)
+
+
+def test_rope_table_takes_frequencies(lib):
+    f = [0.5 ** i for i in range(8)]
+    a = ta.Rope("interleaved", 16, inv_freq=f, theta=float("nan"))
+    b = ta.Rope("interleaved", 16, theta=2.0 ** 8)
+    assert list(a.struct.turns)[:8] == pytest.approx(list(b.struct.turns)[:8], rel=1e-14)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=24), dict(rotary_dim=0), dict(rotary_dim=144), dict(theta=0.0),
+    dict(theta=float("inf")), dict(scale=float("nan")), dict(magnitude=float("inf")),
+    dict(inv_freq=[float("inf")] * 32),
+])
+def test_rope_refusals(lib, kw):
+    with pytest.raises(ta.TreeAttnError) as e:
+        ta.Rope("half", **{"rotary_dim": 64, **kw})
+    assert e.value.status == ta.TA_ERR_INVALID_ARGUMENT
+
+
+def test_rope_refuses_unknown_layouts_and_short_tables(lib):
+    with pytest.raises(ValueError):
+        ta.Rope("quarter", 64)
+    with pytest.raises(ValueError):
+        ta.Rope("half", 64, inv_freq=[1.0])
+    assert lib.tree_attn_rope_init(None, 1, 64, 1e4, 1.0, 1.0, None) == ta.TA_ERR_INVALID_ARGUMENT
+    r = ta.Rope("half", 64).struct
+    assert lib.tree_attn_rope_init(ctypes.byref(r), 3, 64, 1e4, 1.0, 1.0,
+                                   None) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+# --------------------------------------------------------------------------
+# refusals of the C entry points (fake pointers: nothing is launched)
+# --------------------------------------------------------------------------
+
+F = 0x10000
+ODD = ctypes.c_void_p(F + 8)
+
+
+def _dims(**kw):
+    d = dict(batch_size=3, h_q=8, h_kv=2, head_dim=128, dtype=ta.TA_BF16, num_pages=12,
+             nnz_pages=6)
+    d.update(kw)
+    return ta.CacheDims(**d)
+
+
+def _append(lib, dims=None, **kw):
+    a = dict(q=F, qs=1024, k=F, ks=256, v=F, vs=256, n=5, ai=F, pos=F, qw=F, kw=F, eps=1e-6,
+             rope=ctypes.byref(ta.Rope("half", 128).struct), pages=F, pi=F, pv=F, li=F, qo=F,
+             ws=2 * F, wsb=1 << 30)
+    a.update(kw)
+    return lib.tree_attn_append_paged(a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["n"],
+                                      a["ai"], a["pos"], a["qw"], a["kw"], a["eps"], a["rope"],
+                                      a["pages"], a["pi"], a["pv"], a["li"], a["qo"],
+                                      ctypes.byref(dims or _dims()), a["ws"], a["wsb"], None)
+
+
+def _decode(lib, dims=None, **kw):
+    a = dict(q=F, pages=F, pi=F, pv=F, li=F, out=F, lse=F, sm=0.1, ws=2 * F, wsb=1 << 30)
+    a.update(kw)
+    return lib.tree_attn_decode_paged(a["q"], a["pages"], a["pi"], a["pv"], a["li"], a["out"],
+                                      a["lse"], a["sm"], ctypes.byref(dims or _dims()), a["ws"],
+                                      a["wsb"], None)
+
+
+def _compact(lib, dims=None, **kw):
+    a = dict(pages=F, pi=F, pv=F, li=F, mn=F, ai=F, an=F, n=4, npi=3 * F, npv=4 * F, nli=5 * F,
+             fr=6 * F, nf=7 * F, ws=2 * F, wsb=1 << 30)
+    a.update(kw)
+    return lib.tree_attn_compact_paged(a["pages"], a["pi"], a["pv"], a["li"], a["mn"], a["ai"],
+                                       a["an"], a["n"], a["npi"], a["npv"], a["nli"], a["fr"],
+                                       a["nf"], ctypes.byref(dims or _dims()), a["ws"], a["wsb"],
+                                       None)
+
+
+def _copy(lib, dims=None, **kw):
+    a = dict(pages=F, src=F, dst=F, n=4, ws=2 * F, wsb=1 << 30)
+    a.update(kw)
+    return lib.tree_attn_copy_pages(a["pages"], a["src"], a["dst"], a["n"],
+                                    ctypes.byref(dims or _dims()), a["ws"], a["wsb"], None)
+
+
+CALLS = {"append": _append, "decode": _decode, "compact": _compact, "copy": _copy}
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("dims,expect", [
+    (dict(batch_size=0), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(h_q=7), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(h_kv=0), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(dtype=5), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(num_pages=0), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(nnz_pages=-1), ta.TA_ERR_INVALID_ARGUMENT),
+    (dict(nnz_pages=1 << 27), ta.TA_ERR_INVALID_ARGUMENT),     # kv rows past int32
+    (dict(head_dim=96), ta.TA_ERR_UNSUPPORTED),
+    (dict(h_q=258, h_kv=2), ta.TA_ERR_UNSUPPORTED),            # 129 heads per kv head
+    (dict(batch_size=16385), ta.TA_ERR_UNSUPPORTED),
+])
+def test_bad_dims(lib, call, dims, expect):
+    assert CALLS[call](lib, _dims(**dims)) == expect
+    assert ta.cache_workspace_size(_dims(**dims)) == 0
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("kw", [dict(pages=None), dict(pages=ODD), dict(ws=None),
+                                dict(ws=ctypes.c_void_p(2 * F + 16)), dict(wsb=16)])
+def test_bad_pool_or_workspace(lib, call, kw):
+    assert CALLS[call](lib, **kw) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("call", ["append", "decode", "compact"])
+@pytest.mark.parametrize("name", ["pi", "pv", "li"])
+def test_missing_table(lib, call, name):
+    assert CALLS[call](lib, **{name: None}) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=-1), dict(q=None), dict(k=None), dict(v=None), dict(qo=None), dict(ai=None),
+    dict(pos=None), dict(eps=-1.0), dict(eps=float("nan")), dict(q=ODD), dict(k=ODD), dict(v=ODD),
+    dict(qo=ODD), dict(qw=ODD), dict(kw=ODD), dict(qs=1028), dict(qs=1016), dict(ks=248),
+    dict(vs=0), dict(ks=-256),
+])
+def test_append_refusals(lib, kw):
+    assert _append(lib, **kw) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+def test_append_refuses_a_rotation_wider_than_the_head(lib):
+    assert _append(lib, _dims(head_dim=64)) == ta.TA_ERR_INVALID_ARGUMENT
+    blank = ta._RopeStruct()
+    assert _append(lib, rope=ctypes.byref(blank)) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+def test_append_of_nothing(lib):
+    assert _append(lib, n=0, q=None, k=None, v=None, qo=None) == ta.TA_OK
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(out=None), dict(lse=None), dict(q=ODD),
+                                dict(out=ODD), dict(sm=float("inf"))])
+def test_decode_refusals(lib, kw):
+    assert _decode(lib, **kw) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [
+    dict(n=-1), dict(mn=None), dict(ai=None), dict(an=None), dict(npi=None), dict(npv=None),
+    dict(nli=None), dict(fr=None), dict(nf=None),
+    dict(npi=F), dict(npv=F), dict(nli=F), dict(fr=F), dict(fr=4 * F),     # over the old table
+])
+def test_compact_refusals(lib, kw):
+    assert _compact(lib, **kw) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("kw", [dict(n=-1), dict(src=None), dict(dst=None)])
+def test_copy_refusals(lib, kw):
+    assert _copy(lib, **kw) == ta.TA_ERR_INVALID_ARGUMENT
+
+
+def test_copy_of_nothing(lib):
+    assert _copy(lib, n=0, src=None, dst=None) == ta.TA_OK

@@ -28,7 +28,7 @@ __all__ = [
     "TreeAttention", "PagedDims", "make_paged_dims", "paged_workspace_size", "tree_attn_paged",
     "MAX_CHUNKS", "split_workspace_size", "tree_attn_split", "merge_states", "last_cuda_error",
     "folds_rotation", "noalloc_device_status", "set_wait_hooks", "auto_split_chunks",
-    "set_scheduler",
+    "set_scheduler", "CacheDims", "Rope", "PagedCache", "cache_workspace_size",
 ]
 
 TA_OK = 0
@@ -67,6 +67,18 @@ class PagedDims(ctypes.Structure):
                 ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32),
                 ("nnz_pages", ctypes.c_int32)]
+
+
+class CacheDims(ctypes.Structure):
+    _fields_ = [("batch_size", ctypes.c_int32), ("h_q", ctypes.c_int32),
+                ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32),
+                ("nnz_pages", ctypes.c_int32)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
 
 
 _lib = None
@@ -134,6 +146,22 @@ def lib() -> ctypes.CDLL:
     L.tree_attn_merge_states.argtypes = [vp, vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
                                          ctypes.c_int, vp, vp, vp]
     L.tree_attn_merge_states.restype = ctypes.c_int
+    i32, i64, f32, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    cdims, rope = ctypes.POINTER(CacheDims), ctypes.POINTER(_RopeStruct)
+    L.tree_attn_cache_workspace_size.argtypes = [cdims]
+    L.tree_attn_cache_workspace_size.restype = sz
+    L.tree_attn_rope_init.argtypes = [rope, i32, i32, f64, f64, f32, vp]
+    L.tree_attn_rope_init.restype = ctypes.c_int
+    L.tree_attn_append_paged.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32p, i32p, vp, vp, f32,
+                                         rope, vp, i32p, i32p, i32p, vp, cdims, vp, sz, vp]
+    L.tree_attn_append_paged.restype = ctypes.c_int
+    L.tree_attn_decode_paged.argtypes = [vp, vp, i32p, i32p, i32p, vp, vp, f32, cdims, vp, sz, vp]
+    L.tree_attn_decode_paged.restype = ctypes.c_int
+    L.tree_attn_compact_paged.argtypes = [vp, i32p, i32p, i32p, i32p, i32p, i32p, i32, i32p, i32p,
+                                          i32p, i32p, i32p, cdims, vp, sz, vp]
+    L.tree_attn_compact_paged.restype = ctypes.c_int
+    L.tree_attn_copy_pages.argtypes = [vp, i32p, i32p, i32, cdims, vp, sz, vp]
+    L.tree_attn_copy_pages.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -447,3 +475,216 @@ class TreeAttention:
                   lse, self.rotary_mode, self.rope_scale, self.rope_theta, self.sm_scale,
                   self.workspace, stream)
         return out, lse
+
+
+def cache_workspace_size(dims: CacheDims) -> int:
+    return int(lib().tree_attn_cache_workspace_size(ctypes.byref(dims)))
+
+
+class Rope:
+    """A rotation for ``PagedCache.append``: ``layout`` "half" (pairs j, j +
+    rotary_dim / 2) or "interleaved" (pairs 2j, 2j + 1) on the first
+    ``rotary_dim`` elements of a head, pair j turning by ``position * scale *
+    theta ** (-2 j / rotary_dim)`` -- or ``position * scale * inv_freq[j]`` with
+    a table of rotary_dim / 2 frequencies, for any rescaling of them for long
+    contexts.  ``magnitude`` multiplies cos and sin."""
+
+    LAYOUTS = {"half": 1, "interleaved": 2}
+
+    def __init__(self, layout: str, rotary_dim: int, theta: float = 1e4, scale: float = 1.0,
+                 magnitude: float = 1.0, inv_freq=None):
+        if layout not in self.LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(self.LAYOUTS)}, got {layout!r}")
+        table = None
+        if inv_freq is not None:
+            freq = [float(f) for f in inv_freq]
+            if len(freq) != rotary_dim // 2:
+                raise ValueError("inv_freq must have rotary_dim / 2 entries")
+            table = (ctypes.c_double * len(freq))(*freq)
+        self.struct = _RopeStruct()
+        self.rotary_dim = int(rotary_dim)
+        st = lib().tree_attn_rope_init(ctypes.byref(self.struct), self.LAYOUTS[layout],
+                                       self.rotary_dim, float(theta), float(scale),
+                                       float(magnitude), table)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_rope_init")
+
+
+class PagedCache:
+    """A paged KV cache and its page table, with the calls of a decoding loop
+    on it (``include/tree_attn.h``, "Serving a paged KV cache").
+
+    ``pages [num_pages, 2, h_kv, 16, d]`` and the int32 table ``page_indptr
+    [B+1]``, ``page_values``, ``length_info [B]`` are CUDA tensors, held and not
+    copied: their contents may change between calls.  ``h_q`` is the number of
+    query heads.  The handle owns a workspace, so calls on it that may overlap
+    on the GPU need handles of their own (``with_table(..., workspace=None)``);
+    every call is asynchronous on ``stream`` (default: torch's current
+    stream), and ``device_status`` reports inconsistent tables."""
+
+    def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, workspace=None):
+        if pages.dim() != 5 or pages.shape[1] != 2 or pages.shape[3] != 16:
+            raise ValueError("pages must be [num_pages, 2, h_kv, 16, head_dim]")
+        _check_dev("pages", pages)
+        for name, t in (("page_indptr", page_indptr), ("page_values", page_values),
+                        ("length_info", length_info)):
+            _check_dev(name, t, torch.int32)
+            if t.get_device() != pages.get_device():
+                raise ValueError(f"{name} must be on the device of pages")
+        if page_indptr.numel() != length_info.numel() + 1:
+            raise ValueError("page_indptr must have one entry more than length_info")
+        self.pages, self.page_indptr = pages, page_indptr
+        self.page_values, self.length_info = page_values, length_info
+        self.dtype, self.device = pages.dtype, pages.device
+        self._dev = pages.get_device()
+        self.batch_size, self.h_q = length_info.numel(), int(h_q)
+        self.h_kv, self.head_dim = pages.shape[2], pages.shape[4]
+        self.dims = CacheDims(batch_size=self.batch_size, h_q=self.h_q, h_kv=self.h_kv,
+                              head_dim=self.head_dim, dtype=_dtype_code(pages.dtype),
+                              num_pages=pages.shape[0], nnz_pages=page_values.numel())
+        with torch.cuda.device(self._dev):
+            need = cache_workspace_size(self.dims)
+        if need == 0:
+            raise TreeAttnError(TA_ERR_UNSUPPORTED, "tree_attn_cache_workspace_size")
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            # zero-filled once: the library keeps its counters consistent afterwards
+            workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        _check_dev("workspace", workspace)
+        self.workspace = workspace
+        self._lib = lib()
+        self._table = (page_indptr.data_ptr(), page_values.data_ptr(), length_info.data_ptr())
+        self._pages = pages.data_ptr()
+        self._tail = (ctypes.byref(self.dims), workspace.data_ptr(),
+                      workspace.numel() * workspace.element_size())
+
+    def with_table(self, page_indptr, page_values, length_info, workspace="same"):
+        """A handle on the same pool with another page table (as ``compact``
+        writes); it shares this handle's workspace where that is large enough,
+        unless given another one (None: a new one)."""
+        return PagedCache(self.pages, page_indptr, page_values, length_info, self.h_q,
+                          self.workspace if isinstance(workspace, str) else workspace)
+
+    def _ptr(self, name, t, dtype, shape):
+        """Address of a contiguous tensor argument, checked."""
+        if t.get_device() != self._dev:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _rows(self, name, t, heads):
+        """Address and token stride of a [tokens, heads, d] argument."""
+        if t.get_device() != self._dev:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if t.dtype is not self.dtype:
+            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
+        d = self.head_dim
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+            raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+        st = t.stride()
+        if st[2] != 1 or (heads > 1 and st[1] != d):
+            raise ValueError(f"the rows of one token must be contiguous in {name}")
+        return t.data_ptr(), st[0] if t.shape[0] > 1 else heads * d
+
+    def _stream(self, stream):
+        if torch.cuda.current_device() != self._dev:
+            raise ValueError(f"the cache is on {self.device}, which is not the current device")
+        if stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _done(self, status, what):
+        if status != TA_OK:
+            raise TreeAttnError(status, what)
+
+    def append(self, q, k, v, append_indptr, positions=None, *, rope: Optional[Rope] = None,
+               q_weight=None, k_weight=None, norm_eps: float = 1e-6, q_out=None, stream=None):
+        """Write new tokens' keys and values to the last rows of their
+        sequences (``append_indptr [B+1]``) and return their queries, after the
+        norm (where a weight is given) and the rotation (with ``rope``, at
+        ``positions [tokens]``).  q, k, v are ``[tokens, heads, d]`` and may be
+        views of one fused projection."""
+        qp, qs = self._rows("q", q, self.h_q)
+        kp, ks = self._rows("k", k, self.h_kv)
+        vp, vs = self._rows("v", v, self.h_kv)
+        n = q.shape[0]
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("q, k and v must have the same number of tokens")
+        if rope is not None and positions is None:
+            raise ValueError("rope needs positions")
+        st = self._stream(stream)
+        if q_out is None:
+            q_out = torch.empty((n, self.h_q, self.head_dim), dtype=self.dtype, device=self.device)
+        d = (self.head_dim,)
+        self._done(self._lib.tree_attn_append_paged(
+            qp, qs, kp, ks, vp, vs, n,
+            self._ptr("append_indptr", append_indptr, torch.int32, (self.batch_size + 1,)),
+            None if positions is None else self._ptr("positions", positions, torch.int32, (n,)),
+            None if q_weight is None else self._ptr("q_weight", q_weight, self.dtype, d),
+            None if k_weight is None else self._ptr("k_weight", k_weight, self.dtype, d),
+            norm_eps, None if rope is None else ctypes.byref(rope.struct), self._pages,
+            *self._table, self._ptr("q_out", q_out, self.dtype, (n, self.h_q, self.head_dim)),
+            *self._tail, st), "tree_attn_append_paged")
+        return q_out
+
+    def decode(self, q, sm_scale: float, out=None, lse=None, stream=None):
+        """Attention of one new token per sequence, ``q [B, h_q, d]``, over all
+        its kv rows; returns ``out`` and the base-2 ``lse [B, h_q]``."""
+        shape = (self.batch_size, self.h_q, self.head_dim)
+        st = self._stream(stream)
+        qp = self._ptr("q", q, self.dtype, shape)
+        if out is None:
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+        if lse is None:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=self.device)
+        self._done(self._lib.tree_attn_decode_paged(
+            qp, self._pages, *self._table, self._ptr("out", out, self.dtype, shape),
+            self._ptr("lse", lse, torch.float32, shape[:2]), sm_scale, *self._tail, st),
+            "tree_attn_decode_paged")
+        return out, lse
+
+    def compact(self, mn_indptr, accept_indptr, accept_nodes, *, new_page_indptr=None,
+                new_page_values=None, new_length_info=None, freed_pages=None, num_freed=None,
+                stream=None):
+        """Keep the accepted nodes (``accept_nodes`` ascending per sequence) of
+        the trees that end the sequences (``mn_indptr``), moving their rows down
+        behind the prefix.  Returns the new ``page_indptr, page_values,
+        length_info`` (for ``with_table``), the freed pages and their number
+        ``[1]``, all on the device."""
+        st = self._stream(stream)
+        b1, nnz = self.batch_size + 1, self.page_values.numel()
+
+        def array(name, t, n):
+            if t is None:
+                t = torch.empty(n, dtype=torch.int32, device=self.device)
+            return t, self._ptr(name, t, torch.int32, (n,))
+
+        outs = [array("new_page_indptr", new_page_indptr, b1),
+                array("new_page_values", new_page_values, nnz),
+                array("new_length_info", new_length_info, b1 - 1),
+                array("freed_pages", freed_pages, nnz), array("num_freed", num_freed, 1)]
+        n = accept_nodes.numel()
+        self._done(self._lib.tree_attn_compact_paged(
+            self._pages, *self._table, self._ptr("mn_indptr", mn_indptr, torch.int32, (b1,)),
+            self._ptr("accept_indptr", accept_indptr, torch.int32, (b1,)),
+            self._ptr("accept_nodes", accept_nodes, torch.int32, (n,)), n,
+            *[p for _, p in outs], *self._tail, st), "tree_attn_compact_paged")
+        return tuple(t for t, _ in outs)
+
+    def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
+        """``pages[dst_pages[i]] = pages[src_pages[i]]``; no destination may be
+        another pair's source or destination."""
+        st = self._stream(stream)
+        n = (src_pages.numel(),)
+        self._done(self._lib.tree_attn_copy_pages(
+            self._pages, self._ptr("src_pages", src_pages, torch.int32, n),
+            self._ptr("dst_pages", dst_pages, torch.int32, n), n[0], *self._tail, st),
+            "tree_attn_copy_pages")
+
+    def device_status(self, stream=None) -> int:
+        """Synchronise the stream and return (and clear) the device status."""
+        return device_status(self.workspace, stream)

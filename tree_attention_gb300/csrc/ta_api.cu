@@ -1,6 +1,7 @@
 // ta_api.cu -- host side of the C ABI declared in include/tree_attn.h:
-// argument validation, workspace layout, TMA tensor-map encoding and the two
-// launches (plan kernel, persistent attention kernel) of one tree_attn call.
+// argument validation, workspace layout, TMA tensor-map encoding and the
+// launches (plan kernel, persistent attention kernel) of one tree_attn call,
+// and those of the paged-cache calls.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -828,6 +829,241 @@ ta_status tree_attn_paged(const void* q, const int32_t* q_indptr, const void* pa
     e = bf16 ? ta::launch_attn<128, true, true>(tm_q, tm_pages, tm_pages, ap, grid, st)
              : ta::launch_attn<128, false, true>(tm_q, tm_pages, tm_pages, ap, grid, st);
   return cuda_status(e);
+}
+
+}  // extern "C"
+
+
+// ---------------------------------------------------------------------------
+// serving a paged KV cache
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxCacheBatch = 16384;
+
+bool cache_dims_valid(const ta_cache_dims* d) {
+  if (!d) return false;
+  if (d->batch_size < 1 || d->h_q < 1 || d->h_kv < 1 || d->h_q % d->h_kv != 0) return false;
+  if (d->dtype != TA_FP16 && d->dtype != TA_BF16) return false;
+  if (d->head_dim < 1 || d->num_pages < 1 || d->nnz_pages < 0) return false;
+  if ((int64_t)d->nnz_pages * ta::kPageSize > INT32_MAX) return false;
+  return true;
+}
+
+ta_status cache_dims_supported(const ta_cache_dims* d) {
+  if (d->head_dim != 64 && d->head_dim != 128) return TA_ERR_UNSUPPORTED;
+  if (d->h_q / d->h_kv > ta::kMaxGroup || d->batch_size > kMaxCacheBatch)
+    return TA_ERR_UNSUPPORTED;
+  // a token's rows and a page's column blocks stay far inside int32
+  if ((int64_t)(d->h_q + 2 * (int64_t)d->h_kv) * d->head_dim > (1 << 24)) return TA_ERR_UNSUPPORTED;
+  return TA_OK;
+}
+
+// Checks shared by the cache calls.
+ta_status check_cache(const ta_cache_dims* dims, const void* pages, const void* workspace,
+                      size_t workspace_bytes) {
+  if (!cache_dims_valid(dims)) return TA_ERR_INVALID_ARGUMENT;
+  const ta_status sup = cache_dims_supported(dims);
+  if (sup != TA_OK) return sup;
+  if (!pages || !workspace) return TA_ERR_INVALID_ARGUMENT;
+  if (!aligned(pages, 16) || !aligned(workspace, 256)) return TA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < tree_attn_cache_workspace_size(dims)) return TA_ERR_INVALID_ARGUMENT;
+  return TA_OK;
+}
+
+ta_status check_table(const ta_cache_dims* dims, const int32_t* page_indptr,
+                      const int32_t* page_values, const int32_t* length_info) {
+  if (!page_indptr || !length_info) return TA_ERR_INVALID_ARGUMENT;
+  if (dims->nnz_pages > 0 && !page_values) return TA_ERR_INVALID_ARGUMENT;
+  return TA_OK;
+}
+
+ta::PageTable page_table(const ta_cache_dims* d, const int32_t* page_indptr,
+                         const int32_t* page_values, const int32_t* length_info) {
+  return ta::PageTable{page_indptr, page_values, length_info, d->batch_size, d->nnz_pages,
+                       d->num_pages};
+}
+
+unsigned int* error_word(void* workspace) { return &static_cast<WsHeader*>(workspace)->error; }
+
+}  // namespace
+
+extern "C" {
+
+size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims) {
+  if (!cache_dims_valid(dims) || cache_dims_supported(dims) != TA_OK) return 0;
+  return 256;
+}
+
+ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim, double theta,
+                              double scale, float magnitude, const double* inv_freq) {
+  if (!rope) return TA_ERR_INVALID_ARGUMENT;
+  if (layout != TA_ROPE_HALF && layout != TA_ROPE_INTERLEAVED) return TA_ERR_INVALID_ARGUMENT;
+  if (rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16 != 0) return TA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(scale) || !std::isfinite(magnitude)) return TA_ERR_INVALID_ARGUMENT;
+  if (!inv_freq && (!std::isfinite(theta) || !(theta > 0.0))) return TA_ERR_INVALID_ARGUMENT;
+  ta_rope r{};
+  r.layout = layout;
+  r.rotary_dim = rotary_dim;
+  r.magnitude = magnitude;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int j = 0; j < rotary_dim / 2; ++j) {
+    const double f = inv_freq ? inv_freq[j] : std::pow(theta, -2.0 * j / rotary_dim);
+    const double turns = scale * f / two_pi;
+    if (!std::isfinite(turns)) return TA_ERR_INVALID_ARGUMENT;
+    // the fraction of a turn in 64-bit fixed point; a negative one as its
+    // complement, so that small fractions of either sign keep their bits
+    const double frac = turns - std::trunc(turns);
+    const uint64_t fixed = static_cast<uint64_t>(std::ldexp(std::fabs(frac), 64));
+    r.turns[j] = frac < 0 ? ~fixed + 1 : fixed;
+  }
+  *rope = r;
+  return TA_OK;
+}
+
+ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride,
+                                 int32_t total_new, const int32_t* append_indptr,
+                                 const int32_t* positions, const void* q_weight,
+                                 const void* k_weight, float norm_eps, const ta_rope* rope,
+                                 void* pages, const int32_t* page_indptr,
+                                 const int32_t* page_values, const int32_t* length_info,
+                                 void* q_out, const ta_cache_dims* dims, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  ta_status s = check_cache(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  if (total_new < 0) return TA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(norm_eps) || norm_eps < 0.f) return TA_ERR_INVALID_ARGUMENT;
+  if (rope && ((rope->layout != TA_ROPE_HALF && rope->layout != TA_ROPE_INTERLEAVED) ||
+               rope->rotary_dim < 16 || rope->rotary_dim % 16 != 0 ||
+               rope->rotary_dim > dims->head_dim))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (total_new == 0) return TA_OK;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (!q || !k || !v || !q_out || !append_indptr || (rope && !positions))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return TA_ERR_INVALID_ARGUMENT;
+  const int64_t rq = (int64_t)dims->h_q * dims->head_dim, rk = (int64_t)dims->h_kv * dims->head_dim;
+  if (q_stride % 8 || k_stride % 8 || v_stride % 8 || q_stride < rq || k_stride < rk ||
+      v_stride < rk)
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::AppendParams ap{};
+  ap.q = static_cast<const uint16_t*>(q);
+  ap.k = static_cast<const uint16_t*>(k);
+  ap.v = static_cast<const uint16_t*>(v);
+  ap.q_stride = q_stride;
+  ap.k_stride = k_stride;
+  ap.v_stride = v_stride;
+  ap.append_indptr = append_indptr;
+  ap.positions = positions;
+  ap.q_weight = static_cast<const uint16_t*>(q_weight);
+  ap.k_weight = static_cast<const uint16_t*>(k_weight);
+  ap.pages = static_cast<uint16_t*>(pages);
+  ap.q_out = static_cast<uint16_t*>(q_out);
+  ap.tab = page_table(dims, page_indptr, page_values, length_info);
+  ap.error = error_word(workspace);
+  ap.total_new = total_new;
+  ap.h_q = dims->h_q;
+  ap.h_kv = dims->h_kv;
+  ap.eps = norm_eps;
+  if (rope) {
+    ap.rope_layout = rope->layout;
+    ap.rotary_dim = rope->rotary_dim;
+    ap.magnitude = rope->magnitude;
+    std::memcpy(ap.turns, rope->turns, sizeof(ap.turns));
+  }
+  return cuda_status(ta::launch_append(ap, dims->head_dim, dims->dtype == TA_BF16,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+ta_status tree_attn_decode_paged(const void* q, const void* pages, const int32_t* page_indptr,
+                                 const int32_t* page_values, const int32_t* length_info,
+                                 void* out, float* lse, float sm_scale,
+                                 const ta_cache_dims* dims, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  ta_status s = check_cache(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !std::isfinite(sm_scale))
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::DecodeParams dp{};
+  dp.q = static_cast<const uint16_t*>(q);
+  dp.pages = static_cast<const uint16_t*>(pages);
+  dp.out = static_cast<uint16_t*>(out);
+  dp.lse = lse;
+  dp.tab = page_table(dims, page_indptr, page_values, length_info);
+  dp.error = error_word(workspace);
+  dp.h_q = dims->h_q;
+  dp.h_kv = dims->h_kv;
+  dp.g = dims->h_q / dims->h_kv;
+  dp.scale_log2 = sm_scale * 1.4426950408889634f;
+  return cuda_status(ta::launch_decode(dp, dims->head_dim, dims->dtype == TA_BF16,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+ta_status tree_attn_compact_paged(void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  const int32_t* mn_indptr, const int32_t* accept_indptr,
+                                  const int32_t* accept_nodes, int32_t total_accept,
+                                  int32_t* new_page_indptr, int32_t* new_page_values,
+                                  int32_t* new_length_info, int32_t* freed_pages,
+                                  int32_t* num_freed, const ta_cache_dims* dims,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  ta_status s = check_cache(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (total_accept < 0 || !mn_indptr || !accept_indptr || (total_accept > 0 && !accept_nodes))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (!new_page_indptr || !new_length_info || !num_freed) return TA_ERR_INVALID_ARGUMENT;
+  if (dims->nnz_pages > 0 && (!new_page_values || !freed_pages)) return TA_ERR_INVALID_ARGUMENT;
+  if (new_page_indptr == page_indptr || new_length_info == length_info ||
+      (dims->nnz_pages > 0 && (new_page_values == page_values || freed_pages == page_values ||
+                               freed_pages == new_page_values)))
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::CompactParams cp{};
+  cp.pages = static_cast<uint4*>(pages);
+  cp.tab = page_table(dims, page_indptr, page_values, length_info);
+  cp.mn_indptr = mn_indptr;
+  cp.accept_indptr = accept_indptr;
+  cp.accept_nodes = accept_nodes;
+  cp.new_indptr = new_page_indptr;
+  cp.new_values = new_page_values;
+  cp.new_length = new_length_info;
+  cp.freed = freed_pages;
+  cp.num_freed = num_freed;
+  cp.error = error_word(workspace);
+  cp.total_accept = total_accept;
+  cp.h_kv = dims->h_kv;
+  cp.row_vecs = dims->head_dim / 8;
+  return cuda_status(ta::launch_compact(cp, static_cast<cudaStream_t>(stream)));
+}
+
+ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int32_t* dst_pages,
+                               int32_t n, const ta_cache_dims* dims, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const ta_status s = check_cache(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  if (n < 0) return TA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return TA_OK;
+  if (!src_pages || !dst_pages) return TA_ERR_INVALID_ARGUMENT;
+  const int nsm = sm_count();
+  if (nsm <= 0) return cuda_failure();
+  ta::CopyParams cp{};
+  cp.pages = static_cast<uint4*>(pages);
+  cp.src = src_pages;
+  cp.dst = dst_pages;
+  cp.error = error_word(workspace);
+  cp.n = n;
+  cp.num_pages = dims->num_pages;
+  cp.page_vecs = (int64_t)2 * dims->h_kv * ta::kPageSize * (dims->head_dim / 8);
+  const int64_t want = ta::ceil_div(n * cp.page_vecs, 256);
+  const int grid = (int)std::min<int64_t>(want, 4LL * nsm);
+  return cuda_status(ta::launch_copy_pages(cp, grid, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

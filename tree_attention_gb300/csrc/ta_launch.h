@@ -1,5 +1,6 @@
 // ta_launch.h -- internal interface between the C-ABI host code (ta_api.cu)
-// and the kernel translation units (ta_plan.cu, ta_attn.cu).
+// and the kernel translation units (ta_plan.cu, ta_attn.cu, ta_merge.cu,
+// ta_cache.cu, ta_decode.cu).
 #pragma once
 
 #include <cuda.h>
@@ -113,6 +114,62 @@ struct MergeParams {
   int h_q, h_kv, g;
 };
 
+// Page table of a paged cache: sequence b owns page_values[page_indptr[b] ..
+// page_indptr[b+1]-1], its last page holding length_info[b] rows.
+struct PageTable {
+  const int32_t* page_indptr;
+  const int32_t* page_values;
+  const int32_t* length_info;
+  int batch, nnz_pages, num_pages;
+};
+
+struct AppendParams {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements from token to token
+  const int32_t* append_indptr;
+  const int32_t* positions;
+  const uint16_t *q_weight, *k_weight;    // null: no norm
+  uint16_t* pages;
+  uint16_t* q_out;
+  PageTable tab;
+  unsigned int* error;
+  int total_new, h_q, h_kv;
+  float eps;
+  int rope_layout, rotary_dim;            // layout 0: no rotation
+  float magnitude;
+  uint64_t turns[64];
+};
+
+struct DecodeParams {
+  const uint16_t* q;
+  const uint16_t* pages;
+  uint16_t* out;
+  float* lse;
+  PageTable tab;
+  unsigned int* error;
+  int h_q, h_kv, g;
+  float scale_log2;         // sm_scale * log2(e)
+};
+
+struct CompactParams {
+  uint4* pages;
+  PageTable tab;
+  const int32_t* mn_indptr;
+  const int32_t* accept_indptr;
+  const int32_t* accept_nodes;
+  int32_t *new_indptr, *new_values, *new_length, *freed, *num_freed;
+  unsigned int* error;
+  int total_accept, h_kv, row_vecs;       // row_vecs: 16-byte vectors per head row
+};
+
+struct CopyParams {
+  uint4* pages;
+  const int32_t *src, *dst;
+  unsigned int* error;
+  int n, num_pages;
+  int64_t page_vecs;                      // 16-byte vectors per page
+};
+
 // Plan kernel: sequence/tile enumeration, tile classification and LPT
 // ordering.  ``grid`` >= max_pairs.
 cudaError_t launch_plan(const PlanParams& p, int grid, cudaStream_t stream);
@@ -140,6 +197,18 @@ cudaError_t launch_merge(const MergeParams& p, int head_dim, bool bf16, int grid
 cudaError_t launch_merge_states(const void* parts, const float* lses, int n_parts,
                                 long long rows, int head_dim, bool bf16, void* out, float* lse,
                                 int grid, cudaStream_t stream);
+
+// Appends tokens to the cache (norm and rotation of q and k on the way).
+cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, cudaStream_t stream);
+
+// One token per sequence against the paged cache.
+cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, cudaStream_t stream);
+
+// Accepted tree nodes moved down, new page table, freed pages.
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+// pages[dst[i]] = pages[src[i]].
+cudaError_t launch_copy_pages(const CopyParams& p, int grid, cudaStream_t stream);
 
 // Persistent tree-attention kernel.
 template <int D, bool BF16, bool PAGED>
