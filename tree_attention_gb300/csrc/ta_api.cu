@@ -892,7 +892,8 @@ extern "C" {
 
 size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims) {
   if (!cache_dims_valid(dims) || cache_dims_supported(dims) != TA_OK) return 0;
-  return 256;
+  return ta::decode_workspace(dims->batch_size, dims->h_kv, dims->h_q / dims->h_kv, dims->head_dim,
+                              std::max(1, sm_count())).total;
 }
 
 ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim, double theta,
@@ -1001,7 +1002,14 @@ ta_status tree_attn_decode_paged(const void* q, const void* pages, const int32_t
   dp.h_kv = dims->h_kv;
   dp.g = dims->h_q / dims->h_kv;
   dp.scale_log2 = sm_scale * 1.4426950408889634f;
-  return cuda_status(ta::launch_decode(dp, dims->head_dim, dims->dtype == TA_BF16,
+  const int nsm = sm_count();
+  if (nsm <= 0) return cuda_failure();
+  const ta::DecodeWorkspace w =
+      ta::decode_workspace(dims->batch_size, dims->h_kv, dp.g, dims->head_dim, nsm);
+  dp.groups = w.groups;
+  dp.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_parts);
+  dp.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + w.off_counters);
+  return cuda_status(ta::launch_decode(dp, dims->head_dim, dims->dtype == TA_BF16, nsm,
                                        static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,6 +1,38 @@
 // ta_decode.cu -- attention of one token per sequence over a paged KV cache.
+//
+//   out = sum_j 2^(s_j - lse) v_j,  s_j = log2(e) sm_scale q.k_j,
+//   lse = log2 sum_j 2^s_j
+//
+// over the kv rows j of a sequence, for the g query heads that share a kv
+// head.  Every key and value is read once and serves g heads: g flops per byte
+// at 16 bits, far below the ~290 where the tensor cores would bound it, so the
+// kernel is built around the loads.
+//
+// * The unit of work is one page of one kv head, 16 rows of K and of V, each a
+//   contiguous block.  The units of the whole batch, numbered kv head by kv head
+//   and within one in page-table order, are cut into equal ranges, one per
+//   warp of a grid of one CTA per SM: no sequence lengths, however ragged,
+//   leave an SM idle, and page_indptr is already the prefix sum this needs.
+// * A warp's lanes load their operands of mma.sync straight from global memory
+//   in 16-byte pieces, without shared memory: a fragment's element order is
+//   free as long as both operands agree, so a lane's 8 consecutive elements
+//   are two k-steps of its fragments (keys) or, paired with the neighbouring
+//   token's by a byte permute, four m-tiles (values).
+// * S^T = K Q^T has 16 tokens by 8 heads, O^T = V^T P^T 16 elements by 8 heads,
+//   so g <= 8 heads cost one tile each and the weights pass from one product to
+//   the other by a transposition within registers (movmatrix).
+// * A page's keys are consumed by the first product before its softmax, and
+//   the next page's are requested into the same registers right there (and so
+//   the values after the second product): each warp always has a page in
+//   flight with no second set of registers.
+// * A range may hold parts of several sequences.  A sequence that lies in one
+//   warp's range is written by it; the parts of one that spans warps are
+//   merged in shared memory, and of one that spans CTAs by the last of its
+//   CTAs to finish (a counter), in CTA order, so results do not depend on
+//   timing.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "ta_device.cuh"
@@ -9,82 +41,465 @@
 namespace ta {
 namespace {
 
-constexpr int kDecodeThreads = 128;
+// 16 bytes that are read once: not kept in L1.
+__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
-// One CTA per (q head, sequence); each warp takes every fourth kv row with a
-// running maximum and sum, then the warps' states are merged.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kDecodeThreads) decode_kernel(const DecodeParams p) {
-  constexpr int V = D / 32, W = kDecodeThreads / 32;
-  __shared__ float s_o[W][D], s_m[W], s_l[W];
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// NT tiles of 8 heads per warp.  The warps per CTA follow from the registers a
+// lane needs (a page of K and of V, Q, O: 32 + 32 + 16 NT + 32 NT for d = 128).
+template <int D, int NT>
+struct Shape {
+  static constexpr int kWarps = D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 16 : 12);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kState = kHeads * D + 2 * kHeads;   // floats: O, then m, then l
+  static constexpr int kPieces = 2 * kWarps;               // parts a CTA can hold
+};
+
+// The largest b with s_indptr[b] <= x, over batch sequences; by one warp.
+__device__ __forceinline__ int find_in(const int32_t* s_indptr, int batch, int x, int lane) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33;
+    const int at = lo + (lane + 1) * step;
+    const bool le = at < hi && s_indptr[at] <= x;
+    lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
+    decode_kernel(const DecodeParams p) {
+  using S = Shape<D, NT>;
+  constexpr int W = S::kWarps, KS = D / 32, VH = D / 64;
+  // the exponent that a weight may reach over its reference, and where a moved
+  // reference puts the largest: fp16 weights are held 2^7 higher than bf16
+  // ones, as what lies 2^-24 below a weight of one is the type's end and long
+  // sequences have mass there
+  constexpr float kTop = BF16 ? 8.f : 15.f, kRef = BF16 ? 0.f : 7.f;
+  extern __shared__ __align__(16) float s_state[];         // [kPieces][kState]
+  int32_t* s_indptr = reinterpret_cast<int32_t*>(s_state + S::kPieces * S::kState);
+  uint8_t* s_len = reinterpret_cast<uint8_t*>(s_indptr + p.tab.batch + 1);
+  __shared__ int s_seg[S::kPieces];                        // the sequence and kv head of each part
+  __shared__ int s_last;
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int batch = p.tab.batch;
+
+  // the page table's offsets and last lengths, checked as a whole
   bool bad = false;
-  for (int i = threadIdx.x; i < p.tab.batch; i += kDecodeThreads) {
-    const int p0 = p.tab.page_indptr[i], p1 = p.tab.page_indptr[i + 1];
-    const int last = p.tab.length_info[i];
-    bad |= p0 < 0 || p1 < p0 || p1 > p.tab.nnz_pages || (i == 0 && p0 != 0) ||
-           (p1 > p0 && (last < 1 || last > kPageSize));
+  for (int i = tid; i <= batch; i += S::kThreads) {
+    const int a = p.tab.page_indptr[i];
+    s_indptr[i] = a;
+    bad |= i == 0 ? a != 0 : a < 0 || a > p.tab.nnz_pages;
+    if (i < batch) {
+      const int e = p.tab.page_indptr[i + 1], len = p.tab.length_info[i];
+      bad |= e < a || (e > a && (len < 1 || len > kPageSize));
+      s_len[i] = (uint8_t)len;
+    }
   }
+  if (tid < S::kPieces) s_seg[tid] = -1;
   if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
+    if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
     return;
   }
-  const int p0 = p.tab.page_indptr[b], np = p.tab.page_indptr[b + 1] - p0;
-  const int kv = np > 0 ? (np - 1) * kPageSize + p.tab.length_info[b] : 0;
-  const size_t row_q = (size_t)b * p.h_q + h;
-  float q[V], o[V], m = -INFINITY, l = 0.f, lc = 0.f;
-  for (int i = 0; i < V; ++i) {
-    q[i] = unpack2<BF16>(p.q[row_q * D + lane * V + i]).x;
-    o[i] = 0.f;
+  // sequences without rows
+  for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+    if (s_indptr[b] != s_indptr[b + 1]) continue;
+    uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.h_q * D);
+    for (int i = tid; i < p.h_q * (D / 8); i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < p.h_q; i += S::kThreads) p.lse[(size_t)b * p.h_q + i] = -INFINITY;
   }
-  for (int r = warp; r < kv; r += W) {
-    const int page = p.tab.page_values[p0 + r / kPageSize];
-    const bool in = page >= 0 && page < p.tab.num_pages;
-    const uint16_t* k = p.pages + (((size_t)page * 2 * p.h_kv + h / p.g) * kPageSize + r % kPageSize) * D;
-    const uint16_t* v = k + (size_t)p.h_kv * kPageSize * D;
-    float s = 0.f, x[V];
-    for (int i = 0; i < V; ++i) {
-      s += in ? q[i] * unpack2<BF16>(k[lane * V + i]).x : 0.f;
-      x[i] = in ? unpack2<BF16>(v[lane * V + i]).x : 0.f;
+
+  // this CTA's and this warp's range of units
+  const int P = s_indptr[batch];
+  const int64_t U = (int64_t)P * p.h_kv;
+  const int group = blockIdx.x % p.groups;                 // of the heads of one kv head
+  const int cta = blockIdx.x / p.groups;
+  const int64_t ctas = min((int64_t)(gridDim.x / p.groups), (U + W - 1) / W);
+  if (cta >= ctas) return;
+  const int head0 = group * S::kHeads;                     // of the kv head's g
+  const int64_t u_end = ((int64_t)cta * W + warp + 1) * U / (ctas * W);
+  int64_t u = ((int64_t)cta * W + warp) * U / (ctas * W);
+
+  if (u < u_end) {
+    const int64_t u_first = u;
+    int kvh = (int)(u / P), pg = (int)(u % P);
+    int b = find_in(s_indptr, batch, pg, lane);
+    int seg_end = s_indptr[b + 1];
+    // physical pages of the next 32 units and of the 32 after them
+    auto pages_at = [&](int64_t x) {
+      return x + lane < u_end ? p.tab.page_values[(int)((x + lane) % P)] : 0;
+    };
+    int64_t ahead = u;
+    int pv = pages_at(u), pv_next = pages_at(u + 32);
+
+    uint4 qf[NT][KS], kf[2][KS], vf[4][VH];
+    float o[NT][4 * VH][4], m[NT][2], l[NT][2];
+    const uint16_t* k_page = nullptr;   // the page whose values are still to be requested
+    int rows = 0;                       // its rows that count; 0 for zeros
+    auto load_q = [&]() {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int h = head0 + n * 8 + r;
+        const uint16_t* q = p.q + ((size_t)b * p.h_q + (size_t)kvh * p.g + h) * D + 8 * c;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          qf[n][s] = h < p.g ? load_stream(q + 32 * s) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_k = [&]() {               // of unit u; sets k_page and rows
+      const int page = __shfl_sync(0xffffffffu, pv, (int)(u - ahead));
+      const bool in = page >= 0 && page < p.tab.num_pages;
+      rows = in ? (pg + 1 == seg_end ? s_len[b] : kPageSize) : 0;
+      k_page = p.pages + ((int64_t)page * 2 * p.h_kv + kvh) * (kPageSize * D);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          kf[i][s] = in ? load_stream(k_page + (r + 8 * i) * D + 32 * s + 8 * c)
+                        : make_uint4(0, 0, 0, 0);
+    };
+    auto load_v = [&]() {
+      const uint16_t* v = k_page + (int64_t)p.h_kv * kPageSize * D + 8 * r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int h = 0; h < VH; ++h)    // a slot past the last row may hold anything
+          vf[i][h] = tok < rows ? load_stream(v + tok * D + 64 * h) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto reset = [&]() {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -FLT_MAX;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4 * VH; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+      }
+    };
+    load_q();
+    load_k();
+    load_v();
+    reset();
+    while (true) {
+      // scores of the page's 16 tokens
+      float x[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          mma16816<BF16>(x[n], kf[0][s].x, kf[1][s].x, kf[0][s].y, kf[1][s].y, qf[n][s].x, qf[n][s].y);
+          mma16816<BF16>(y, kf[0][s].z, kf[1][s].z, kf[0][s].w, kf[1][s].w, qf[n][s].z, qf[n][s].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = (x[n][i] + y[i]) * p.scale_log2;
+      }
+      const bool seg_done = pg + 1 == seg_end;
+      const int len = seg_done ? s_len[b] : kPageSize;
+      const int b_now = b, kvh_now = kvh;
+      // the next unit's keys (and queries)
+      ++u;
+      const bool more = u < u_end;
+      if (more) {
+        if (++pg == P) {
+          pg = 0;
+          ++kvh;
+          b = -1;
+          seg_end = 0;
+        }
+        if (pg == seg_end) {
+          do ++b;
+          while (s_indptr[b + 1] == pg);
+          seg_end = s_indptr[b + 1];
+        }
+        if (u - ahead == 32) {
+          ahead = u;
+          pv = pv_next;
+          pv_next = pages_at(u + 32);
+        }
+        load_k();
+        if (seg_done) load_q();
+      }
+      // weights
+      if (len < kPageSize) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r + 8 * (i >> 1) >= len) x[n][i] = -INFINITY;
+      }
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) over |= x[n][i] - m[n][i & 1] > kTop;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(x[n][j], x[n][j + 2]);
+#pragma unroll
+            for (int i = 4; i <= 16; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const float moved = fmaxf(m[n][j], top - kRef);
+            const float f = exp2_approx(m[n][j] - moved);
+            m[n][j] = moved;
+            l[n][j] *= f;
+#pragma unroll
+            for (int t = 0; t < 4 * VH; ++t) {
+              o[n][t][j] *= f;
+              o[n][t][j + 2] *= f;
+            }
+          }
+      }
+      uint32_t w0[NT], w1[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = exp2_approx(x[n][i] - m[n][i & 1]);
+        l[n][0] += x[n][0] + x[n][2];
+        l[n][1] += x[n][1] + x[n][3];
+        // one rounding of each weight to 16 bits, for the tensor cores; the sum
+        // l takes them unrounded
+        w0[n] = transpose8x8(pack2<BF16>(x[n][0], x[n][1]));
+        w1[n] = transpose8x8(pack2<BF16>(x[n][2], x[n][3]));
+      }
+#pragma unroll
+      for (int h = 0; h < VH; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t v0 = word(vf[0][h], t), v1 = word(vf[1][h], t);
+          const uint32_t v2 = word(vf[2][h], t), v3 = word(vf[3][h], t);
+          const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+          const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<BF16>(o[n][4 * h + t], a0, a1, a2, a3, w0[n], w1[n]);
+        }
+      if (more) load_v();
+      if (!seg_done && more) continue;
+
+      // the end of a sequence or of the range
+      const int64_t seg_lo = (int64_t)kvh_now * P + s_indptr[b_now];
+      const bool whole = seg_done && seg_lo >= u_first;
+      const int piece = 2 * warp + (seg_lo >= u_first ? 1 : 0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float z = l[n][j];
+#pragma unroll
+          for (int i = 4; i <= 16; i <<= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
+          const int h = n * 8 + 2 * c + j;
+          if (whole) {
+            if (head0 + h < p.g) {
+              const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
+              const size_t row = (size_t)b_now * p.h_q + (size_t)kvh_now * p.g + head0 + h;
+#pragma unroll
+              for (int v = 0; v < VH; ++v) {
+                uint32_t y[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                  y[t] = pack2<BF16>(o[n][4 * v + t][j] * inv, o[n][4 * v + t][j + 2] * inv);
+                *reinterpret_cast<uint4*>(p.out + row * D + 64 * v + 8 * r) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              if (r == 0) p.lse[row] = m[n][j] + log2f(z);
+            }
+          } else {
+            float* st = s_state + piece * S::kState;
+#pragma unroll
+            for (int v = 0; v < VH; ++v) {
+              float4* y = reinterpret_cast<float4*>(st + h * D + 64 * v + 8 * r);
+              y[0] = make_float4(o[n][4 * v][j], o[n][4 * v][j + 2], o[n][4 * v + 1][j],
+                                 o[n][4 * v + 1][j + 2]);
+              y[1] = make_float4(o[n][4 * v + 2][j], o[n][4 * v + 2][j + 2], o[n][4 * v + 3][j],
+                                 o[n][4 * v + 3][j + 2]);
+            }
+            if (r == 0) {
+              st[S::kHeads * D + h] = m[n][j];
+              st[S::kHeads * D + S::kHeads + h] = z;
+            }
+          }
+        }
+      if (!whole && lane == 0) s_seg[piece] = kvh_now * batch + b_now;
+      if (!more) break;
+      reset();
     }
-    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    // compensated: thousands of small weights next to a large one must count
-    const float lf = l * f, ls = lf + w;
-    lc = lc * f + (lf >= w ? (lf - ls) + w : (w - ls) + lf);
-    l = ls;
-    for (int i = 0; i < V; ++i) o[i] = o[i] * f + w * x[i];
-  }
-  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l + lc;
   }
   __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-  for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w]);
-  for (int w = 0; w < W; ++w) ll += s_l[w] > 0.f ? s_l[w] * exp2f(s_m[w] - mm) : 0.f;
-  for (int i = threadIdx.x; i < D; i += kDecodeThreads) {
-    float acc = 0.f;
-    for (int w = 0; w < W; ++w) acc += s_l[w] > 0.f ? s_o[w][i] * exp2f(s_m[w] - mm) : 0.f;
-    p.out[row_q * D + i] = (uint16_t)pack2<BF16>(ll > 0.f ? acc / ll : 0.f, 0.f);
+
+  // parts of one sequence in several warps, then in several CTAs
+  const int64_t c_lo = (int64_t)cta * U / ctas, c_hi = ((int64_t)cta + 1) * U / ctas;
+  constexpr int V4 = D / 4;
+  auto finish = [&](int seg, int h, int i, float mx, float z, float4 a) {
+    const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
+    const size_t row = (size_t)(seg % batch) * p.h_q + (size_t)(seg / batch) * p.g + head0 + h;
+    reinterpret_cast<uint2*>(p.out + row * D)[i] =
+        make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
+    if (i == 0) p.lse[row] = mx + log2f(z);
+  };
+  const int heads = min(S::kHeads, p.g - head0);
+  for (int i0 = 0; i0 < S::kPieces;) {
+    const int seg = s_seg[i0];
+    int i1 = i0 + 1;
+    if (seg >= 0)
+      while (i1 < S::kPieces && (s_seg[i1] == seg || s_seg[i1] < 0)) ++i1;
+    if (seg < 0) {
+      i0 = i1;
+      continue;
+    }
+    const int64_t base = (int64_t)(seg / batch) * P;
+    const int64_t lo = base + s_indptr[seg % batch], hi = base + s_indptr[seg % batch + 1];
+    const bool whole = lo >= c_lo && hi <= c_hi;
+    const int slot = blockIdx.x * 2 + (lo >= c_lo ? 1 : 0);
+    for (int e = tid; e < heads * V4; e += S::kThreads) {
+      const int h = e / V4, i = e % V4;
+      float mx = -FLT_MAX, z = 0.f;
+      for (int k = i0; k < i1; ++k)
+        if (s_seg[k] >= 0) mx = fmaxf(mx, s_state[k * S::kState + S::kHeads * D + h]);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = i0; k < i1; ++k) {
+        if (s_seg[k] < 0) continue;
+        const float* st = s_state + k * S::kState;
+        const float f = exp2_approx(st[S::kHeads * D + h] - mx);
+        const float4 y = reinterpret_cast<const float4*>(st + h * D)[i];
+        z += f * st[S::kHeads * D + S::kHeads + h];
+        a.x += f * y.x;
+        a.y += f * y.y;
+        a.z += f * y.z;
+        a.w += f * y.w;
+      }
+      if (whole) {
+        finish(seg, h, i, mx, z, a);
+      } else {
+        float* st = p.parts + (size_t)slot * S::kState;
+        reinterpret_cast<float4*>(st + h * D)[i] = a;
+        if (i == 0) {
+          st[S::kHeads * D + h] = mx;
+          st[S::kHeads * D + S::kHeads + h] = z;
+        }
+      }
+    }
+    i0 = i1;
+    if (whole) continue;
+    // the CTAs that share the sequence: the last of them to come here merges
+    const int first = (int)(((lo + 1) * ctas - 1) / U), last = (int)((hi * ctas - 1) / U);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      int* n = p.counters + (size_t)seg * p.groups + group;
+      s_last = atomicAdd(n, 1) == last - first;
+      if (s_last) *n = 0;
+    }
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      for (int e = tid; e < heads * V4; e += S::kThreads) {
+        const int h = e / V4, i = e % V4;
+        auto part = [&](int k) {   // of CTA k: its second part where the sequence starts in it
+          return p.parts + (size_t)(((size_t)k * p.groups + group) * 2 +
+                                    (lo >= (int64_t)k * U / ctas ? 1 : 0)) * S::kState;
+        };
+        float mx = -FLT_MAX, z = 0.f;
+#pragma unroll 4
+        for (int k = first; k <= last; ++k) mx = fmaxf(mx, __ldcg(part(k) + S::kHeads * D + h));
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = first; k <= last; ++k) {
+          const float* st = part(k);
+          const float f = exp2_approx(__ldcg(st + S::kHeads * D + h) - mx);
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(st + h * D) + i);
+          z += f * __ldcg(st + S::kHeads * D + S::kHeads + h);
+          a.x += f * y.x;
+          a.y += f * y.y;
+          a.z += f * y.z;
+          a.w += f * y.w;
+        }
+        finish(seg, h, i, mx, z, a);
+      }
+    }
   }
-  if (threadIdx.x == 0) p.lse[row_q] = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+}
+
+template <int D, bool BF16, int NT>
+cudaError_t launch(const DecodeParams& p, int nsm, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  const size_t smem = (size_t)S::kPieces * S::kState * 4 + (size_t)(p.tab.batch + 1) * 4 + p.tab.batch;
+  const auto kern = decode_kernel<D, BF16, NT>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int per = nsm / p.groups > 0 ? nsm / p.groups : 1;
+  return launch_pdl(kern, dim3(per * p.groups), dim3(S::kThreads), smem, stream, p);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_heads(const DecodeParams& p, int nsm, cudaStream_t stream) {
+  return p.g <= 8 ? launch<D, BF16, 1>(p, nsm, stream) : launch<D, BF16, 2>(p, nsm, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, cudaStream_t stream) {
-  const dim3 g(p.h_q, p.tab.batch), b(kDecodeThreads);
+DecodeWorkspace decode_workspace(int batch, int h_kv, int g, int head_dim, int nsm) {
+  DecodeWorkspace w{};
+  const int heads = g <= 8 ? 8 : 16;
+  w.groups = (g + heads - 1) / heads;
+  const int64_t ctas = (int64_t)(nsm / w.groups > 0 ? nsm / w.groups : 1) * w.groups;
+  w.off_parts = 256;
+  w.off_counters = w.off_parts + round_up(ctas * 2 * (heads * (int64_t)head_dim + 2 * heads) * 4, 256);
+  w.total = w.off_counters + round_up((int64_t)batch * h_kv * w.groups * 4, 256);
+  return w;
+}
+
+cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int nsm,
+                          cudaStream_t stream) {
   if (head_dim == 128)
-    return bf16 ? launch_pdl(decode_kernel<128, true>, g, b, 0, stream, p)
-                : launch_pdl(decode_kernel<128, false>, g, b, 0, stream, p);
-  return bf16 ? launch_pdl(decode_kernel<64, true>, g, b, 0, stream, p)
-              : launch_pdl(decode_kernel<64, false>, g, b, 0, stream, p);
+    return bf16 ? launch_heads<128, true>(p, nsm, stream) : launch_heads<128, false>(p, nsm, stream);
+  return bf16 ? launch_heads<64, true>(p, nsm, stream) : launch_heads<64, false>(p, nsm, stream);
 }
 
 }  // namespace ta

@@ -147,9 +147,21 @@ struct DecodeParams {
   float* lse;
   PageTable tab;
   unsigned int* error;
+  float* parts;             // states of the sequences that several CTAs share
+  int* counters;            // per (kv head, sequence, head group): its CTAs done; 0 between calls
   int h_q, h_kv, g;
+  int groups;               // head groups per kv head (one CTA handles one)
   float scale_log2;         // sm_scale * log2(e)
 };
+
+// Workspace of launch_decode: header | parts | counters.  The parts come first,
+// as their size does not follow from the batch: calls with another batch size
+// find the counters in the same place.
+struct DecodeWorkspace {
+  int groups;
+  int64_t off_parts, off_counters, total;
+};
+DecodeWorkspace decode_workspace(int batch, int h_kv, int g, int head_dim, int nsm);
 
 struct CompactParams {
   uint4* pages;
@@ -202,7 +214,8 @@ cudaError_t launch_merge_states(const void* parts, const float* lses, int n_part
 cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, cudaStream_t stream);
 
 // One token per sequence against the paged cache.
-cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int nsm,
+                          cudaStream_t stream);
 
 // Accepted tree nodes moved down, new page table, freed pages.
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
