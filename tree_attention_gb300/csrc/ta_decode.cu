@@ -81,6 +81,8 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+constexpr int kMaxCtas = 256;   // most CTAs of the grid
+
 // NT tiles of 8 heads per warp.  The warps per CTA follow from the registers a
 // lane needs (a page of K and of V, Q, O: 32 + 32 + 16 NT + 32 NT for d = 128).
 template <int D, int NT>
@@ -90,6 +92,8 @@ struct Shape {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kState = kHeads * D + 2 * kHeads;   // floats: O, then m, then l
   static constexpr int kPieces = 2 * kWarps;               // parts a CTA can hold
+  static_assert(kPieces <= 32, "one lane per part");
+  static_assert(kPieces * kState >= kMaxCtas * kHeads + 4 * kThreads, "the last merge's sums fit");
 };
 
 // The largest b with s_indptr[b] <= x, over batch sequences; by one warp.
@@ -119,7 +123,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   int32_t* s_indptr = reinterpret_cast<int32_t*>(s_state + S::kPieces * S::kState);
   uint8_t* s_len = reinterpret_cast<uint8_t*>(s_indptr + p.tab.batch + 1);
   __shared__ int s_seg[S::kPieces];                        // the sequence and kv head of each part
-  __shared__ int s_last;
+  __shared__ int4 s_part[S::kPieces];                      // part, its s_seg, see below
+  __shared__ float s_factor[S::kPieces][S::kHeads];
+  __shared__ int s_count, s_merge[2];
+  __shared__ int2 s_range[2];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -372,97 +379,191 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   }
   __syncthreads();
 
-  // parts of one sequence in several warps, then in several CTAs
-  const int64_t c_lo = (int64_t)cta * U / ctas, c_hi = ((int64_t)cta + 1) * U / ctas;
-  constexpr int V4 = D / 4;
-  auto finish = [&](int seg, int h, int i, float mx, float z, float4 a) {
-    const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-    const size_t row = (size_t)(seg % batch) * p.h_q + (size_t)(seg / batch) * p.g + head0 + h;
-    reinterpret_cast<uint2*>(p.out + row * D)[i] =
-        make_uint2(pack2<BF16>(a.x * inv, a.y * inv), pack2<BF16>(a.z * inv, a.w * inv));
-    if (i == 0) p.lse[row] = mx + log2f(z);
-  };
-  const int heads = min(S::kHeads, p.g - head0);
-  for (int i0 = 0; i0 < S::kPieces;) {
-    const int seg = s_seg[i0];
-    int i1 = i0 + 1;
-    if (seg >= 0)
-      while (i1 < S::kPieces && (s_seg[i1] == seg || s_seg[i1] < 0)) ++i1;
-    if (seg < 0) {
-      i0 = i1;
-      continue;
+  // The parts left in shared memory, in range order: s_part lists them, with the
+  // first and one past the last of the parts of the same sequence.
+  if (warp == 0) {
+    const int seg = lane < S::kPieces ? s_seg[lane] : -1;
+    const unsigned have = __ballot_sync(0xffffffffu, seg >= 0);
+    const int at = __popc(have & ((1u << lane) - 1));
+    // the part before this one in the list, if it is of the same sequence
+    const unsigned below = have & ((1u << lane) - 1);
+    const int prev = __shfl_sync(0xffffffffu, seg, below ? 31 - __clz(below) : lane);
+    const unsigned starts = __ballot_sync(0xffffffffu, seg >= 0 && (!below || prev != seg));
+    if (seg >= 0) {
+      const unsigned upto = starts & (0xffffffffu >> (31 - lane));
+      const unsigned after = starts & ~(0xffffffffu >> (31 - lane));
+      const int g0 = 31 - __clz(upto), g1 = after ? __ffs(after) - 1 : 32;
+      s_part[at] = make_int4(lane, seg, __popc(have & ((1u << g0) - 1)),
+                             g1 == 32 ? __popc(have) : __popc(have & ((1u << g1) - 1)));
     }
+    if (lane == 0) s_count = __popc(have);
+  }
+  __syncthreads();
+  const int count = s_count;
+  if (count == 0) return;
+  const int heads = min(S::kHeads, p.g - head0);
+  const int64_t c_lo = (int64_t)cta * U / ctas, c_hi = ((int64_t)cta + 1) * U / ctas;
+  auto units_of = [&](int seg, int64_t& lo, int64_t& hi) {
     const int64_t base = (int64_t)(seg / batch) * P;
-    const int64_t lo = base + s_indptr[seg % batch], hi = base + s_indptr[seg % batch + 1];
+    lo = base + s_indptr[seg % batch];
+    hi = base + s_indptr[seg % batch + 1];
+  };
+  auto row_of = [&](int seg, int h) {
+    return (size_t)(seg % batch) * p.h_q + (size_t)(seg / batch) * p.g + head0 + h;
+  };
+  // each part's factor; a sequence that lies in this CTA is also normalised
+  for (int e = tid; e < count * S::kHeads; e += S::kThreads) {
+    const int h = e % S::kHeads;
+    const int4 me = s_part[e / S::kHeads];
+    float mx = -FLT_MAX, z = 0.f;
+    for (int k = me.z; k < me.w; ++k)
+      mx = fmaxf(mx, s_state[s_part[k].x * S::kState + S::kHeads * D + h]);
+    for (int k = me.z; k < me.w; ++k) {
+      const float* ml = s_state + s_part[k].x * S::kState + S::kHeads * D;
+      z += exp2_approx(ml[h] - mx) * ml[S::kHeads + h];
+    }
+    float f = exp2_approx(s_state[me.x * S::kState + S::kHeads * D + h] - mx);
+    int64_t lo, hi;
+    units_of(me.y, lo, hi);
+    const bool first = e / S::kHeads == me.z;
+    if (lo >= c_lo && hi <= c_hi) {
+      f *= z > 0.f || z != z ? 1.f / z : 0.f;
+      if (first && h < heads) p.lse[row_of(me.y, h)] = mx + log2f(z);
+    } else if (first) {
+      float* st = p.parts + (size_t)(blockIdx.x * 2 + (lo >= c_lo ? 1 : 0)) * S::kState;
+      st[S::kHeads * D + h] = mx;
+      st[S::kHeads * D + S::kHeads + h] = z;
+    }
+    s_factor[e / S::kHeads][h] = f;
+  }
+  __syncthreads();
+  constexpr int V4 = D / 4;
+  auto store_out = [&](int seg, int h, int i, float4 a) {
+    reinterpret_cast<uint2*>(p.out + row_of(seg, h) * D)[i] =
+        make_uint2(pack2<BF16>(a.x, a.y), pack2<BF16>(a.z, a.w));
+  };
+  int shared_seg[2] = {-1, -1};        // by slot: sequences that go on in other CTAs
+  for (int g0 = 0; g0 < count;) {
+    const int4 grp = s_part[g0];
+    int64_t lo, hi;
+    units_of(grp.y, lo, hi);
     const bool whole = lo >= c_lo && hi <= c_hi;
-    const int slot = blockIdx.x * 2 + (lo >= c_lo ? 1 : 0);
+    const int slot = lo >= c_lo ? 1 : 0;
+    if (!whole) shared_seg[slot] = grp.y;
     for (int e = tid; e < heads * V4; e += S::kThreads) {
       const int h = e / V4, i = e % V4;
-      float mx = -FLT_MAX, z = 0.f;
-      for (int k = i0; k < i1; ++k)
-        if (s_seg[k] >= 0) mx = fmaxf(mx, s_state[k * S::kState + S::kHeads * D + h]);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = i0; k < i1; ++k) {
-        if (s_seg[k] < 0) continue;
-        const float* st = s_state + k * S::kState;
-        const float f = exp2_approx(st[S::kHeads * D + h] - mx);
-        const float4 y = reinterpret_cast<const float4*>(st + h * D)[i];
-        z += f * st[S::kHeads * D + S::kHeads + h];
+#pragma unroll 4
+      for (int k = g0; k < grp.w; ++k) {
+        const float f = s_factor[k][h];
+        const float4 y = reinterpret_cast<const float4*>(s_state + s_part[k].x * S::kState + h * D)[i];
         a.x += f * y.x;
         a.y += f * y.y;
         a.z += f * y.z;
         a.w += f * y.w;
       }
-      if (whole) {
-        finish(seg, h, i, mx, z, a);
-      } else {
-        float* st = p.parts + (size_t)slot * S::kState;
-        reinterpret_cast<float4*>(st + h * D)[i] = a;
-        if (i == 0) {
-          st[S::kHeads * D + h] = mx;
-          st[S::kHeads * D + S::kHeads + h] = z;
-        }
-      }
+      if (whole)
+        store_out(grp.y, h, i, a);
+      else
+        reinterpret_cast<float4*>(p.parts + (size_t)(blockIdx.x * 2 + slot) * S::kState + h * D)[i] = a;
     }
-    i0 = i1;
-    if (whole) continue;
-    // the CTAs that share the sequence: the last of them to come here merges
-    const int first = (int)(((lo + 1) * ctas - 1) / U), last = (int)((hi * ctas - 1) / U);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      int* n = p.counters + (size_t)seg * p.groups + group;
-      s_last = atomicAdd(n, 1) == last - first;
-      if (s_last) *n = 0;
-    }
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      for (int e = tid; e < heads * V4; e += S::kThreads) {
-        const int h = e / V4, i = e % V4;
-        auto part = [&](int k) {   // of CTA k: its second part where the sequence starts in it
-          return p.parts + (size_t)(((size_t)k * p.groups + group) * 2 +
-                                    (lo >= (int64_t)k * U / ctas ? 1 : 0)) * S::kState;
-        };
-        float mx = -FLT_MAX, z = 0.f;
-#pragma unroll 4
-        for (int k = first; k <= last; ++k) mx = fmaxf(mx, __ldcg(part(k) + S::kHeads * D + h));
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = first; k <= last; ++k) {
-          const float* st = part(k);
-          const float f = exp2_approx(__ldcg(st + S::kHeads * D + h) - mx);
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(st + h * D) + i);
-          z += f * __ldcg(st + S::kHeads * D + S::kHeads + h);
-          a.x += f * y.x;
-          a.y += f * y.y;
-          a.z += f * y.z;
-          a.w += f * y.w;
-        }
-        finish(seg, h, i, mx, z, a);
-      }
-    }
+    g0 = grp.w;
   }
+  if (shared_seg[0] < 0 && shared_seg[1] < 0) return;
+
+  // sequences that several CTAs share: the last of these to come here merges
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    int merge = 0;
+    const int seg = shared_seg[tid];
+    if (seg >= 0) {
+      int64_t lo, hi;
+      units_of(seg, lo, hi);
+      const int first = (int)(((lo + 1) * ctas - 1) / U), last = (int)((hi * ctas - 1) / U);
+      int* n = p.counters + (size_t)seg * p.groups + group;
+      if (atomicAdd(n, 1) == last - first) {
+        *n = 0;
+        merge = 1;
+      }
+      s_range[tid] = make_int2(first, last - first + 1);
+    }
+    s_merge[tid] = merge;
+    __threadfence();
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int slot = 0; slot < 2; ++slot) {
+    if (!s_merge[slot]) continue;
+    const int seg = shared_seg[slot], first = s_range[slot].x, n = s_range[slot].y;
+    // of the CTAs the first holds the sequence's start, its second part
+    auto part = [&](int k) {
+      return p.parts + (size_t)(((size_t)(first + k) * p.groups + group) * 2 + (k == 0 ? 1 : 0)) * S::kState;
+    };
+    // the threads share the n parts of an element where there are more threads
+    const int items = heads * V4, share = S::kThreads / items > 0 ? min(n, S::kThreads / items) : 1;
+    float* s_f = s_state;                              // [n][kHeads]
+    float4* s_sum = reinterpret_cast<float4*>(s_state + kMaxCtas * S::kHeads);   // [share][items]
+    for (int h = warp; h < S::kHeads; h += W) {
+      float mx = -FLT_MAX, z = 0.f;
+      for (int k = lane; k < n; k += 32) {
+        const float v = __ldcg(part(k) + S::kHeads * D + h);
+        s_f[k * S::kHeads + h] = v;
+        mx = fmaxf(mx, v);
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+      for (int k = lane; k < n; k += 32) {
+        const float f = exp2_approx(s_f[k * S::kHeads + h] - mx);
+        s_f[k * S::kHeads + h] = f;
+        z += f * __ldcg(part(k) + S::kHeads * D + S::kHeads + h);
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
+      const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
+      for (int k = lane; k < n; k += 32) s_f[k * S::kHeads + h] *= inv;
+      if (lane == 0 && h < heads) p.lse[row_of(seg, h)] = mx + log2f(z);
+    }
+    __syncthreads();
+    for (int e = tid; e < items * share; e += S::kThreads) {
+      const int x = e % items, h = x / V4, i = x % V4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int k = e / items; k < n; k += share) {
+        const float f = s_f[k * S::kHeads + h];
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(part(k) + h * D) + i);
+        a.x += f * y.x;
+        a.y += f * y.y;
+        a.z += f * y.z;
+        a.w += f * y.w;
+      }
+      if (share == 1)
+        store_out(seg, h, i, a);
+      else
+        s_sum[e] = a;
+    }
+    if (share > 1) {
+      __syncthreads();
+      if (tid < items) {
+        float4 a = s_sum[tid];
+        for (int k = 1; k < share; ++k) {
+          const float4 y = s_sum[k * items + tid];
+          a.x += y.x;
+          a.y += y.y;
+          a.z += y.z;
+          a.w += y.w;
+        }
+        store_out(seg, tid / V4, tid % V4, a);
+      }
+    }
+    __syncthreads();                   // the next one writes the shared memory again
+  }
+}
+
+// CTAs that work on one head group: one CTA per SM in all.
+int ctas_per_group(int nsm, int groups) {
+  const int n = (nsm < kMaxCtas ? nsm : kMaxCtas) / groups;
+  return n > 0 ? n : 1;
 }
 
 template <int D, bool BF16, int NT>
@@ -473,7 +574,7 @@ cudaError_t launch(const DecodeParams& p, int nsm, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int per = nsm / p.groups > 0 ? nsm / p.groups : 1;
+  const int per = ctas_per_group(nsm, p.groups);
   return launch_pdl(kern, dim3(per * p.groups), dim3(S::kThreads), smem, stream, p);
 }
 
@@ -488,7 +589,7 @@ DecodeWorkspace decode_workspace(int batch, int h_kv, int g, int head_dim, int n
   DecodeWorkspace w{};
   const int heads = g <= 8 ? 8 : 16;
   w.groups = (g + heads - 1) / heads;
-  const int64_t ctas = (int64_t)(nsm / w.groups > 0 ? nsm / w.groups : 1) * w.groups;
+  const int64_t ctas = (int64_t)ctas_per_group(nsm, w.groups) * w.groups;
   w.off_parts = 256;
   w.off_counters = w.off_parts + round_up(ctas * 2 * (heads * (int64_t)head_dim + 2 * heads) * 4, 256);
   w.total = w.off_counters + round_up((int64_t)batch * h_kv * w.groups * 4, 256);
