@@ -268,7 +268,8 @@ ta_status tree_attn_paged(const void* q, const int32_t* q_indptr, const void* pa
  * nnz_pages (nnz_pages is the array's capacity).
  *   batch_size   B, 1..16384
  *   h_q, h_kv, head_dim, dtype, num_pages   as in ta_paged_dims
- *   nnz_pages    entries of page_values (16 * nnz_pages <= INT32_MAX) */
+ *   nnz_pages    entries of page_values (16 * nnz_pages <= INT32_MAX, nnz_pages *
+ *                h_kv < 2^30) */
 typedef struct {
   int32_t batch_size;
   int32_t h_q;

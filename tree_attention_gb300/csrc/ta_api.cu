@@ -854,6 +854,8 @@ ta_status cache_dims_supported(const ta_cache_dims* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return TA_ERR_UNSUPPORTED;
   if (d->h_q / d->h_kv > ta::kMaxGroup || d->batch_size > kMaxCacheBatch)
     return TA_ERR_UNSUPPORTED;
+  // the work of tree_attn_decode_paged is counted in pages of one kv head
+  if ((int64_t)d->nnz_pages * d->h_kv > INT32_MAX / 2) return TA_ERR_UNSUPPORTED;
   // a token's rows and a page's column blocks stay far inside int32
   if ((int64_t)(d->h_q + 2 * (int64_t)d->h_kv) * d->head_dim > (1 << 24)) return TA_ERR_UNSUPPORTED;
   return TA_OK;

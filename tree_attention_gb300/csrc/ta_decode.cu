@@ -81,8 +81,6 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-constexpr int kMaxCtas = 256;   // most CTAs of the grid
-
 // NT tiles of 8 heads per warp.  The warps per CTA follow from the registers a
 // lane needs (a page of K and of V, Q, O: 32 + 32 + 16 NT + 32 NT for d = 128).
 template <int D, int NT>
@@ -93,7 +91,7 @@ struct Shape {
   static constexpr int kState = kHeads * D + 2 * kHeads;   // floats: O, then m, then l
   static constexpr int kPieces = 2 * kWarps;               // parts a CTA can hold
   static_assert(kPieces <= 32, "one lane per part");
-  static_assert(kPieces * kState >= kMaxCtas * kHeads + 4 * kThreads, "the last merge's sums fit");
+  static_assert(kPieces * kState >= 6 * kThreads, "the last merge's sums fit");
 };
 
 // The largest b with s_indptr[b] <= x, over batch sequences; by one warp.
@@ -122,11 +120,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   extern __shared__ __align__(16) float s_state[];         // [kPieces][kState]
   int32_t* s_indptr = reinterpret_cast<int32_t*>(s_state + S::kPieces * S::kState);
   uint8_t* s_len = reinterpret_cast<uint8_t*>(s_indptr + p.tab.batch + 1);
-  __shared__ int s_seg[S::kPieces];                        // the sequence and kv head of each part
-  __shared__ int4 s_part[S::kPieces];                      // part, its s_seg, see below
-  __shared__ float s_factor[S::kPieces][S::kHeads];
-  __shared__ int s_count, s_merge[2];
-  __shared__ int2 s_range[2];
+  __shared__ int2 s_seg[S::kPieces];                       // each part's sequence (or -1) and kv head
+  __shared__ int s_part[S::kPieces];                       // the parts there are, in range order
+  __shared__ int4 s_group[S::kPieces];                     // runs of s_part of one sequence
+  __shared__ int2 s_group_at[S::kPieces];
+  __shared__ int s_groups, s_merge[2];
+  __shared__ int4 s_shared[2];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -145,7 +144,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       s_len[i] = (uint8_t)len;
     }
   }
-  if (tid < S::kPieces) s_seg[tid] = -1;
+  if (tid < S::kPieces) s_seg[tid].x = -1;
+  if (tid < 2) s_shared[tid].w = 0;
   if (__syncthreads_or(bad)) {
     if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
     return;
@@ -158,27 +158,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     for (int i = tid; i < p.h_q; i += S::kThreads) p.lse[(size_t)b * p.h_q + i] = -INFINITY;
   }
 
-  // this CTA's and this warp's range of units
+  // this CTA's and this warp's range of units: U = warps * per + extra, one
+  // more for each of the first ``extra`` warps
   const int P = s_indptr[batch];
-  const int64_t U = (int64_t)P * p.h_kv;
+  const int U = P * p.h_kv;
   const int group = blockIdx.x % p.groups;                 // of the heads of one kv head
   const int cta = blockIdx.x / p.groups;
-  const int64_t ctas = min((int64_t)(gridDim.x / p.groups), (U + W - 1) / W);
+  const int ctas = min((int)gridDim.x / p.groups, (U + W - 1) / W);
   if (cta >= ctas) return;
+  const int per = U / (ctas * W), extra = U % (ctas * W);
+  auto range_start = [&](int w) { return w * per + min(w, extra); };
   const int head0 = group * S::kHeads;                     // of the kv head's g
-  const int64_t u_end = ((int64_t)cta * W + warp + 1) * U / (ctas * W);
-  int64_t u = ((int64_t)cta * W + warp) * U / (ctas * W);
+  const int u_end = range_start(cta * W + warp + 1);
+  int u = range_start(cta * W + warp);
 
   if (u < u_end) {
-    const int64_t u_first = u;
-    int kvh = (int)(u / P), pg = (int)(u % P);
+    const int u_first = u;
+    int kvh = u / P, pg = u % P;
     int b = find_in(s_indptr, batch, pg, lane);
     int seg_end = s_indptr[b + 1];
     // physical pages of the next 32 units and of the 32 after them
-    auto pages_at = [&](int64_t x) {
-      return x + lane < u_end ? p.tab.page_values[(int)((x + lane) % P)] : 0;
+    auto pages_at = [&](int x) {
+      return x + lane < u_end ? p.tab.page_values[(x + lane) % P] : 0;
     };
-    int64_t ahead = u;
+    int ahead = u;
     int pv = pages_at(u), pv_next = pages_at(u + 32);
 
     uint4 qf[NT][KS], kf[2][KS], vf[4][VH];
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       }
     };
     auto load_k = [&]() {               // of unit u; sets k_page and rows
-      const int page = __shfl_sync(0xffffffffu, pv, (int)(u - ahead));
+      const int page = __shfl_sync(0xffffffffu, pv, u - ahead);
       const bool in = page >= 0 && page < p.tab.num_pages;
       rows = in ? (pg + 1 == seg_end ? s_len[b] : kPageSize) : 0;
       k_page = p.pages + ((int64_t)page * 2 * p.h_kv + kvh) * (kPageSize * D);
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       if (!seg_done && more) continue;
 
       // the end of a sequence or of the range
-      const int64_t seg_lo = (int64_t)kvh_now * P + s_indptr[b_now];
+      const int seg_lo = kvh_now * P + s_indptr[b_now];
       const bool whole = seg_done && seg_lo >= u_first;
       const int piece = 2 * warp + (seg_lo >= u_first ? 1 : 0);
 #pragma unroll
@@ -372,198 +375,174 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             }
           }
         }
-      if (!whole && lane == 0) s_seg[piece] = kvh_now * batch + b_now;
+      if (!whole && lane == 0) s_seg[piece] = make_int2(b_now, kvh_now);
       if (!more) break;
       reset();
     }
   }
   __syncthreads();
 
-  // The parts left in shared memory, in range order: s_part lists them, with the
-  // first and one past the last of the parts of the same sequence.
+  // The parts left in shared memory, listed in range order, and the runs of
+  // parts of one sequence: {first part, one past the last, slot, -}, slot -1 for
+  // a sequence that lies in this CTA, else 0 where its start does not, 1 where
+  // it does.
+  const int c_lo = range_start(cta * W), c_hi = range_start(cta * W + W);
   if (warp == 0) {
-    const int seg = lane < S::kPieces ? s_seg[lane] : -1;
-    const unsigned have = __ballot_sync(0xffffffffu, seg >= 0);
-    const int at = __popc(have & ((1u << lane) - 1));
-    // the part before this one in the list, if it is of the same sequence
+    const int2 seg = lane < S::kPieces ? s_seg[lane] : make_int2(-1, 0);
+    const unsigned have = __ballot_sync(0xffffffffu, seg.x >= 0);
     const unsigned below = have & ((1u << lane) - 1);
-    const int prev = __shfl_sync(0xffffffffu, seg, below ? 31 - __clz(below) : lane);
-    const unsigned starts = __ballot_sync(0xffffffffu, seg >= 0 && (!below || prev != seg));
-    if (seg >= 0) {
-      const unsigned upto = starts & (0xffffffffu >> (31 - lane));
+    const int before = below ? 31 - __clz(below) : lane;   // the part before this one
+    const int2 prev = make_int2(__shfl_sync(0xffffffffu, seg.x, before),
+                                __shfl_sync(0xffffffffu, seg.y, before));
+    const bool head = seg.x >= 0 && (!below || prev.x != seg.x || prev.y != seg.y);
+    const unsigned starts = __ballot_sync(0xffffffffu, head);
+    if (seg.x >= 0) s_part[__popc(below)] = lane;
+    if (head) {
       const unsigned after = starts & ~(0xffffffffu >> (31 - lane));
-      const int g0 = 31 - __clz(upto), g1 = after ? __ffs(after) - 1 : 32;
-      s_part[at] = make_int4(lane, seg, __popc(have & ((1u << g0) - 1)),
-                             g1 == 32 ? __popc(have) : __popc(have & ((1u << g1) - 1)));
+      const int next = after ? __ffs(after) - 1 : 32;
+      const int lo = seg.y * P + s_indptr[seg.x], hi = seg.y * P + s_indptr[seg.x + 1];
+      const int slot = lo >= c_lo && hi <= c_hi ? -1 : lo >= c_lo ? 1 : 0;
+      const int at = __popc(starts & ((1u << lane) - 1));
+      s_group[at] = make_int4(__popc(below), next == 32 ? __popc(have) : __popc(have & ((1u << next) - 1)),
+                              slot, 0);
+      s_group_at[at] = seg;
+      if (slot >= 0) {
+        // the CTAs that hold a part of it
+        auto cta_of = [&](int x) {
+          const int wide = extra * (per + 1);
+          return (x < wide ? x / (per + 1) : extra + (x - wide) / per) / W;
+        };
+        const int first = cta_of(lo);
+        s_shared[slot] = make_int4(seg.x, seg.y, first, cta_of(hi - 1) - first + 1);
+      }
     }
-    if (lane == 0) s_count = __popc(have);
-  }
-  __syncthreads();
-  const int count = s_count;
-  if (count == 0) return;
-  const int heads = min(S::kHeads, p.g - head0);
-  const int64_t c_lo = (int64_t)cta * U / ctas, c_hi = ((int64_t)cta + 1) * U / ctas;
-  auto units_of = [&](int seg, int64_t& lo, int64_t& hi) {
-    const int64_t base = (int64_t)(seg / batch) * P;
-    lo = base + s_indptr[seg % batch];
-    hi = base + s_indptr[seg % batch + 1];
-  };
-  auto row_of = [&](int seg, int h) {
-    return (size_t)(seg % batch) * p.h_q + (size_t)(seg / batch) * p.g + head0 + h;
-  };
-  // each part's factor; a sequence that lies in this CTA is also normalised
-  for (int e = tid; e < count * S::kHeads; e += S::kThreads) {
-    const int h = e % S::kHeads;
-    const int4 me = s_part[e / S::kHeads];
-    float mx = -FLT_MAX, z = 0.f;
-    for (int k = me.z; k < me.w; ++k)
-      mx = fmaxf(mx, s_state[s_part[k].x * S::kState + S::kHeads * D + h]);
-    for (int k = me.z; k < me.w; ++k) {
-      const float* ml = s_state + s_part[k].x * S::kState + S::kHeads * D;
-      z += exp2_approx(ml[h] - mx) * ml[S::kHeads + h];
-    }
-    float f = exp2_approx(s_state[me.x * S::kState + S::kHeads * D + h] - mx);
-    int64_t lo, hi;
-    units_of(me.y, lo, hi);
-    const bool first = e / S::kHeads == me.z;
-    if (lo >= c_lo && hi <= c_hi) {
-      f *= z > 0.f || z != z ? 1.f / z : 0.f;
-      if (first && h < heads) p.lse[row_of(me.y, h)] = mx + log2f(z);
-    } else if (first) {
-      float* st = p.parts + (size_t)(blockIdx.x * 2 + (lo >= c_lo ? 1 : 0)) * S::kState;
-      st[S::kHeads * D + h] = mx;
-      st[S::kHeads * D + S::kHeads + h] = z;
-    }
-    s_factor[e / S::kHeads][h] = f;
+    if (lane == 0) s_groups = __popc(starts);
   }
   __syncthreads();
   constexpr int V4 = D / 4;
-  auto store_out = [&](int seg, int h, int i, float4 a) {
-    reinterpret_cast<uint2*>(p.out + row_of(seg, h) * D)[i] =
-        make_uint2(pack2<BF16>(a.x, a.y), pack2<BF16>(a.z, a.w));
-  };
-  int shared_seg[2] = {-1, -1};        // by slot: sequences that go on in other CTAs
-  for (int g0 = 0; g0 < count;) {
-    const int4 grp = s_part[g0];
-    int64_t lo, hi;
-    units_of(grp.y, lo, hi);
-    const bool whole = lo >= c_lo && hi <= c_hi;
-    const int slot = lo >= c_lo ? 1 : 0;
-    if (!whole) shared_seg[slot] = grp.y;
-    for (int e = tid; e < heads * V4; e += S::kThreads) {
-      const int h = e / V4, i = e % V4;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int k = g0; k < grp.w; ++k) {
-        const float f = s_factor[k][h];
-        const float4 y = reinterpret_cast<const float4*>(s_state + s_part[k].x * S::kState + h * D)[i];
-        a.x += f * y.x;
-        a.y += f * y.y;
-        a.z += f * y.z;
-        a.w += f * y.w;
-      }
-      if (whole)
-        store_out(grp.y, h, i, a);
-      else
-        reinterpret_cast<float4*>(p.parts + (size_t)(blockIdx.x * 2 + slot) * S::kState + h * D)[i] = a;
+  const int heads = min(S::kHeads, p.g - head0), items = heads * V4;
+  // One thread's 4 elements of a state: O relative to m, and l.
+  struct Acc {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float pm, float pl, float4 y) {
+      const float top = fmaxf(m, pm), f = exp2_approx(m - top), w = exp2_approx(pm - top);
+      m = top;
+      l = l * f + pl * w;
+      o.x = o.x * f + y.x * w;
+      o.y = o.y * f + y.y * w;
+      o.z = o.z * f + y.z * w;
+      o.w = o.w * f + y.w * w;
     }
-    g0 = grp.w;
+  };
+  auto finish = [&](int2 at, int h, int i, const Acc& a) {
+    const float inv = a.l > 0.f || a.l != a.l ? 1.f / a.l : 0.f;
+    const size_t row = (size_t)at.x * p.h_q + (size_t)at.y * p.g + head0 + h;
+    reinterpret_cast<uint2*>(p.out + row * D)[i] = make_uint2(
+        pack2<BF16>(a.o.x * inv, a.o.y * inv), pack2<BF16>(a.o.z * inv, a.o.w * inv));
+    if (i == 0) p.lse[row] = a.m + log2f(a.l);
+  };
+  const int n_groups = s_groups;
+  for (int e = tid; e < n_groups * items; e += S::kThreads) {
+    const int h = e % items / V4, i = e % V4;
+    const int4 grp = s_group[e / items];
+    Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int k = grp.x; k < grp.y; ++k) {
+      const float* st = s_state + s_part[k] * S::kState;
+      a.add(st[S::kHeads * D + h], st[S::kHeads * D + S::kHeads + h],
+            reinterpret_cast<const float4*>(st + h * D)[i]);
+    }
+    if (grp.z < 0) {
+      finish(s_group_at[e / items], h, i, a);
+    } else {
+      float* st = p.parts + (size_t)(blockIdx.x * 2 + grp.z) * S::kState;
+      __stcg(reinterpret_cast<float4*>(st + h * D) + i, a.o);
+      if (i == 0) {
+        __stcg(st + S::kHeads * D + h, a.m);
+        __stcg(st + S::kHeads * D + S::kHeads + h, a.l);
+      }
+    }
   }
-  if (shared_seg[0] < 0 && shared_seg[1] < 0) return;
+  if (s_shared[0].w == 0 && s_shared[1].w == 0) return;
 
   // sequences that several CTAs share: the last of these to come here merges
-  __threadfence();
   __syncthreads();
   if (tid < 2) {
+    const int4 sh = s_shared[tid];
     int merge = 0;
-    const int seg = shared_seg[tid];
-    if (seg >= 0) {
-      int64_t lo, hi;
-      units_of(seg, lo, hi);
-      const int first = (int)(((lo + 1) * ctas - 1) / U), last = (int)((hi * ctas - 1) / U);
-      int* n = p.counters + (size_t)seg * p.groups + group;
-      if (atomicAdd(n, 1) == last - first) {
-        *n = 0;
-        merge = 1;
-      }
-      s_range[tid] = make_int2(first, last - first + 1);
+    if (sh.w > 0) {
+      int* n = p.counters + ((size_t)sh.y * batch + sh.x) * p.groups + group;
+      __threadfence();
+      merge = atomicAdd(n, 1) == sh.w - 1;
+      __threadfence();
+      if (merge) *n = 0;
     }
     s_merge[tid] = merge;
-    __threadfence();
   }
   __syncthreads();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     if (!s_merge[slot]) continue;
-    const int seg = shared_seg[slot], first = s_range[slot].x, n = s_range[slot].y;
-    // of the CTAs the first holds the sequence's start, its second part
+    const int4 sh = s_shared[slot];
+    const int n = sh.w;
+    // of its CTAs the first holds the sequence's start, its second part
     auto part = [&](int k) {
-      return p.parts + (size_t)(((size_t)(first + k) * p.groups + group) * 2 + (k == 0 ? 1 : 0)) * S::kState;
+      return p.parts + (size_t)(((size_t)(sh.z + k) * p.groups + group) * 2 + (k == 0 ? 1 : 0)) * S::kState;
     };
     // the threads share the n parts of an element where there are more threads
-    const int items = heads * V4, share = S::kThreads / items > 0 ? min(n, S::kThreads / items) : 1;
-    float* s_f = s_state;                              // [n][kHeads]
-    float4* s_sum = reinterpret_cast<float4*>(s_state + kMaxCtas * S::kHeads);   // [share][items]
-    for (int h = warp; h < S::kHeads; h += W) {
-      float mx = -FLT_MAX, z = 0.f;
-      for (int k = lane; k < n; k += 32) {
-        const float v = __ldcg(part(k) + S::kHeads * D + h);
-        s_f[k * S::kHeads + h] = v;
-        mx = fmaxf(mx, v);
-      }
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
-      for (int k = lane; k < n; k += 32) {
-        const float f = exp2_approx(s_f[k * S::kHeads + h] - mx);
-        s_f[k * S::kHeads + h] = f;
-        z += f * __ldcg(part(k) + S::kHeads * D + S::kHeads + h);
-      }
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
-      const float inv = z > 0.f || z != z ? 1.f / z : 0.f;
-      for (int k = lane; k < n; k += 32) s_f[k * S::kHeads + h] *= inv;
-      if (lane == 0 && h < heads) p.lse[row_of(seg, h)] = mx + log2f(z);
-    }
-    __syncthreads();
+    // than elements, and each has several parts' loads in flight
+    const int share = max(1, min(n, S::kThreads / items));
+    float* s_ml = s_state;                                            // [share][items][2]
+    float4* s_o = reinterpret_cast<float4*>(s_state + 2 * S::kThreads);   // [share][items]
     for (int e = tid; e < items * share; e += S::kThreads) {
       const int x = e % items, h = x / V4, i = x % V4;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int k = e / items; k < n; k += share) {
-        const float f = s_f[k * S::kHeads + h];
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(part(k) + h * D) + i);
-        a.x += f * y.x;
-        a.y += f * y.y;
-        a.z += f * y.z;
-        a.w += f * y.w;
+      Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      constexpr int kBatch = 8;
+      for (int k0 = e / items; k0 < n; k0 += share * kBatch) {
+        float pm[kBatch], pl[kBatch];
+        float4 y[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          pm[k] = -FLT_MAX;
+          pl[k] = 0.f;
+          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k * share < n) {
+            const float* st = part(k0 + k * share);
+            y[k] = __ldcg(reinterpret_cast<const float4*>(st + h * D) + i);
+            pm[k] = __ldcg(st + S::kHeads * D + h);
+            pl[k] = __ldcg(st + S::kHeads * D + S::kHeads + h);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) a.add(pm[k], pl[k], y[k]);
       }
-      if (share == 1)
-        store_out(seg, h, i, a);
-      else
-        s_sum[e] = a;
+      if (share == 1) {
+        finish(make_int2(sh.x, sh.y), h, i, a);
+      } else {
+        s_ml[2 * e] = a.m;
+        s_ml[2 * e + 1] = a.l;
+        s_o[e] = a.o;
+      }
     }
     if (share > 1) {
       __syncthreads();
       if (tid < items) {
-        float4 a = s_sum[tid];
+        Acc a{s_ml[2 * tid], s_ml[2 * tid + 1], s_o[tid]};
         for (int k = 1; k < share; ++k) {
-          const float4 y = s_sum[k * items + tid];
-          a.x += y.x;
-          a.y += y.y;
-          a.z += y.z;
-          a.w += y.w;
+          const int e = k * items + tid;
+          a.add(s_ml[2 * e], s_ml[2 * e + 1], s_o[e]);
         }
-        store_out(seg, tid / V4, tid % V4, a);
+        finish(make_int2(sh.x, sh.y), tid / V4, tid % V4, a);
       }
+      __syncthreads();                 // the other slot's merge writes there again
     }
-    __syncthreads();                   // the next one writes the shared memory again
   }
 }
 
 // CTAs that work on one head group: one CTA per SM in all.
 int ctas_per_group(int nsm, int groups) {
-  const int n = (nsm < kMaxCtas ? nsm : kMaxCtas) / groups;
-  return n > 0 ? n : 1;
+  return nsm / groups > 0 ? nsm / groups : 1;
 }
 
 template <int D, bool BF16, int NT>
