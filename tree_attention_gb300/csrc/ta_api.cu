@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -72,10 +73,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// SMs of the current device (0: none), asked once per device.
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -839,8 +844,6 @@ ta_status tree_attn_paged(const void* q, const int32_t* q_indptr, const void* pa
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kMaxCacheBatch = 16384;
-
 bool cache_dims_valid(const ta_cache_dims* d) {
   if (!d) return false;
   if (d->batch_size < 1 || d->h_q < 1 || d->h_kv < 1 || d->h_q % d->h_kv != 0) return false;
@@ -852,7 +855,7 @@ bool cache_dims_valid(const ta_cache_dims* d) {
 
 ta_status cache_dims_supported(const ta_cache_dims* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return TA_ERR_UNSUPPORTED;
-  if (d->h_q / d->h_kv > ta::kMaxGroup || d->batch_size > kMaxCacheBatch)
+  if (d->h_q / d->h_kv > ta::kMaxGroup || d->batch_size > ta::kMaxCacheBatch)
     return TA_ERR_UNSUPPORTED;
   // the work of tree_attn_decode_paged is counted in pages of one kv head
   if ((int64_t)d->nnz_pages * d->h_kv > INT32_MAX / 2) return TA_ERR_UNSUPPORTED;
