@@ -1073,9 +1073,9 @@ ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int3
   cp.error = error_word(workspace);
   cp.n = n;
   cp.num_pages = dims->num_pages;
-  cp.page_vecs = (int64_t)2 * dims->h_kv * ta::kPageSize * (dims->head_dim / 8);
-  const int64_t want = ta::ceil_div(n * cp.page_vecs, 256);
-  const int grid = (int)std::min<int64_t>(want, 4LL * nsm);
+  cp.page_lines = dims->h_kv * dims->head_dim / 64;   // 2 planes x 16 slots x 2 bytes
+  // a CTA for every two lines while they fit the GPU at once (5 CTAs per SM)
+  const int grid = (int)std::min<int64_t>(ta::ceil_div((int64_t)n * cp.page_lines, 2), 5LL * nsm);
   return cuda_status(ta::launch_copy_pages(cp, grid, static_cast<cudaStream_t>(stream)));
 }
 

@@ -316,58 +316,104 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
 // copies of pages
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
+constexpr int kCopyDepth = 10;       // lines a CTA has in flight
 constexpr int kCopyPairs = 256;      // pairs a CTA checks at a time
 constexpr int kCopyFilter = 4096;    // bits
 
-// The n pages are one list of 16-byte vectors, cut evenly over the CTAs.  A CTA
-// copies the vectors of a few consecutive pairs; before that it looks for its
+// A position in the list of lines: pair k of this round's, line ``line`` of its page.
+struct CopyAt {
+  int k, line;
+  __device__ __forceinline__ void next(int page_lines) {
+    if (++line == page_lines) {
+      line = 0;
+      ++k;
+    }
+  }
+};
+
+// The n pages are one list of 4 KB lines (a page is h_kv * d / 64 of them: one
+// 16-byte vector per thread each), cut evenly over the CTAs.  Lines pass
+// through a ring in shared memory by cp.async, each thread reading back only
+// what it fetched itself, so nothing waits for anything but its own data: ten
+// lines in flight in each of five CTAs keep 200 KB of loads on the way to an
+// SM, which the registers could not hold.  Before its first store a CTA looks for its
 // pairs' destinations among all other pairs' sources and destinations, through
-// a bit filter in shared memory (a hit is then looked up exactly).
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyParams p) {
+// a bit filter in shared memory (a hit is then looked up exactly), while the
+// first lines arrive.
+__global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyParams p) {
+  __shared__ uint4 s_ring[kCopyDepth][kCopyThreads];
   __shared__ unsigned int s_filter[kCopyFilter / 32];
   __shared__ int s_src[kCopyPairs], s_dst[kCopyPairs];
   __shared__ int s_skip[kCopyPairs];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int64_t total = (int64_t)p.n * p.page_vecs;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t lo = per * blockIdx.x;
-  const int64_t hi = min(total, lo + per);
+  const int64_t total = (int64_t)p.n * p.page_lines;
+  const int64_t per = total / gridDim.x, extra = total % gridDim.x;
+  const int64_t lo = per * blockIdx.x + min((int64_t)blockIdx.x, extra);
+  const int64_t hi = lo + per + (blockIdx.x < extra);
   if (lo >= hi) return;
-  const int first = (int)(lo / p.page_vecs), last = (int)((hi - 1) / p.page_vecs);
+  const int64_t first = lo / p.page_lines, last = (hi - 1) / p.page_lines;
+  const int64_t page_vecs = (int64_t)p.page_lines * kCopyThreads;
   for (int64_t base = first; base <= last; base += kCopyPairs) {
     const int m = (int)min((int64_t)kCopyPairs, last - base + 1);
     __syncthreads();
     for (int i = tid; i < kCopyFilter / 32; i += kCopyThreads) s_filter[i] = 0;
-    __syncthreads();
+    int s = 0, d = 0;
     if (tid < m) {
-      const int s = __ldg(p.src + base + tid), d = __ldg(p.dst + base + tid);
-      s_src[tid] = s;
-      s_dst[tid] = d;
-      s_skip[tid] = s < 0 || s >= p.num_pages || d < 0 || d >= p.num_pages;
-      if (s != d) atomicOr(&s_filter[(d & (kCopyFilter - 1)) >> 5], 1u << (d & 31));
+      s = p.src[base + tid];
+      d = p.dst[base + tid];
     }
     __syncthreads();
+    if (tid < m) {
+      const bool out = s < 0 || s >= p.num_pages || d < 0 || d >= p.num_pages;
+      s_src[tid] = s;
+      s_dst[tid] = d;
+      s_skip[tid] = out || s == d;
+      if (s != d) atomicOr(&s_filter[(d & (kCopyFilter - 1)) >> 5], 1u << (d & 31));
+      if (out) report_bad_tables(p.error);
+    }
+    __syncthreads();
+    const int line0 = (int)(max(lo, base * p.page_lines) - base * p.page_lines);
+    const int lines = (int)(min(hi, (base + m) * p.page_lines) - base * p.page_lines) - line0;
+    CopyAt get{line0 / p.page_lines, line0 % p.page_lines}, put = get;
+    auto fetch = [&](int l) {
+      if (l < lines) {
+        if (!s_skip[get.k]) {
+          const uint4* from = p.pages + s_src[get.k] * page_vecs + get.line * kCopyThreads + tid;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           smem_u32(&s_ring[l % kCopyDepth][tid])),
+                       "l"(from)
+                       : "memory");
+        }
+        get.next(p.page_lines);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int l = 0; l < kCopyDepth; ++l) fetch(l);
+    __syncthreads();                   // s_skip is read above and written below
+#pragma unroll 4
     for (int i = tid; i < p.n; i += kCopyThreads) {
-      const int v[2] = {__ldg(p.src + i), __ldg(p.dst + i)};
+      const int w[2] = {p.src[i], p.dst[i]};
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (!(s_filter[(v[x] & (kCopyFilter - 1)) >> 5] >> (v[x] & 31) & 1)) continue;
+        if (!(s_filter[(w[x] & (kCopyFilter - 1)) >> 5] >> (w[x] & 31) & 1)) continue;
         for (int k = 0; k < m; ++k)
-          if (s_dst[k] == v[x] && base + k != i && s_src[k] != s_dst[k]) s_skip[k] = 1;
+          if (s_dst[k] == w[x] && base + k != i && s_src[k] != s_dst[k]) {
+            s_skip[k] = 1;
+            report_bad_tables(p.error);
+          }
       }
     }
     __syncthreads();
-    if (tid < m && s_skip[tid]) report_bad_tables(p.error);
-    const int64_t from = max(lo, base * p.page_vecs);
-    const int64_t to = min(hi, (base + m) * p.page_vecs);
-    for (int64_t i = from + tid; i < to; i += kCopyThreads) {
-      const int k = (int)(i / p.page_vecs - base);
-      const int64_t off = i % p.page_vecs;
-      if (!s_skip[k] && s_src[k] != s_dst[k])
-        p.pages[s_dst[k] * p.page_vecs + off] = p.pages[s_src[k] * p.page_vecs + off];
+    for (int l = 0; l < lines; ++l) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kCopyDepth - 1) : "memory");
+      if (!s_skip[put.k])
+        p.pages[s_dst[put.k] * page_vecs + put.line * kCopyThreads + tid] = s_ring[l % kCopyDepth][tid];
+      put.next(p.page_lines);
+      fetch(l + kCopyDepth);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 

@@ -179,7 +179,7 @@ struct CopyParams {
   const int32_t *src, *dst;
   unsigned int* error;
   int n, num_pages;
-  int64_t page_vecs;                      // 16-byte vectors per page
+  int page_lines;                         // 4 KB lines per page
 };
 
 // Plan kernel: sequence/tile enumeration, tile classification and LPT
