@@ -975,13 +975,21 @@ ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
   ap.h_q = dims->h_q;
   ap.h_kv = dims->h_kv;
   ap.eps = norm_eps;
+  // CTAs of 4 warps: one resident wave, or a warp per step (512 / head_dim heads
+  // of one token's q, k or v) where there are fewer
+  const int nsm = sm_count();
+  if (nsm <= 0) return cuda_failure();
+  const int rows = 512 / dims->head_dim;
+  const int64_t steps = ta::ceil_div(dims->h_q, rows) + 2 * ta::ceil_div(dims->h_kv, rows);
+  const int grid = (int)std::min<int64_t>((int64_t)ta::kAppendCtas * nsm,
+                                          ta::ceil_div(total_new * steps, 4));
   if (rope) {
     ap.rope_layout = rope->layout;
     ap.rotary_dim = rope->rotary_dim;
     ap.magnitude = rope->magnitude;
     std::memcpy(ap.turns, rope->turns, sizeof(ap.turns));
   }
-  return cuda_status(ta::launch_append(ap, dims->head_dim, dims->dtype == TA_BF16,
+  return cuda_status(ta::launch_append(ap, dims->head_dim, dims->dtype == TA_BF16, grid,
                                        static_cast<cudaStream_t>(stream)));
 }
 

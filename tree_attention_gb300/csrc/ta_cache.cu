@@ -23,6 +23,7 @@ __device__ __forceinline__ void report_bad_tables(unsigned int* error) {
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
+constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight
 
 // The largest b in [0, batch) with indptr[b] <= t, by one warp: 32 probes cut
 // the range by 33 each round, so 1,000 sequences take two round trips to
@@ -41,150 +42,248 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
   return lo;
 }
 
-// One CTA per token.  A row (one head's d elements) belongs to d / 16 lanes;
-// each holds two 16-byte chunks of it, chosen so that both elements of every
-// rotated pair are in one lane.  Rows 0 .. h_q-1 are the token's queries, then
-// its keys, then its values.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+// A step is 32 * 16 elements of one token's queries, keys or values; the steps
+// of all tokens are cut evenly over the warps of one resident wave.  A row (one head's d elements) belongs to d / 16 lanes; each holds
+// two 16-byte chunks of it, chosen so that both elements of every rotated pair
+// are in one lane.
+//
+// Bound by memory: 4 bytes of traffic per element against the memory's rate
+// leave a lane some 200 instructions for its 16 elements of a step, and the
+// latencies within a step have to be hidden by few warps, as what a token's
+// rows have in common is kept in registers: cos and sin, made once per token,
+// and their products with the weights, made once for its queries and once for
+// its keys.  Each lane fetches its own chunks kAppendDepth steps ahead into
+// shared memory (cp.async; nothing else reads them, so no barrier), past the
+// ends of tokens, and the arithmetic is in pairs of float32.
+template <int D, bool BF16, int LAYOUT>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;           // lanes per row
-  constexpr int kRows = 32 / kLanes;       // rows per warp and step
-  __shared__ float2 s_cs[64];              // cos, sin of each pair (times magnitude)
-  __shared__ long long s_slot;             // element offset of the token's K slot, head 0
+  constexpr int kRows = 32 / kLanes;       // rows per step
+  constexpr bool kHalves = LAYOUT == 1;
+  __shared__ uint4 s_ring[kAppendThreads / 32][kAppendDepth][2][32];
+  __shared__ __align__(16) float2 s_cos_sin[kAppendThreads / 32][D / 2];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < p.rotary_dim / 2 && p.rope_layout != 0) {
-    // the fraction of a turn, exact modulo 1, then one rounding to float32
-    const uint64_t ph = (uint64_t)(int64_t)p.positions[t] * p.turns[tid];
-    const float half_turns = (float)(int64_t)ph * 0x1p-63f;   // in [-1, 1]
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    s_cs[tid] = make_float2(c * p.magnitude, s * p.magnitude);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % kLanes, lane_row = lane / kLanes;
+  // this lane's chunks of 8 elements, such that the lanes of a row hold runs of
+  // chunks: interleaved pairs lie within a chunk, half layout pairs chunk i with
+  // chunk i + rotary_dim / 16; rot0, rot1: whether a chunk is rotated
+  const int rd = LAYOUT != 0 ? p.rotary_dim : 0;
+  int c0 = sub, c1 = sub + kLanes;
+  bool rot0 = c0 < rd / 8, rot1 = c1 < rd / 8;
+  if (kHalves) {
+    rot0 = rot1 = sub < rd / 16;
+    c0 = rot0 ? sub : sub + rd / 16;
+    c1 = c0 + (rot0 ? rd / 16 : kLanes - rd / 16);
   }
-  if (warp == kAppendThreads / 32 - 1) {
-    const int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
-    const int a0 = __ldg(p.append_indptr + b), a1 = __ldg(p.append_indptr + b + 1);
-    const int p0 = __ldg(p.tab.page_indptr + b), p1 = __ldg(p.tab.page_indptr + b + 1);
-    const int last = __ldg(p.tab.length_info + b);
-    long long slot = -1;
-    if (a0 >= 0 && t >= a0 && t < a1 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
-        p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize) {
-      const long long kv = (long long)(p1 - p0 - 1) * kPageSize + last;
-      const long long row = kv - (a1 - t);
-      if (kv >= a1 - a0) {
-        const int page = __ldg(p.tab.page_values + p0 + row / kPageSize);
-        if (page >= 0 && page < p.tab.num_pages)
-          slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
+  // steps of a token: its queries' (kind 0), keys' (1) and values' (2)
+  const int steps_q = (p.h_q + kRows - 1) / kRows, steps_kv = (p.h_kv + kRows - 1) / kRows;
+  const int all = steps_q + 2 * steps_kv;
+  // this warp's share of all tokens' steps: from step ``s`` of token ``t`` on
+  const int64_t total = (int64_t)p.total_new * all;
+  const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
+  const int64_t gw = (int64_t)blockIdx.x * (kAppendThreads / 32) + warp;
+  const int64_t lo = gw * total / warps;
+  int64_t left = (gw + 1) * total / warps - lo;
+  if (left <= 0) return;
+  int t = (int)(lo / all), begin = (int)(lo % all);
+  auto first_step = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? steps_q : steps_q + steps_kv; };
+
+  // The fetches: their token, step, and of the step's rows this lane's.
+  int64_t f_left = left;
+  int f_t = t, f_step = begin, f_next_kind = begin, f_row = 0, f_rows = 0, f_slot = 0;
+  const uint16_t* f_src = nullptr;
+  auto fetch = [&]() {
+    if (f_left > 0) {
+      --f_left;
+      if (f_step == f_next_kind) {         // the first step, or the first of another kind
+        const int kind = f_step < steps_q ? 0 : f_step < steps_q + steps_kv ? 1 : 2;
+        f_row = (f_step - first_step(kind)) * kRows + lane_row;
+        f_rows = kind == 0 ? p.h_q : p.h_kv;
+        f_src = (kind == 0   ? p.q + f_t * p.q_stride
+                 : kind == 1 ? p.k + f_t * p.k_stride
+                             : p.v + f_t * p.v_stride) + f_row * D;
+        f_next_kind = kind == 2 ? 0 : first_step(kind + 1);
+      }
+      if (f_row < f_rows) {
+        const uint32_t to = smem_u32(&s_ring[warp][f_slot][0][lane]);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(f_src + 8 * c0)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(f_src + 8 * c1)
+                     : "memory");
+      }
+      f_row += kRows;
+      f_src += kRows * D;
+      f_slot = f_slot + 1 == kAppendDepth ? 0 : f_slot + 1;
+      if (++f_step == all) {
+        f_step = 0;
+        ++f_t;
       }
     }
-    if (lane == 0) {
-      s_slot = slot;
-      if (slot < 0) report_bad_tables(p.error);
-    }
-  }
-  __syncthreads();
-  const long long slot = s_slot;
-  const int rd = p.rope_layout != 0 ? p.rotary_dim : 0;
-  const int sub = lane % kLanes;
-  const int rows = p.h_q + 2 * p.h_kv;
-  // this lane's chunks of 8 elements: half layout pairs chunk i with chunk
-  // i + rotary_dim / 16, interleaved pairs lie within a chunk; the part of
-  // the head that is not rotated is split in adjacent chunks
-  const bool rot = sub < rd / 16;
-  int c0 = 2 * sub, c1 = 2 * sub + 1;
-  if (p.rope_layout == 1 && rot) {
-    c0 = sub;
-    c1 = sub + rd / 16;
-  }
-  for (int r0 = warp * kRows; r0 < rows; r0 += kRows * (kAppendThreads / 32)) {
-    const int r = r0 + lane / kLanes;
-    const bool live = r < rows;
-    const uint16_t* src = p.q;
-    uint16_t* dst = nullptr;
-    const uint16_t* w = nullptr;
-    bool plain = false;                     // a value row: copied as it is
-    if (live) {
-      if (r < p.h_q) {
-        src = p.q + (int64_t)t * p.q_stride + (int64_t)r * D;
-        dst = p.q_out + ((int64_t)t * p.h_q + r) * D;
-        w = p.q_weight;
-      } else if (r < p.h_q + p.h_kv) {
-        const int h = r - p.h_q;
-        src = p.k + (int64_t)t * p.k_stride + (int64_t)h * D;
-        if (slot >= 0) dst = p.pages + slot + (int64_t)h * kPageSize * D;
-        w = p.k_weight;
-      } else {
-        const int h = r - p.h_q - p.h_kv;
-        src = p.v + (int64_t)t * p.v_stride + (int64_t)h * D;
-        if (slot >= 0) dst = p.pages + slot + (int64_t)(p.h_kv + h) * kPageSize * D;
-        plain = true;
-      }
-    }
-    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-    if (live) {
-      u0 = reinterpret_cast<const uint4*>(src)[c0];
-      u1 = reinterpret_cast<const uint4*>(src)[c1];
-    }
-    const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-    float x0[8], x1[8];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAppendDepth; ++i) fetch();
+
+  // the current sequence's tokens, first table entry and kv rows (kv < 0: bad tables)
+  int a0 = 0, a1 = 0, p0 = 0, kv = -1;
+  int ring = 0;
+  long long slot = -1;                     // element offset of the token's K slot, head 0
+  auto token = [&]() {
+    __syncwarp();
+    if (LAYOUT != 0) {
+      const int64_t pos = p.positions[t];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = unpack2<BF16>(w0[i]), b = unpack2<BF16>(w1[i]);
-      x0[2 * i] = a.x;
-      x0[2 * i + 1] = a.y;
-      x1[2 * i] = b.x;
-      x1[2 * i + 1] = b.y;
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (w != nullptr) {
-      const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = unpack2<BF16>(reinterpret_cast<const uint32_t*>(w)[c0 * 4 + i]);
-        const float2 b = unpack2<BF16>(reinterpret_cast<const uint32_t*>(w)[c1 * 4 + i]);
-        x0[2 * i] *= inv * a.x;
-        x0[2 * i + 1] *= inv * a.y;
-        x1[2 * i] *= inv * b.x;
-        x1[2 * i + 1] *= inv * b.y;
-      }
-    }
-    if (rot && !plain) {
-      if (p.rope_layout == 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 cs = s_cs[8 * sub + i];
-          const float a = x0[i], b = x1[i];
-          x0[i] = a * cs.x - b * cs.y;
-          x1[i] = b * cs.x + a * cs.y;
+      for (int i = 0; i < D / 64; ++i) {
+        const int j = lane + 32 * i;
+        if (j < rd / 2) {
+          // the fraction of a turn, exact modulo 1, then one rounding to float32
+          const uint64_t ph = (uint64_t)pos * p.turns[j];
+          const float half_turns = (float)(int64_t)ph * 0x1p-63f;   // in [-1, 1]
+          float sn, cs;
+          sincospif(half_turns, &sn, &cs);
+          s_cos_sin[warp][j] = make_float2(cs * p.magnitude, sn * p.magnitude);
         }
-      } else {
+      }
+    }
+    if (t < a0 || t >= a1) {
+      const int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
+      a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
+      p0 = p.tab.page_indptr[b];
+      const int p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
+      const bool good = a0 >= 0 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
+                        p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize;
+      kv = good ? (p1 - p0 - 1) * kPageSize + last : -1;
+      if (kv < a1 - a0) kv = -1;
+    }
+    slot = -1;
+    if (kv >= 0 && t >= a0 && t < a1) {
+      const int row = kv - (a1 - t);
+      const int page = p.tab.page_values[p0 + row / kPageSize];
+      if (page >= 0 && page < p.tab.num_pages)
+        slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
+    }
+    if (slot < 0 && lane == 0) report_bad_tables(p.error);
+    __syncwarp();
+  };
+
+  for (; left > 0; ++t, begin = 0) {
+    const int end = (int)min((int64_t)all, begin + left);
+    left -= end - begin;
+    token();
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+      const int k_lo = first_step(kind), k_hi = kind == 2 ? all : first_step(kind + 1);
+      const int s_lo = max(begin, k_lo), s_hi = min(end, k_hi);
+      if (s_lo >= s_hi) continue;
+      // where rows go: planes and heads of the cache follow one another
+      int row = (s_lo - k_lo) * kRows + lane_row;
+      const int rows = kind == 0 ? p.h_q : p.h_kv;
+      const int64_t stride = kind == 0 ? D : kPageSize * D;
+      uint16_t* dst = kind == 0 ? p.q_out + (int64_t)t * p.h_q * D
+                                : p.pages + slot + (kind == 2 ? (int64_t)p.h_kv * stride : 0);
+      dst += row * stride;
+      if (kind != 0 && slot < 0) row = rows;           // nothing is written
+      // x * own + partner * other, times 1 / rms
+      float2 own0[4], own1[4], other0[4], other1[4];
+      const uint16_t* w = kind == 0 ? p.q_weight : p.k_weight;
+      const bool norm = w != nullptr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own0[i] = own1[i] = make_float2(1.f, 1.f);
+      if (kind < 2) {
+        if (norm) {
+          const uint4 a = reinterpret_cast<const uint4*>(w)[c0];
+          const uint4 b = reinterpret_cast<const uint4*>(w)[c1];
+          own0[0] = unpack2<BF16>(a.x), own0[1] = unpack2<BF16>(a.y);
+          own0[2] = unpack2<BF16>(a.z), own0[3] = unpack2<BF16>(a.w);
+          own1[0] = unpack2<BF16>(b.x), own1[1] = unpack2<BF16>(b.y);
+          own1[2] = unpack2<BF16>(b.z), own1[3] = unpack2<BF16>(b.w);
+        }
+        // two pairs each: cos, sin, cos, sin
+        const float4* cs = reinterpret_cast<const float4*>(s_cos_sin[warp]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 ca = s_cs[8 * sub + i], cb = s_cs[8 * sub + 4 + i];
-          const float a0 = x0[2 * i], a1 = x0[2 * i + 1];
-          const float b0 = x1[2 * i], b1 = x1[2 * i + 1];
-          x0[2 * i] = a0 * ca.x - a1 * ca.y;
-          x0[2 * i + 1] = a1 * ca.x + a0 * ca.y;
-          x1[2 * i] = b0 * cb.x - b1 * cb.y;
-          x1[2 * i + 1] = b1 * cb.x + b0 * cb.y;
+          other0[i] = other1[i] = make_float2(0.f, 0.f);
+          const float2 w0 = own0[i], w1 = own1[i];
+          if (kHalves) {
+            if (!rot0) continue;
+            const float4 x = cs[4 * c0 + i];           // pairs 8 c0 + 2 i, 8 c0 + 2 i + 1
+            own0[i] = make_float2(w0.x * x.x, w0.y * x.z);
+            other0[i] = make_float2(-w1.x * x.y, -w1.y * x.w);
+            own1[i] = make_float2(w1.x * x.x, w1.y * x.z);
+            other1[i] = make_float2(w0.x * x.y, w0.y * x.w);
+          } else {
+            if (rot0) {
+              const float4 x = cs[2 * c0 + (i >> 1)];  // pair 4 c0 + i
+              const float2 a = i & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+              own0[i] = make_float2(w0.x * a.x, w0.y * a.x);
+              other0[i] = make_float2(-w0.y * a.y, w0.x * a.y);
+            }
+            if (rot1) {
+              const float4 x = cs[2 * c1 + (i >> 1)];
+              const float2 a = i & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+              own1[i] = make_float2(w1.x * a.x, w1.y * a.x);
+              other1[i] = make_float2(-w1.y * a.y, w1.x * a.y);
+            }
+          }
         }
       }
-    }
-    if (!plain) {
-      u0 = make_uint4(pack2<BF16>(x0[0], x0[1]), pack2<BF16>(x0[2], x0[3]),
-                      pack2<BF16>(x0[4], x0[5]), pack2<BF16>(x0[6], x0[7]));
-      u1 = make_uint4(pack2<BF16>(x1[0], x1[1]), pack2<BF16>(x1[2], x1[3]),
-                      pack2<BF16>(x1[4], x1[5]), pack2<BF16>(x1[6], x1[7]));
-    }
-    if (dst != nullptr) {
-      reinterpret_cast<uint4*>(dst)[c0] = u0;
-      reinterpret_cast<uint4*>(dst)[c1] = u1;
+      // what neither norm nor rotation touches keeps its bits
+      const bool plain0 = kind == 2 || !(norm || rot0), plain1 = kind == 2 || !(norm || rot1);
+#pragma unroll 1
+      for (int s = s_lo; s < s_hi; ++s) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAppendDepth - 1) : "memory");
+        uint4 u0 = s_ring[warp][ring][0][lane], u1 = s_ring[warp][ring][1][lane];
+        ring = ring + 1 == kAppendDepth ? 0 : ring + 1;
+        if (kind < 2) {
+          float2 x0[4] = {unpack2<BF16>(u0.x), unpack2<BF16>(u0.y), unpack2<BF16>(u0.z),
+                          unpack2<BF16>(u0.w)};
+          float2 x1[4] = {unpack2<BF16>(u1.x), unpack2<BF16>(u1.y), unpack2<BF16>(u1.z),
+                          unpack2<BF16>(u1.w)};
+          const float2 zero = make_float2(0.f, 0.f);
+          if (norm) {
+            float2 sa = zero, sb = zero;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sa = ffma2(x0[i], x0[i], sa);
+              sb = ffma2(x1[i], x1[i], sb);
+            }
+            float sum = (sa.x + sa.y) + (sb.x + sb.y);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x0[i] = ffma2(x0[i], make_float2(inv, inv), zero);
+              x1[i] = ffma2(x1[i], make_float2(inv, inv), zero);
+            }
+          }
+          float2 y0[4], y1[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y0[i] = ffma2(x0[i], own0[i], zero);
+            y1[i] = ffma2(x1[i], own1[i], zero);
+            if (rot0)
+              y0[i] = ffma2(kHalves ? x1[i] : make_float2(x0[i].y, x0[i].x), other0[i], y0[i]);
+            if (rot1)
+              y1[i] = ffma2(kHalves ? x0[i] : make_float2(x1[i].y, x1[i].x), other1[i], y1[i]);
+          }
+          if (!plain0)
+            u0 = make_uint4(pack2<BF16>(y0[0].x, y0[0].y), pack2<BF16>(y0[1].x, y0[1].y),
+                            pack2<BF16>(y0[2].x, y0[2].y), pack2<BF16>(y0[3].x, y0[3].y));
+          if (!plain1)
+            u1 = make_uint4(pack2<BF16>(y1[0].x, y1[0].y), pack2<BF16>(y1[1].x, y1[1].y),
+                            pack2<BF16>(y1[2].x, y1[2].y), pack2<BF16>(y1[3].x, y1[3].y));
+        }
+        if (row < rows) {
+          reinterpret_cast<uint4*>(dst)[c0] = u0;
+          reinterpret_cast<uint4*>(dst)[c1] = u1;
+        }
+        row += kRows;
+        dst += kRows * stride;
+        fetch();                           // into the slot read above
+      }
     }
   }
 }
@@ -316,7 +415,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
 // copies of pages
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kCopyDepth = 10;       // lines a CTA has in flight
+constexpr int kCopyDepth = 6;        // lines a CTA has in flight
 constexpr int kCopyPairs = 256;      // pairs a CTA checks at a time
 constexpr int kCopyFilter = 4096;    // bits
 
@@ -334,9 +433,9 @@ struct CopyAt {
 // The n pages are one list of 4 KB lines (a page is h_kv * d / 64 of them: one
 // 16-byte vector per thread each), cut evenly over the CTAs.  Lines pass
 // through a ring in shared memory by cp.async, each thread reading back only
-// what it fetched itself, so nothing waits for anything but its own data: ten
-// lines in flight in each of five CTAs keep 200 KB of loads on the way to an
-// SM, which the registers could not hold.  Before its first store a CTA looks for its
+// what it fetched itself, so nothing waits for anything but its own data: six
+// lines in flight in each of five CTAs keep 120 KB of loads on the way to an
+// SM (ten lines measured the same on large copies and slower on small ones).  Before its first store a CTA looks for its
 // pairs' destinations among all other pairs' sources and destinations, through
 // a bit filter in shared memory (a hit is then looked up exactly), while the
 // first lines arrive.
@@ -409,7 +508,8 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
     for (int l = 0; l < lines; ++l) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kCopyDepth - 1) : "memory");
       if (!s_skip[put.k])
-        p.pages[s_dst[put.k] * page_vecs + put.line * kCopyThreads + tid] = s_ring[l % kCopyDepth][tid];
+        __stcs(p.pages + s_dst[put.k] * page_vecs + put.line * kCopyThreads + tid,
+               s_ring[l % kCopyDepth][tid]);
       put.next(p.page_lines);
       fetch(l + kCopyDepth);
     }
@@ -417,15 +517,23 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
   }
 }
 
+template <int D, bool BF16>
+cudaError_t launch_append_as(const AppendParams& p, int grid, cudaStream_t stream) {
+  const auto kern = p.rope_layout == 1   ? append_kernel<D, BF16, 1>
+                    : p.rope_layout == 2 ? append_kernel<D, BF16, 2>
+                                         : append_kernel<D, BF16, 0>;
+  return launch_pdl(kern, dim3(grid), dim3(kAppendThreads), 0, stream, p);
+}
+
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, cudaStream_t stream) {
-  const dim3 g(p.total_new), b(kAppendThreads);
+cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, int grid,
+                          cudaStream_t stream) {
   if (head_dim == 128)
-    return bf16 ? launch_pdl(append_kernel<128, true>, g, b, 0, stream, p)
-                : launch_pdl(append_kernel<128, false>, g, b, 0, stream, p);
-  return bf16 ? launch_pdl(append_kernel<64, true>, g, b, 0, stream, p)
-              : launch_pdl(append_kernel<64, false>, g, b, 0, stream, p);
+    return bf16 ? launch_append_as<128, true>(p, grid, stream)
+                : launch_append_as<128, false>(p, grid, stream);
+  return bf16 ? launch_append_as<64, true>(p, grid, stream)
+              : launch_append_as<64, false>(p, grid, stream);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {

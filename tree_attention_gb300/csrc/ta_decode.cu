@@ -72,12 +72,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -297,7 +291,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 #pragma unroll
             for (int i = 4; i <= 16; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
             const float moved = fmaxf(m[n][j], top - kRef);
-            const float f = exp2_approx(m[n][j] - moved);
+            const float f = ex2_approx(m[n][j] - moved);
             m[n][j] = moved;
             l[n][j] *= f;
 #pragma unroll
@@ -311,7 +305,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[n][i] = exp2_approx(x[n][i] - m[n][i & 1]);
+        for (int i = 0; i < 4; ++i) x[n][i] = ex2_approx(x[n][i] - m[n][i & 1]);
         l[n][0] += x[n][0] + x[n][2];
         l[n][1] += x[n][1] + x[n][3];
         // one rounding of each weight to 16 bits, for the tensor cores; the sum
@@ -427,7 +421,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     float m, l;
     float4 o;
     __device__ __forceinline__ void add(float pm, float pl, float4 y) {
-      const float top = fmaxf(m, pm), f = exp2_approx(m - top), w = exp2_approx(pm - top);
+      const float top = fmaxf(m, pm), f = ex2_approx(m - top), w = ex2_approx(pm - top);
       m = top;
       l = l * f + pl * w;
       o.x = o.x * f + y.x * w;

@@ -211,7 +211,8 @@ cudaError_t launch_merge_states(const void* parts, const float* lses, int n_part
                                 int grid, cudaStream_t stream);
 
 // Appends tokens to the cache (norm and rotation of q and k on the way).
-cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, int grid,
+                          cudaStream_t stream);
 
 // One token per sequence against the paged cache.
 cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int nsm,

@@ -19,6 +19,7 @@ constexpr int kBlockN = 128;
 constexpr int kKvBoxRows = 128;  // kv rows per TMA box (one box per kv tile)
 constexpr int kMaxGroup = 128;   // largest supported h_q / h_kv
 constexpr int kPageSize = 16;    // kv slots per page of a paged KV cache
+constexpr int kAppendCtas = 5;   // CTAs of the append kernel per SM (its registers allow them)
 constexpr int kMaxCacheBatch = 16384;   // sequences of a paged-cache call
 constexpr int kTilesPerUnit = 2; // Q tiles per work unit
 
