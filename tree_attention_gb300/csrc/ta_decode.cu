@@ -102,6 +102,33 @@ __device__ __forceinline__ int find_in(const int32_t* s_indptr, int batch, int x
   return lo;
 }
 
+// One thread's 4 elements of a state: O relative to m, and l.
+struct Acc {
+  float m, l;
+  float4 o;
+  // n states more, the largest m first, so that their factors are independent
+  template <int n>
+  __device__ __forceinline__ void add(const float (&pm)[n], const float (&pl)[n],
+                                      const float4 (&y)[n]) {
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < n; ++k) top = fmaxf(top, pm[k]);
+    const float f = ex2_approx(m - top);
+    m = top;
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float w = ex2_approx(pm[k] - top);
+      l += pl[k] * w;
+      o.x += y[k].x * w;
+      o.y += y[k].y * w;
+      o.z += y[k].z * w;
+      o.w += y[k].w * w;
+    }
+  }
+};
+
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     decode_kernel(const DecodeParams p) {
@@ -127,6 +154,32 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   const int r = lane >> 2, c = lane & 3;
   const int batch = p.tab.batch;
 
+  // This CTA's and this warp's range of units, for a table of ``pages`` entries:
+  // U = warps * per + extra units, one more for each of the first ``extra`` warps.
+  const int group = blockIdx.x % p.groups;                 // of the heads of one kv head
+  const int cta = blockIdx.x / p.groups;
+  int P = 0, ctas = 0, per = 0, extra = 0, u = 0, u_end = 0, pv = 0;
+  auto range_start = [&](int w) { return w * per + min(w, extra); };
+  // physical pages of the 32 units from x on, one per lane
+  auto pages_at = [&](int x) {
+    return x + lane < u_end ? p.tab.page_values[(x + lane) % P] : 0;
+  };
+  auto plan = [&](int pages) {
+    P = pages;
+    const int U = pages * p.h_kv;
+    ctas = min((int)gridDim.x / p.groups, (U + W - 1) / W);
+    u = u_end = 0;
+    if (cta >= ctas) return;
+    per = U / (ctas * W);
+    extra = U % (ctas * W);
+    u = range_start(cta * W + warp);
+    u_end = range_start(cta * W + warp + 1);
+    pv = pages_at(u);
+  };
+  // the table is usually as long as its array: its first entries are on their
+  // way while its offsets arrive
+  plan(p.tab.nnz_pages);
+
   // the page table's offsets and last lengths, checked as a whole
   bool bad = false;
   for (int i = tid; i <= batch; i += S::kThreads) {
@@ -145,6 +198,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
     return;
   }
+  if (s_indptr[batch] != P) plan(s_indptr[batch]);
   // sequences without rows
   for (int b = blockIdx.x; b < batch; b += gridDim.x) {
     if (s_indptr[b] != s_indptr[b + 1]) continue;
@@ -152,81 +206,112 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     for (int i = tid; i < p.h_q * (D / 8); i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < p.h_q; i += S::kThreads) p.lse[(size_t)b * p.h_q + i] = -INFINITY;
   }
-
-  // this CTA's and this warp's range of units: U = warps * per + extra, one
-  // more for each of the first ``extra`` warps
-  const int P = s_indptr[batch];
-  const int U = P * p.h_kv;
-  const int group = blockIdx.x % p.groups;                 // of the heads of one kv head
-  const int cta = blockIdx.x / p.groups;
-  const int ctas = min((int)gridDim.x / p.groups, (U + W - 1) / W);
   if (cta >= ctas) return;
-  const int per = U / (ctas * W), extra = U % (ctas * W);
-  auto range_start = [&](int w) { return w * per + min(w, extra); };
   const int head0 = group * S::kHeads;                     // of the kv head's g
-  const int u_end = range_start(cta * W + warp + 1);
-  int u = range_start(cta * W + warp);
-
-  if (u < u_end) {
-    const int u_first = u;
-    int kvh = u / P, pg = u % P;
-    int b = find_in(s_indptr, batch, pg, lane);
-    int seg_end = s_indptr[b + 1];
-    // physical pages of the next 32 units and of the 32 after them
-    auto pages_at = [&](int x) {
-      return x + lane < u_end ? p.tab.page_values[(x + lane) % P] : 0;
-    };
-    int ahead = u;
-    int pv = pages_at(u), pv_next = pages_at(u + 32);
-
-    uint4 qf[NT][KS], kf[2][KS], vf[4][VH];
-    float o[NT][4 * VH][4], m[NT][2], l[NT][2];
-    const uint16_t* k_page = nullptr;   // the page whose values are still to be requested
-    int rows = 0;                       // its rows that count; 0 for zeros
-    auto load_q = [&]() {
+  const int u_first = u;
+  const bool work = u < u_end;
+  int kvh = u / P, pg = u % P, b = 0, seg_end = 0, ahead = u, pv_next = 0;
+  uint4 qf[NT][KS], kf[2][KS], vf[4][VH];
+  const uint16_t* k_page = nullptr;   // the page whose values are still to be requested
+  int rows = 0;                       // its rows that count; 0 for zeros
+  auto load_q = [&]() {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int h = head0 + n * 8 + r;
-        const uint16_t* q = p.q + ((size_t)b * p.h_q + (size_t)kvh * p.g + h) * D + 8 * c;
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-          qf[n][s] = h < p.g ? load_stream(q + 32 * s) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto load_k = [&]() {               // of unit u; sets k_page and rows
-      const int page = __shfl_sync(0xffffffffu, pv, u - ahead);
-      const bool in = page >= 0 && page < p.tab.num_pages;
-      rows = in ? (pg + 1 == seg_end ? s_len[b] : kPageSize) : 0;
-      k_page = p.pages + ((int64_t)page * 2 * p.h_kv + kvh) * (kPageSize * D);
+    for (int n = 0; n < NT; ++n) {
+      const int h = head0 + n * 8 + r;
+      const uint16_t* q = p.q + ((size_t)b * p.h_q + (size_t)kvh * p.g + h) * D + 8 * c;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
+        qf[n][s] = h < p.g ? load_stream(q + 32 * s) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load_k = [&]() {               // of unit u; sets k_page and rows
+    const int page = __shfl_sync(0xffffffffu, pv, u - ahead);
+    const bool in = page >= 0 && page < p.tab.num_pages;
+    rows = in ? (pg + 1 == seg_end ? s_len[b] : kPageSize) : 0;
+    k_page = p.pages + ((int64_t)page * 2 * p.h_kv + kvh) * (kPageSize * D);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          kf[i][s] = in ? load_stream(k_page + (r + 8 * i) * D + 32 * s + 8 * c)
-                        : make_uint4(0, 0, 0, 0);
-    };
-    auto load_v = [&]() {
-      const uint16_t* v = k_page + (int64_t)p.h_kv * kPageSize * D + 8 * r;
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
+      for (int i = 0; i < 2; ++i)
+        kf[i][s] = in ? load_stream(k_page + (r + 8 * i) * D + 32 * s + 8 * c)
+                      : make_uint4(0, 0, 0, 0);
+  };
+  auto load_v = [&]() {
+    const uint16_t* v = k_page + (int64_t)p.h_kv * kPageSize * D + 8 * r;
 #pragma unroll
-        for (int h = 0; h < VH; ++h)    // a slot past the last row may hold anything
-          vf[i][h] = tok < rows ? load_stream(v + tok * D + 64 * h) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto reset = [&]() {
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -FLT_MAX;
-        l[n][0] = l[n][1] = 0.f;
+      for (int h = 0; h < VH; ++h)    // a slot past the last row may hold anything
+        vf[i][h] = tok < rows ? load_stream(v + tok * D + 64 * h) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  float o[NT][4 * VH][4], m[NT][2], l[NT][2];
+  auto reset = [&]() {
 #pragma unroll
-        for (int t = 0; t < 4 * VH; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
-      }
-    };
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -FLT_MAX;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4 * VH; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+    }
+  };
+  if (work) {
+    pv_next = pages_at(u + 32);
+    b = find_in(s_indptr, batch, pg, lane);
+    seg_end = s_indptr[b + 1];
     load_q();
     load_k();
     load_v();
+    // the sequences that this range shares with others: one that began before
+    // it, one that goes on behind it
+    const int last = u_end - 1, kvh_last = last / P;
+    const int b_last = find_in(s_indptr, batch, last % P, lane);
+    if (lane == 0) {
+      if (kvh * P + s_indptr[b] < u) s_seg[2 * warp] = make_int2(b, kvh);
+      const int at = kvh_last * P;
+      if (at + s_indptr[b_last] >= u && at + s_indptr[b_last + 1] > u_end)
+        s_seg[2 * warp + 1] = make_int2(b_last, kvh_last);
+    }
+  }
+  __syncthreads();
+  // The parts that the warps will leave in shared memory, listed in range order,
+  // and the runs of parts of one sequence: {first part, one past the last, slot,
+  // -}, slot -1 for a sequence that lies in this CTA, else 0 where its start does
+  // not, 1 where it does.  Read behind the barrier after the loop.
+  const int c_lo = range_start(cta * W), c_hi = range_start(cta * W + W);
+  if (warp == 0) {
+    const int2 seg = lane < S::kPieces ? s_seg[lane] : make_int2(-1, 0);
+    const unsigned have = __ballot_sync(0xffffffffu, seg.x >= 0);
+    const unsigned below = have & ((1u << lane) - 1);
+    const int before = below ? 31 - __clz(below) : lane;   // the part before this one
+    const int2 prev = make_int2(__shfl_sync(0xffffffffu, seg.x, before),
+                                __shfl_sync(0xffffffffu, seg.y, before));
+    const bool head = seg.x >= 0 && (!below || prev.x != seg.x || prev.y != seg.y);
+    const unsigned starts = __ballot_sync(0xffffffffu, head);
+    if (seg.x >= 0) s_part[__popc(below)] = lane;
+    if (head) {
+      const unsigned after = starts & ~(0xffffffffu >> (31 - lane));
+      const int next = after ? __ffs(after) - 1 : 32;
+      const int lo = seg.y * P + s_indptr[seg.x], hi = seg.y * P + s_indptr[seg.x + 1];
+      const int slot = lo >= c_lo && hi <= c_hi ? -1 : lo >= c_lo ? 1 : 0;
+      const int at = __popc(starts & ((1u << lane) - 1));
+      s_group[at] = make_int4(__popc(below), next == 32 ? __popc(have) : __popc(have & ((1u << next) - 1)),
+                              slot, 0);
+      s_group_at[at] = seg;
+      if (slot >= 0) {
+        // the CTAs that hold a part of it
+        auto cta_of = [&](int x) {
+          const int wide = extra * (per + 1);
+          return (x < wide ? x / (per + 1) : extra + (x - wide) / per) / W;
+        };
+        const int first = cta_of(lo);
+        s_shared[slot] = make_int4(seg.x, seg.y, first, cta_of(hi - 1) - first + 1);
+      }
+    }
+    if (lane == 0) s_groups = __popc(starts);
+  }
+  if (work) {
     reset();
     while (true) {
       // scores of the page's 16 tokens
@@ -370,66 +455,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             }
           }
         }
-      if (!whole && lane == 0) s_seg[piece] = make_int2(b_now, kvh_now);
       if (!more) break;
       reset();
     }
   }
   __syncthreads();
 
-  // The parts left in shared memory, listed in range order, and the runs of
-  // parts of one sequence: {first part, one past the last, slot, -}, slot -1 for
-  // a sequence that lies in this CTA, else 0 where its start does not, 1 where
-  // it does.
-  const int c_lo = range_start(cta * W), c_hi = range_start(cta * W + W);
-  if (warp == 0) {
-    const int2 seg = lane < S::kPieces ? s_seg[lane] : make_int2(-1, 0);
-    const unsigned have = __ballot_sync(0xffffffffu, seg.x >= 0);
-    const unsigned below = have & ((1u << lane) - 1);
-    const int before = below ? 31 - __clz(below) : lane;   // the part before this one
-    const int2 prev = make_int2(__shfl_sync(0xffffffffu, seg.x, before),
-                                __shfl_sync(0xffffffffu, seg.y, before));
-    const bool head = seg.x >= 0 && (!below || prev.x != seg.x || prev.y != seg.y);
-    const unsigned starts = __ballot_sync(0xffffffffu, head);
-    if (seg.x >= 0) s_part[__popc(below)] = lane;
-    if (head) {
-      const unsigned after = starts & ~(0xffffffffu >> (31 - lane));
-      const int next = after ? __ffs(after) - 1 : 32;
-      const int lo = seg.y * P + s_indptr[seg.x], hi = seg.y * P + s_indptr[seg.x + 1];
-      const int slot = lo >= c_lo && hi <= c_hi ? -1 : lo >= c_lo ? 1 : 0;
-      const int at = __popc(starts & ((1u << lane) - 1));
-      s_group[at] = make_int4(__popc(below), next == 32 ? __popc(have) : __popc(have & ((1u << next) - 1)),
-                              slot, 0);
-      s_group_at[at] = seg;
-      if (slot >= 0) {
-        // the CTAs that hold a part of it
-        auto cta_of = [&](int x) {
-          const int wide = extra * (per + 1);
-          return (x < wide ? x / (per + 1) : extra + (x - wide) / per) / W;
-        };
-        const int first = cta_of(lo);
-        s_shared[slot] = make_int4(seg.x, seg.y, first, cta_of(hi - 1) - first + 1);
-      }
-    }
-    if (lane == 0) s_groups = __popc(starts);
-  }
-  __syncthreads();
   constexpr int V4 = D / 4;
   const int heads = min(S::kHeads, p.g - head0), items = heads * V4;
-  // One thread's 4 elements of a state: O relative to m, and l.
-  struct Acc {
-    float m, l;
-    float4 o;
-    __device__ __forceinline__ void add(float pm, float pl, float4 y) {
-      const float top = fmaxf(m, pm), f = ex2_approx(m - top), w = ex2_approx(pm - top);
-      m = top;
-      l = l * f + pl * w;
-      o.x = o.x * f + y.x * w;
-      o.y = o.y * f + y.y * w;
-      o.z = o.z * f + y.z * w;
-      o.w = o.w * f + y.w * w;
-    }
-  };
   auto finish = [&](int2 at, int h, int i, const Acc& a) {
     const float inv = a.l > 0.f || a.l != a.l ? 1.f / a.l : 0.f;
     const size_t row = (size_t)at.x * p.h_q + (size_t)at.y * p.g + head0 + h;
@@ -442,11 +475,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const int h = e % items / V4, i = e % V4;
     const int4 grp = s_group[e / items];
     Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-    for (int k = grp.x; k < grp.y; ++k) {
-      const float* st = s_state + s_part[k] * S::kState;
-      a.add(st[S::kHeads * D + h], st[S::kHeads * D + S::kHeads + h],
-            reinterpret_cast<const float4*>(st + h * D)[i]);
+    constexpr int kBatch = 4;
+    for (int k0 = grp.x; k0 < grp.y; k0 += kBatch) {
+      float pm[kBatch], pl[kBatch];
+      float4 y[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool is = k0 + k < grp.y;
+        const float* st = s_state + s_part[is ? k0 + k : k0] * S::kState;
+        pm[k] = is ? st[S::kHeads * D + h] : -FLT_MAX;
+        pl[k] = is ? st[S::kHeads * D + S::kHeads + h] : 0.f;
+        y[k] = is ? reinterpret_cast<const float4*>(st + h * D)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      a.add(pm, pl, y);
     }
     if (grp.z < 0) {
       finish(s_group_at[e / items], h, i, a);
@@ -468,9 +509,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     int merge = 0;
     if (sh.w > 0) {
       int* n = p.counters + ((size_t)sh.y * batch + sh.x) * p.groups + group;
-      __threadfence();
+      // the parts that this CTA's threads wrote before the barrier, then the
+      // others': cumulative, and weaker (quicker) than __threadfence()
+      asm volatile("fence.acq_rel.gpu;" ::: "memory");
       merge = atomicAdd(n, 1) == sh.w - 1;
-      __threadfence();
+      asm volatile("fence.acq_rel.gpu;" ::: "memory");
       if (merge) *n = 0;
     }
     s_merge[tid] = merge;
@@ -509,8 +552,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             pl[k] = __ldcg(st + S::kHeads * D + S::kHeads + h);
           }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) a.add(pm[k], pl[k], y[k]);
+        a.add(pm, pl, y);
       }
       if (share == 1) {
         finish(make_int2(sh.x, sh.y), h, i, a);
@@ -526,7 +568,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         Acc a{s_ml[2 * tid], s_ml[2 * tid + 1], s_o[tid]};
         for (int k = 1; k < share; ++k) {
           const int e = k * items + tid;
-          a.add(s_ml[2 * e], s_ml[2 * e + 1], s_o[e]);
+          a.add({s_ml[2 * e]}, {s_ml[2 * e + 1]}, {s_o[e]});
         }
         finish(make_int2(sh.x, sh.y), tid / V4, tid % V4, a);
       }
