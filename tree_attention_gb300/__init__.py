@@ -559,7 +559,13 @@ class PagedCache:
             workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
         _check_dev("workspace", workspace)
         self.workspace = workspace
-        self._lib = lib()
+        # what the calls pass every time
+        L = lib()
+        self._append, self._decode = L.tree_attn_append_paged, L.tree_attn_decode_paged
+        self._compact, self._copy = L.tree_attn_compact_paged, L.tree_attn_copy_pages
+        self._b, self._b1 = (self.batch_size,), (self.batch_size + 1,)
+        self._nnz = (page_values.numel(),)
+        self._q_shape = (self.batch_size, self.h_q, self.head_dim)
         self._table = (page_indptr.data_ptr(), page_values.data_ptr(), length_info.data_ptr())
         self._pages = pages.data_ptr()
         self._tail = (ctypes.byref(self.dims), workspace.data_ptr(),
@@ -574,26 +580,20 @@ class PagedCache:
 
     def _ptr(self, name, t, dtype, shape):
         """Address of a contiguous tensor argument, checked."""
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        if t.get_device() != self._dev:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == self._dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} on {self.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
 
     def _rows(self, name, t, shape):
         """Address and token stride of a [tokens, heads, d] argument."""
-        if t.dtype is not self.dtype:
-            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-        if t.get_device() != self._dev:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-        n, heads, d = shape
+        if t.dtype is not self.dtype or t.shape != shape or t.get_device() != self._dev:
+            raise ValueError(f"{name} must be {self.dtype} {tuple(shape)} on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
         token, head, one = t.stride()
+        n, heads, d = shape
         if one != 1 or (head != d and heads > 1):
             raise ValueError(f"the rows of one token must be contiguous in {name}")
         return t.data_ptr(), token if n > 1 else heads * d
@@ -612,10 +612,6 @@ class PagedCache:
                 return torch.empty(shape, dtype=dtype, device=self.device)
         return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _done(self, status, what):
-        if status != TA_OK:
-            raise TreeAttnError(status, what)
-
     def append(self, q, k, v, append_indptr, positions=None, *, rope: Optional[Rope] = None,
                q_weight=None, k_weight=None, norm_eps: float = 1e-6, q_out=None, stream=None):
         """Write new tokens' keys and values to the last rows of their
@@ -632,31 +628,34 @@ class PagedCache:
         st = self._stream(stream)
         if q_out is None:
             q_out = self._empty((n, self.h_q, d), self.dtype, stream)
-        self._done(self._lib.tree_attn_append_paged(
+        ptr, i32 = self._ptr, torch.int32
+        st = self._append(
             qp, qs, kp, ks, vp, vs, n,
-            self._ptr("append_indptr", append_indptr, torch.int32, (self.batch_size + 1,)),
-            None if positions is None else self._ptr("positions", positions, torch.int32, (n,)),
-            None if q_weight is None else self._ptr("q_weight", q_weight, self.dtype, (d,)),
-            None if k_weight is None else self._ptr("k_weight", k_weight, self.dtype, (d,)),
+            ptr("append_indptr", append_indptr, i32, self._b1),
+            None if positions is None else ptr("positions", positions, i32, (n,)),
+            None if q_weight is None else ptr("q_weight", q_weight, self.dtype, (d,)),
+            None if k_weight is None else ptr("k_weight", k_weight, self.dtype, (d,)),
             norm_eps, None if rope is None else rope.ref, self._pages,
-            *self._table, self._ptr("q_out", q_out, self.dtype, (n, self.h_q, d)),
-            *self._tail, st), "tree_attn_append_paged")
+            *self._table, ptr("q_out", q_out, self.dtype, (n, self.h_q, d)), *self._tail, st)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_append_paged")
         return q_out
 
     def decode(self, q, sm_scale: float, out=None, lse=None, stream=None):
         """Attention of one new token per sequence, ``q [B, h_q, d]``, over all
         its kv rows; returns ``out`` and the base-2 ``lse [B, h_q]``."""
-        shape = (self.batch_size, self.h_q, self.head_dim)
+        shape = self._q_shape
         st = self._stream(stream)
         qp = self._ptr("q", q, self.dtype, shape)
         if out is None:
             out = self._empty(shape, self.dtype, stream)
         if lse is None:
             lse = self._empty(shape[:2], torch.float32, stream)
-        self._done(self._lib.tree_attn_decode_paged(
+        st = self._decode(
             qp, self._pages, *self._table, self._ptr("out", out, self.dtype, shape),
-            self._ptr("lse", lse, torch.float32, shape[:2]), sm_scale, *self._tail, st),
-            "tree_attn_decode_paged")
+            self._ptr("lse", lse, torch.float32, shape[:2]), sm_scale, *self._tail, st)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_decode_paged")
         return out, lse
 
     def compact(self, mn_indptr, accept_indptr, accept_nodes, *, new_page_indptr=None,
@@ -668,34 +667,41 @@ class PagedCache:
         length_info`` (for ``with_table``), the freed pages and their number
         ``[1]``, all on the device."""
         st = self._stream(stream)
-        b1, nnz = self.batch_size + 1, self.page_values.numel()
-
-        def array(name, t, n):
-            if t is None:
-                t = self._empty(n, torch.int32, stream)
-            return t, self._ptr(name, t, torch.int32, (n,))
-
-        outs = [array("new_page_indptr", new_page_indptr, b1),
-                array("new_page_values", new_page_values, nnz),
-                array("new_length_info", new_length_info, b1 - 1),
-                array("freed_pages", freed_pages, nnz), array("num_freed", num_freed, 1)]
+        ptr, i32, b, b1, nnz = self._ptr, torch.int32, self._b, self._b1, self._nnz
+        if new_page_indptr is None:
+            new_page_indptr = self._empty(b1, i32, stream)
+        if new_page_values is None:
+            new_page_values = self._empty(nnz, i32, stream)
+        if new_length_info is None:
+            new_length_info = self._empty(b, i32, stream)
+        if freed_pages is None:
+            freed_pages = self._empty(nnz, i32, stream)
+        if num_freed is None:
+            num_freed = self._empty((1,), i32, stream)
         n = accept_nodes.numel()
-        self._done(self._lib.tree_attn_compact_paged(
-            self._pages, *self._table, self._ptr("mn_indptr", mn_indptr, torch.int32, (b1,)),
-            self._ptr("accept_indptr", accept_indptr, torch.int32, (b1,)),
-            self._ptr("accept_nodes", accept_nodes, torch.int32, (n,)), n,
-            *[p for _, p in outs], *self._tail, st), "tree_attn_compact_paged")
-        return tuple(t for t, _ in outs)
+        st = self._compact(
+            self._pages, *self._table, ptr("mn_indptr", mn_indptr, i32, b1),
+            ptr("accept_indptr", accept_indptr, i32, b1),
+            ptr("accept_nodes", accept_nodes, i32, (n,)), n,
+            ptr("new_page_indptr", new_page_indptr, i32, b1),
+            ptr("new_page_values", new_page_values, i32, nnz),
+            ptr("new_length_info", new_length_info, i32, b),
+            ptr("freed_pages", freed_pages, i32, nnz), ptr("num_freed", num_freed, i32, (1,)),
+            *self._tail, st)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_compact_paged")
+        return new_page_indptr, new_page_values, new_length_info, freed_pages, num_freed
 
     def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
         """``pages[dst_pages[i]] = pages[src_pages[i]]``; no destination may be
         another pair's source or destination."""
         st = self._stream(stream)
         n = (src_pages.numel(),)
-        self._done(self._lib.tree_attn_copy_pages(
+        st = self._copy(
             self._pages, self._ptr("src_pages", src_pages, torch.int32, n),
-            self._ptr("dst_pages", dst_pages, torch.int32, n), n[0], *self._tail, st),
-            "tree_attn_copy_pages")
+            self._ptr("dst_pages", dst_pages, torch.int32, n), n[0], *self._tail, st)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_copy_pages")
 
     def device_status(self, stream=None) -> int:
         """Synchronise the stream and return (and clear) the device status."""

@@ -519,61 +519,62 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     s_merge[tid] = merge;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int slot = 0; slot < 2; ++slot) {
-    if (!s_merge[slot]) continue;
+  if (!s_merge[0] && !s_merge[1]) return;
+  // The threads share the parts of an element where there are more threads than
+  // elements, and each has several parts' loads in flight.
+  const int most = max(1, S::kThreads / (items * (s_merge[0] + s_merge[1])));
+  const int share0 = s_merge[0] ? min(s_shared[0].w, most) : 0;
+  const int share1 = s_merge[1] ? min(s_shared[1].w, most) : 0;
+  float* s_ml = s_state;                                                // [share][items][2]
+  float4* s_o = reinterpret_cast<float4*>(s_state + 2 * S::kThreads);   // [share][items]
+  for (int e = tid; e < items * (share0 + share1); e += S::kThreads) {
+    const int slot = e >= items * share0;
     const int4 sh = s_shared[slot];
-    const int n = sh.w;
+    const int share = slot ? share1 : share0, y0 = slot ? e - items * share0 : e;
+    const int x = y0 % items, h = x / V4, i = x % V4;
     // of its CTAs the first holds the sequence's start, its second part
     auto part = [&](int k) {
       return p.parts + (size_t)(((size_t)(sh.z + k) * p.groups + group) * 2 + (k == 0 ? 1 : 0)) * S::kState;
     };
-    // the threads share the n parts of an element where there are more threads
-    // than elements, and each has several parts' loads in flight
-    const int share = max(1, min(n, S::kThreads / items));
-    float* s_ml = s_state;                                            // [share][items][2]
-    float4* s_o = reinterpret_cast<float4*>(s_state + 2 * S::kThreads);   // [share][items]
-    for (int e = tid; e < items * share; e += S::kThreads) {
-      const int x = e % items, h = x / V4, i = x % V4;
-      Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      constexpr int kBatch = 8;
-      for (int k0 = e / items; k0 < n; k0 += share * kBatch) {
-        float pm[kBatch], pl[kBatch];
-        float4 y[kBatch];
+    Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    constexpr int kBatch = 8;
+    for (int k0 = y0 / items; k0 < sh.w; k0 += share * kBatch) {
+      float pm[kBatch], pl[kBatch];
+      float4 y[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          pm[k] = -FLT_MAX;
-          pl[k] = 0.f;
-          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k0 + k * share < n) {
-            const float* st = part(k0 + k * share);
-            y[k] = __ldcg(reinterpret_cast<const float4*>(st + h * D) + i);
-            pm[k] = __ldcg(st + S::kHeads * D + h);
-            pl[k] = __ldcg(st + S::kHeads * D + S::kHeads + h);
-          }
+      for (int k = 0; k < kBatch; ++k) {
+        pm[k] = -FLT_MAX;
+        pl[k] = 0.f;
+        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k * share < sh.w) {
+          const float* st = part(k0 + k * share);
+          y[k] = __ldcg(reinterpret_cast<const float4*>(st + h * D) + i);
+          pm[k] = __ldcg(st + S::kHeads * D + h);
+          pl[k] = __ldcg(st + S::kHeads * D + S::kHeads + h);
         }
-        a.add(pm, pl, y);
       }
-      if (share == 1) {
-        finish(make_int2(sh.x, sh.y), h, i, a);
-      } else {
-        s_ml[2 * e] = a.m;
-        s_ml[2 * e + 1] = a.l;
-        s_o[e] = a.o;
-      }
+      a.add(pm, pl, y);
     }
-    if (share > 1) {
-      __syncthreads();
-      if (tid < items) {
-        Acc a{s_ml[2 * tid], s_ml[2 * tid + 1], s_o[tid]};
-        for (int k = 1; k < share; ++k) {
-          const int e = k * items + tid;
-          a.add({s_ml[2 * e]}, {s_ml[2 * e + 1]}, {s_o[e]});
-        }
-        finish(make_int2(sh.x, sh.y), tid / V4, tid % V4, a);
-      }
-      __syncthreads();                 // the other slot's merge writes there again
+    if (share == 1) {
+      finish(make_int2(sh.x, sh.y), h, i, a);
+    } else {
+      s_ml[2 * e] = a.m;
+      s_ml[2 * e + 1] = a.l;
+      s_o[e] = a.o;
     }
+  }
+  if (share0 <= 1 && share1 <= 1) return;
+  __syncthreads();
+  for (int x = tid; x < 2 * items; x += S::kThreads) {
+    const int slot = x >= items, share = slot ? share1 : share0;
+    if (share <= 1) continue;
+    const int e0 = (slot ? items * share0 : 0) + x - slot * items;
+    Acc a{s_ml[2 * e0], s_ml[2 * e0 + 1], s_o[e0]};
+    for (int k = 1; k < share; ++k) {
+      const int e = e0 + k * items;
+      a.add({s_ml[2 * e]}, {s_ml[2 * e + 1]}, {s_o[e]});
+    }
+    finish(make_int2(s_shared[slot].x, s_shared[slot].y), x % items / V4, x % V4, a);
   }
 }
 
