@@ -342,7 +342,8 @@ ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim,
  * share a page that receives tokens.  A token whose sequence's tables are
  * inconsistent (or whose page is outside the pool) is not written to the
  * cache, which tree_attn_device_status reports.  Pointers 16-byte aligned.
- * Asynchronous on stream. */
+ * total_new times the steps of 512 / head_dim heads of a token's q, k and v
+ * must fit an int32 (else TA_ERR_UNSUPPORTED).  Asynchronous on stream. */
 ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
                                  int64_t k_stride, const void* v, int64_t v_stride,
                                  int32_t total_new, const int32_t* append_indptr,

@@ -981,8 +981,11 @@ ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
   if (nsm <= 0) return cuda_failure();
   const int rows = 512 / dims->head_dim;
   const int64_t steps = ta::ceil_div(dims->h_q, rows) + 2 * ta::ceil_div(dims->h_kv, rows);
+  if (total_new * steps > INT32_MAX) return TA_ERR_UNSUPPORTED;
   const int grid = (int)std::min<int64_t>((int64_t)ta::kAppendCtas * nsm,
                                           ta::ceil_div(total_new * steps, 4));
+  ap.steps_per_warp = (int)(total_new * steps / (4 * grid));
+  ap.steps_extra = (int)(total_new * steps % (4 * grid));
   if (rope) {
     ap.rope_layout = rope->layout;
     ap.rotary_dim = rope->rotary_dim;

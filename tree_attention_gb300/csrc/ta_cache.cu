@@ -80,19 +80,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
   // steps of a token: its queries' (kind 0), keys' (1) and values' (2)
   const int steps_q = (p.h_q + kRows - 1) / kRows, steps_kv = (p.h_kv + kRows - 1) / kRows;
   const int all = steps_q + 2 * steps_kv;
-  // this warp's share of all tokens' steps: from step ``s`` of token ``t`` on
-  const int64_t total = (int64_t)p.total_new * all;
-  const int64_t warps = (int64_t)gridDim.x * (kAppendThreads / 32);
-  const int64_t gw = (int64_t)blockIdx.x * (kAppendThreads / 32) + warp;
-  const int64_t lo = gw * total / warps;
-  int64_t left = (gw + 1) * total / warps - lo;
-  if (left <= 0) return;
-  int t = (int)(lo / all), begin = (int)(lo % all);
+  // this warp's share of all tokens' steps: ``left`` of them from step ``begin``
+  // of token ``t`` on
+  const int gw = blockIdx.x * (kAppendThreads / 32) + warp;
+  const int lo = gw * p.steps_per_warp + min(gw, p.steps_extra);
+  int left = p.steps_per_warp + (gw < p.steps_extra);
+  if (left == 0) return;
+  int t = lo / all, begin = lo - t * all;
   auto first_step = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? steps_q : steps_q + steps_kv; };
 
   // The fetches: their token, step, and of the step's rows this lane's.
-  int64_t f_left = left;
-  int f_t = t, f_step = begin, f_next_kind = begin, f_row = 0, f_rows = 0, f_slot = 0;
+  int f_left = left, f_t = t, f_step = begin, f_next_kind = begin, f_row = 0, f_rows = 0, f_slot = 0;
   const uint16_t* f_src = nullptr;
   auto fetch = [&]() {
     if (f_left > 0) {
@@ -101,9 +99,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
         const int kind = f_step < steps_q ? 0 : f_step < steps_q + steps_kv ? 1 : 2;
         f_row = (f_step - first_step(kind)) * kRows + lane_row;
         f_rows = kind == 0 ? p.h_q : p.h_kv;
-        f_src = (kind == 0   ? p.q + f_t * p.q_stride
-                 : kind == 1 ? p.k + f_t * p.k_stride
-                             : p.v + f_t * p.v_stride) + f_row * D;
+        f_src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + f_row * D +
+                f_t * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
         f_next_kind = kind == 2 ? 0 : first_step(kind + 1);
       }
       if (f_row < f_rows) {
@@ -126,14 +123,57 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
 #pragma unroll 1
   for (int i = 0; i < kAppendDepth; ++i) fetch();
 
-  // the current sequence's tokens, first table entry and kv rows (kv < 0: bad tables)
-  int a0 = 0, a1 = 0, p0 = 0, kv = -1;
+  // Positions and cache slots of the next 32 tokens, one per lane: one chain of
+  // dependent loads for all tokens that a warp comes by, and it runs while the
+  // first rows arrive.
+  const int t_end = (lo + left - 1) / all + 1;
+  int m_from = t, m_pos = 0;
+  long long m_slot = -1;                   // element offset of a token's K slot, head 0; -1: none
+  auto look_up = [&]() {
+    const int tt = m_from + lane;
+    const bool mine = tt < t_end;
+    if (LAYOUT != 0 && mine) m_pos = p.positions[tt];
+    // the sequence of the first token, then of the others behind it
+    int b = find_sequence(p.append_indptr, p.tab.batch, m_from, lane);
+    if (mine && tt >= p.append_indptr[b + 1]) {
+      int hi = p.tab.batch;                // the largest b with append_indptr[b] <= tt
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (p.append_indptr[mid] <= tt)
+          b = mid;
+        else
+          hi = mid;
+      }
+    }
+    m_slot = -1;
+    if (!mine) return;
+    const int a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
+    const int p0 = p.tab.page_indptr[b], p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
+    if (a0 >= 0 && tt >= a0 && tt < a1 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
+        p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize) {
+      const int kv = (p1 - p0 - 1) * kPageSize + last, row = kv - (a1 - tt);
+      if (kv >= a1 - a0) {
+        const int page = p.tab.page_values[p0 + row / kPageSize];
+        if (page >= 0 && page < p.tab.num_pages)
+          m_slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
+      }
+    }
+    if (m_slot < 0) report_bad_tables(p.error);
+  };
+  look_up();
+
   int ring = 0;
-  long long slot = -1;                     // element offset of the token's K slot, head 0
-  auto token = [&]() {
-    __syncwarp();
+  for (; left > 0; ++t, begin = 0) {
+    const int end = min(all, begin + left);
+    left -= end - begin;
+    if (t - m_from == 32) {
+      m_from = t;
+      look_up();
+    }
+    const long long slot = __shfl_sync(0xffffffffu, m_slot, t - m_from);
     if (LAYOUT != 0) {
-      const int64_t pos = p.positions[t];
+      const int64_t pos = __shfl_sync(0xffffffffu, m_pos, t - m_from);
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         const int j = lane + 32 * i;
@@ -146,32 +186,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
           s_cos_sin[warp][j] = make_float2(cs * p.magnitude, sn * p.magnitude);
         }
       }
+      __syncwarp();
     }
-    if (t < a0 || t >= a1) {
-      const int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
-      a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
-      p0 = p.tab.page_indptr[b];
-      const int p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
-      const bool good = a0 >= 0 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
-                        p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize;
-      kv = good ? (p1 - p0 - 1) * kPageSize + last : -1;
-      if (kv < a1 - a0) kv = -1;
-    }
-    slot = -1;
-    if (kv >= 0 && t >= a0 && t < a1) {
-      const int row = kv - (a1 - t);
-      const int page = p.tab.page_values[p0 + row / kPageSize];
-      if (page >= 0 && page < p.tab.num_pages)
-        slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
-    }
-    if (slot < 0 && lane == 0) report_bad_tables(p.error);
-    __syncwarp();
-  };
-
-  for (; left > 0; ++t, begin = 0) {
-    const int end = (int)min((int64_t)all, begin + left);
-    left -= end - begin;
-    token();
 #pragma unroll 1
     for (int kind = 0; kind < 3; ++kind) {
       const int k_lo = first_step(kind), k_hi = kind == 2 ? all : first_step(kind + 1);

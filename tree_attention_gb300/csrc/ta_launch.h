@@ -134,6 +134,7 @@ struct AppendParams {
   PageTable tab;
   unsigned int* error;
   int total_new, h_q, h_kv;
+  int steps_per_warp, steps_extra;        // warps below steps_extra have one step more
   float eps;
   int rope_layout, rotary_dim;            // layout 0: no rotation
   float magnitude;
