@@ -308,7 +308,30 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
 // compact
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
-constexpr int kCompactBatch = 16;   // rows whose vectors one thread has in flight
+constexpr int kCompactBatch = 8;   // rows whose vectors one thread has in flight
+
+// What the tables say of one sequence.
+struct CompactSeq {
+  int p0, p1, last, m0, m1, a0, a1;
+  __device__ __forceinline__ int pages() const { return p1 - p0; }
+  __device__ __forceinline__ int tree() const { return m1 - m0; }
+  __device__ __forceinline__ int accepted() const { return a1 - a0; }
+  __device__ __forceinline__ int kv() const { return p1 > p0 ? (p1 - p0 - 1) * kPageSize + last : 0; }
+  // pages it keeps
+  __device__ __forceinline__ int keep() const {
+    return (kv() - tree() + accepted() + kPageSize - 1) / kPageSize;
+  }
+  __device__ __forceinline__ bool good(const CompactParams& p) const {
+    return p0 >= 0 && p1 >= p0 && p1 <= p.tab.nnz_pages &&
+           (p1 == p0 || (last >= 1 && last <= kPageSize)) && a0 >= 0 && a1 >= a0 &&
+           a1 <= p.total_accept && m1 >= m0 && accepted() <= tree() && tree() <= kv();
+  }
+};
+__device__ __forceinline__ CompactSeq compact_seq(const CompactParams& p, int i) {
+  return CompactSeq{p.tab.page_indptr[i], p.tab.page_indptr[i + 1], p.tab.length_info[i],
+                    p.mn_indptr[i],       p.mn_indptr[i + 1],       p.accept_indptr[i],
+                    p.accept_indptr[i + 1]};
+}
 
 // CTA (b, y): sequence b, 256 of the 16-byte columns of its cache rows (a
 // column: one vector of one head of keys or values).  The moves are in place
@@ -318,42 +341,37 @@ constexpr int kCompactBatch = 16;   // rows whose vectors one thread has in flig
 // reads what it has overwritten.
 // CTA (b, 0) also writes sequence b's part of the new table, whose place it
 // finds by summing the pages the sequences before it keep.
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p) {
+// A few rows per sequence: bound by the chain of dependent loads (tables,
+// nodes, pages, rows), so the independent ones are issued together and the
+// registers leave room for four CTAs per SM.
+__global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const CompactParams p) {
   __shared__ long long s_src[kCompactThreads], s_dst[kCompactThreads];
   __shared__ int s_sum[kCompactThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, b = blockIdx.x;
   const PageTable& tb = p.tab;
+  const CompactSeq me = compact_seq(p, b);
+  // all sequences' tables are checked by every CTA: one that is inconsistent
+  // stops them all
   int before = 0;          // pages kept by the sequences before b
-  int bad = 0;
-  if (tid == 0)
-    bad = tb.page_indptr[0] != 0 || p.accept_indptr[0] != 0 ||
-          tb.page_indptr[tb.batch] > tb.nnz_pages ||
-          p.accept_indptr[tb.batch] != p.total_accept;
-  auto rows_of = [&](int i, int& p0, int& np, int& kv, int& tree, int& a0, int& acc) {
-    p0 = __ldg(tb.page_indptr + i);
-    np = __ldg(tb.page_indptr + i + 1) - p0;
-    const int last = __ldg(tb.length_info + i);
-    tree = __ldg(p.mn_indptr + i + 1) - __ldg(p.mn_indptr + i);
-    a0 = __ldg(p.accept_indptr + i);
-    acc = __ldg(p.accept_indptr + i + 1) - a0;
-    kv = np > 0 ? (np - 1) * kPageSize + last : 0;
-    return np >= 0 && p0 >= 0 && np <= tb.nnz_pages &&
-           (np == 0 || (last >= 1 && last <= kPageSize)) && acc >= 0 && acc <= tree && tree <= kv;
-  };
-  int p0, np, kv, tree, a0, acc;
+  bool bad = tid == 0 && (tb.page_indptr[0] != 0 || p.accept_indptr[0] != 0 ||
+                          p.accept_indptr[tb.batch] != p.total_accept);
   for (int i = tid; i < tb.batch; i += kCompactThreads) {
-    bad |= !rows_of(i, p0, np, kv, tree, a0, acc);
-    if (i < b) before += (kv - tree + acc + kPageSize - 1) / kPageSize;
+    const CompactSeq x = compact_seq(p, i);
+    bad |= !x.good(p);
+    if (i < b) before += x.keep();
   }
+  const bool mine = me.good(p);
+  const int acc = mine ? me.accepted() : 0, tree = mine ? me.tree() : 0;
+  auto node_at = [&](int j) { return j >= 0 && j < acc ? p.accept_nodes[me.a0 + j] : -1; };
+  int node = node_at(tid), prev = node_at(tid - 1);
+  const int page0 = mine && tid < me.pages() ? tb.page_values[me.p0 + tid] : 0;
   if (__syncthreads_or(bad)) {
     if (tid == 0) report_bad_tables(p.error);
     return;
   }
-  rows_of(b, p0, np, kv, tree, a0, acc);
-  const int start = kv - tree;
-  const int keep = (start + acc + kPageSize - 1) / kPageSize;
+  const int start = me.kv() - tree, keep = me.keep();
 
   // the moves: every node checked before the first row moves
   const int64_t head_vecs = (int64_t)kPageSize * p.row_vecs;   // one head's plane of a page
@@ -361,26 +379,32 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
   const int col = blockIdx.y * kCompactThreads + tid;
   const int64_t col_off = (int64_t)(col / p.row_vecs) * head_vecs + col % p.row_vecs;
   auto row_offset = [&](int row) -> long long {
-    const int page = __ldg(tb.page_values + p0 + row / kPageSize);
+    const int page = tb.page_values[me.p0 + row / kPageSize];
     if (page < 0 || page >= tb.num_pages) return -1;
     return (long long)page * 2 * p.h_kv * head_vecs + (long long)(row % kPageSize) * p.row_vecs;
   };
   auto stage = [&](int j) {      // move j into slot tid; whether it is valid
-    const int node = __ldg(p.accept_nodes + a0 + j);
-    const int prev = j > 0 ? __ldg(p.accept_nodes + a0 + j - 1) : -1;
     if (node <= prev || node >= tree) return false;
     s_src[tid] = s_dst[tid] = -1;
     if (node == j) return true;  // stays where it is
-    s_src[tid] = row_offset(start + node);
-    s_dst[tid] = row_offset(start + j);
-    return s_src[tid] >= 0 && s_dst[tid] >= 0;
+    const long long from = row_offset(start + node), to = row_offset(start + j);
+    s_src[tid] = from;
+    s_dst[tid] = to;
+    return from >= 0 && to >= 0;
   };
   bool ok = true;
-  for (int j = tid; j < acc; j += kCompactThreads) ok = stage(j) && ok;
+  if (tid < acc) ok = stage(tid);
+  for (int j = tid + kCompactThreads; j < acc; j += kCompactThreads) {
+    node = node_at(j);
+    prev = node_at(j - 1);
+    ok = stage(j) && ok;
+  }
   if (__syncthreads_and(ok)) {
     for (int j0 = 0; j0 < acc; j0 += kCompactThreads) {
       if (acc > kCompactThreads) {
         __syncthreads();
+        node = node_at(j0 + tid);
+        prev = node_at(j0 + tid - 1);
         if (j0 + tid < acc) stage(j0 + tid);
         __syncthreads();
       }
@@ -410,19 +434,19 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
   before = 0;
 #pragma unroll
   for (int i = 0; i < kCompactThreads / 32; ++i) before += s_sum[i];
-  for (int i = tid; i < np; i += kCompactThreads) {
-    const int page = __ldg(tb.page_values + p0 + i);
+  for (int i = tid; i < me.pages(); i += kCompactThreads) {
+    const int page = i == tid ? page0 : tb.page_values[me.p0 + i];
     if (i < keep)
       p.new_values[before + i] = page;
     else
-      p.freed[p0 - before + i - keep] = page;
+      p.freed[me.p0 - before + i - keep] = page;
   }
   if (tid == 0) {
     p.new_indptr[b] = before;
     p.new_length[b] = keep > 0 ? start + acc - (keep - 1) * kPageSize : 0;
     if (b == tb.batch - 1) {
       p.new_indptr[tb.batch] = before + keep;
-      *p.num_freed = p0 + np - (before + keep);
+      *p.num_freed = me.p1 - (before + keep);
     }
   }
 }
