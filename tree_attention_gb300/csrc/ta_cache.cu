@@ -34,7 +34,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
   while (hi - lo > 1) {
     const int step = (hi - lo + 32) / 33;
     const int at = lo + (lane + 1) * step;
-    const bool le = at < hi && __ldg(indptr + at) <= t;
+    const bool le = at < hi && indptr[at] <= t;
     const int c = __popc(__ballot_sync(0xffffffffu, le));
     lo += c * step;
     hi = min(hi, lo + step);
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const Compa
 // copies of pages
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kCopyDepth = 6;        // lines a CTA has in flight
+constexpr int kCopyDepth = 4;        // lines a CTA has in flight
 constexpr int kCopyPairs = 256;      // pairs a CTA checks at a time
 constexpr int kCopyFilter = 4096;    // bits
 
@@ -473,8 +473,8 @@ struct CopyAt {
 // The n pages are one list of 4 KB lines (a page is h_kv * d / 64 of them: one
 // 16-byte vector per thread each), cut evenly over the CTAs.  Lines pass
 // through a ring in shared memory by cp.async, each thread reading back only
-// what it fetched itself, so nothing waits for anything but its own data: six
-// lines in flight in each of five CTAs keep 120 KB of loads on the way to an
+// what it fetched itself, so nothing waits for anything but its own data: four
+// lines in flight in each of five CTAs keep 80 KB of loads on the way to an
 // SM (ten lines measured the same on large copies and slower on small ones).  Before its first store a CTA looks for its
 // pairs' destinations among all other pairs' sources and destinations, through
 // a bit filter in shared memory (a hit is then looked up exactly), while the

@@ -588,18 +588,10 @@ cudaError_t launch(const DecodeParams& p, int nsm, cudaStream_t stream) {
   using S = Shape<D, NT>;
   const size_t smem = (size_t)S::kPieces * S::kState * 4 + (size_t)(p.tab.batch + 1) * 4 + p.tab.batch;
   const auto kern = decode_kernel<D, BF16, NT>;
-  // once per device: the most that any batch needs
-  static std::atomic<uint64_t> allowed{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<uint64_t> allowed{0};   // for the most that any batch needs
+  const cudaError_t e = allow_shared(
+      (const void*)kern, S::kPieces * S::kState * 4 + kMaxCacheBatch * 5 + 4, allowed);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-    const int most = (int)(S::kPieces * S::kState * 4 + kMaxCacheBatch * 5 + 4);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
-    allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
   const int per = ctas_per_group(nsm, p.groups);
   return launch_pdl(kern, dim3(per * p.groups), dim3(S::kThreads), smem, stream, p);
 }
