@@ -108,6 +108,10 @@ DECODE = {
     "group_16": ([300, 31], 16, 1, 64, "bf16"),
     "group_20": ([150, 2], 20, 1, 128, "fp16"),
     "group_128": ([90, 18], 128, 1, 128, "bf16"),
+    "group_12_long": ([7000, 33, 2500], 24, 2, 64, "fp16"),
+    "group_40_long": ([4000, 1, 900], 40, 1, 128, "bf16"),
+    "group_128_long": ([3500], 128, 1, 64, "bf16"),
+    "many_kv_heads": ([260, 0, 31], 80, 80, 64, "bf16"),
     "one_long": ([9000], 4, 1, 128, "bf16"),
     "ragged": ([int(x) for x in np.random.default_rng(4).integers(0, 700, 40)], 8, 2, 64, "bf16"),
     "many_short": ([1 + i % 37 for i in range(300)], 4, 2, 128, "fp16"),
@@ -124,6 +128,27 @@ def test_decode(name):
         out, lse = s.cache.decode(q, sm)
         assert s.cache.device_status() == ta.TA_OK
         check_decode(s, q, out, lse, sm)
+
+
+def test_decode_largest_batch():
+    """16,384 sequences of 0 to 20 rows."""
+    rng = np.random.default_rng(9)
+    s = Setup(rng.integers(0, 21, 16384), 2, 1, 64, "bf16", seed=10)
+    q = s.randn(16384, 2, 64)
+    out, lse = s.cache.decode(q, 0.125)
+    assert s.cache.device_status() == ta.TA_OK
+    check_decode(s, q, out, lse, 0.125)
+    with pytest.raises(ta.TreeAttnError):
+        ta.PagedCache(s.pool, i32(np.zeros(16386)), i32([0]), i32(np.zeros(16385)), h_q=2)
+
+
+def test_decode_without_any_page():
+    pool = torch.full((2, 2, 2, 16, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    c = ta.PagedCache(pool, i32([0, 0, 0]), i32([]), i32([0, 0]), h_q=4)
+    q = torch.ones((2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = c.decode(q, 0.1)
+    assert c.device_status() == ta.TA_OK
+    assert (out == 0).all() and (lse == -np.inf).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -474,9 +499,60 @@ def test_copy_pages_skips_conflicting_pairs():
     assert s.cache.device_status() == ta.TA_OK and torch.equal(s.pool, want)
 
 
+def test_copy_pages_finds_conflicts_anywhere_in_a_long_list():
+    rng = np.random.default_rng(33)
+    pages, n = 12000, 5000
+    s = Setup([16], 1, 1, 64, seed=33, spare=pages - 1)
+    s.pool.copy_(torch.randn(s.pool.shape, device="cuda"))
+    p = rng.permutation(pages)
+    src, dst = p[:n].copy(), p[n:2 * n].copy()
+    for i, j in rng.integers(0, n, (20, 2)):                # a destination twice
+        dst[i] = dst[j]
+    for i, j in rng.integers(0, n, (20, 2)):                # a destination that is a source
+        dst[i] = src[j]
+    uses = {}
+    for i in range(n):
+        for page in {int(src[i]), int(dst[i])}:
+            uses.setdefault(page, set()).add(i)
+    good = [i for i in range(n) if src[i] != dst[i] and uses[int(dst[i])] == {i}]
+    assert n - 60 <= len(good) < n
+    want = s.pool.clone()
+    want[torch.from_numpy(dst[good]).cuda()] = s.pool[torch.from_numpy(src[good]).cuda()]
+    s.cache.copy_pages(i32(src), i32(dst))
+    assert s.cache.device_status() == ta.TA_ERR_INVALID_ARGUMENT
+    assert torch.equal(s.pool, want)
+
+
 # --------------------------------------------------------------------------
 # the handle, and all of them together
 # --------------------------------------------------------------------------
+
+def test_offsets_past_32_bits():
+    """Pages whose first element lies past 2^32 elements: every call gives there
+    what it gives on the same pages of a small pool."""
+    h_kv, d, far = 8, 128, 140000                            # 32768 elements per page
+    s = Setup([100, 37], 16, h_kv, d, "bf16", seed=71, spare=6, fill=0.0)
+    assert far * 2 * h_kv * 16 * d > 2 ** 32
+    big = torch.empty((far + s.pool.shape[0], 2, h_kv, 16, d), dtype=s.dtype, device="cuda")
+    big[far:] = s.pool
+    table = [i32(s.indptr), i32(s.values + far), i32(s.last)]
+    c = ta.PagedCache(big, *table, h_q=16)
+    rope = ta.Rope("interleaved", 64)
+    x = append_inputs(s, [20, 5], True)
+    res = []
+    for cache, off in ((s.cache, 0), (c, far)):
+        q = cache.append(*x, i32([0, 20, 25]), i32(np.arange(25)), rope=rope)
+        last = q[[19, 24]].contiguous()
+        out, lse = cache.decode(last, 0.09)
+        cache.copy_pages(i32(s.values[:2] + off), i32(np.array([p for p in range(14) if p not in
+                                                                s.values[:10].tolist()][:2]) + off))
+        new = cache.compact(i32([0, 20, 25]), i32([0, 3, 4]), i32([1, 5, 19, 2]))
+        assert cache.device_status() == ta.TA_OK
+        res.append([q, out, lse, new[0], new[1][:int(new[0][-1])] - off, new[2],
+                    new[3][:int(new[4])] - off])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    assert torch.equal(big[far:], s.pool)
 
 def test_handle_refusals():
     s = Setup([20, 3], 4, 2, 64, seed=41)

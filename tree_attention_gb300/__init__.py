@@ -555,8 +555,11 @@ class PagedCache:
         if need == 0:
             raise TreeAttnError(TA_ERR_UNSUPPORTED, "tree_attn_cache_workspace_size")
         if workspace is None or workspace.numel() * workspace.element_size() < need:
-            # zero-filled once: the library keeps its counters consistent afterwards
+            # zero-filled once, before a call on any stream: the library keeps its
+            # counters consistent afterwards
             workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self._dev).synchronize()
         _check_dev("workspace", workspace)
         self.workspace = workspace
         # what the calls pass every time
