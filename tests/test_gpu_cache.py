@@ -2,9 +2,10 @@
 references.
 
 Tolerances.  A value rounded to a 16-bit type is off by at most half a step,
-``eps / 2`` of it.  decode: besides the output's rounding each weight of the
-weighted sum is rounded once, which moves the output by at most ``eps / 2 *
-sum w |v|``.  A score is a float32 sum of d products: it is off by at most
+``eps / 2`` of it.  decode: the output is rounded once; a weight passes as its
+rounding and the rounding of the rest, which leaves ``(eps / 2)^2`` of it, and
+the weighted sums add up to a few dozen float32 terms one after the other
+(2^-23 each, truncated), 2^-18 of ``sum w |v|`` together.  A score is a float32 sum of d products: it is off by at most
 ``(d + 4) * 2^-23`` (truncating adds) of the sum of its products' sizes, S, in
 base-2 units; a weight is then off by that times ln 2, relative, twice (in the
 weight and in the sum), and the lse by it once, plus the float32 rounding of
@@ -83,7 +84,7 @@ def check_decode(s, q, out, lse, sm_scale):
     out, lse = f64(out), f64(lse)
     half = torch.finfo(s.dtype).eps / 2
     serr = (s.d + 4) * 2.0 ** -23 * smag
-    tol = half * (np.abs(ro) + mag) + 2 * serr[..., None] * mag + 2.0 ** -20 * mag \
+    tol = half * np.abs(ro) + (half ** 2 + 2.0 ** -18) * mag + 2 * serr[..., None] * mag \
         + torch.finfo(s.dtype).smallest_normal * half * 2
     assert np.isfinite(out).all()
     bad = np.abs(out - ro) > tol

@@ -386,17 +386,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             }
           }
       }
-      uint32_t w0[NT], w1[NT];
+      uint32_t w0[NT][2], w1[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[n][i] = ex2_approx(x[n][i] - m[n][i & 1]);
         l[n][0] += x[n][0] + x[n][2];
         l[n][1] += x[n][1] + x[n][3];
-        // one rounding of each weight to 16 bits, for the tensor cores; the sum
-        // l takes them unrounded
-        w0[n] = transpose8x8(pack2<BF16>(x[n][0], x[n][1]));
-        w1[n] = transpose8x8(pack2<BF16>(x[n][2], x[n][3]));
+        // the tensor cores take a weight as two 16-bit numbers, its rounding and
+        // what that left (2^-16 of it or less is lost), so that the output is
+        // rounded once; measured free up to 8 heads per kv head (the loads bound
+        // the loop), 2 % slower for 16.  The sum l takes the weights as they are
+        const uint32_t h0 = pack2<BF16>(x[n][0], x[n][1]), h1 = pack2<BF16>(x[n][2], x[n][3]);
+        const float2 g0 = unpack2<BF16>(h0), g1 = unpack2<BF16>(h1);
+        w0[n][0] = transpose8x8(h0);
+        w1[n][0] = transpose8x8(h1);
+        w0[n][1] = transpose8x8(pack2<BF16>(x[n][0] - g0.x, x[n][1] - g0.y));
+        w1[n][1] = transpose8x8(pack2<BF16>(x[n][2] - g1.x, x[n][3] - g1.y));
       }
 #pragma unroll
       for (int h = 0; h < VH; ++h)
@@ -407,7 +413,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
           const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
           const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<BF16>(o[n][4 * h + t], a0, a1, a2, a3, w0[n], w1[n]);
+          for (int n = 0; n < NT; ++n) {
+            mma16816<BF16>(o[n][4 * h + t], a0, a1, a2, a3, w0[n][0], w1[n][0]);
+            mma16816<BF16>(o[n][4 * h + t], a0, a1, a2, a3, w0[n][1], w1[n][1]);
+          }
         }
       if (more) load_v();
       if (!seg_done && more) continue;
