@@ -89,6 +89,17 @@ struct Shape {
   static_assert(kPieces * kState >= 6 * kThreads, "the last merge's sums fit");
 };
 
+// U units over up to ``grid`` CTAs of W warps, a unit per warp at least.
+__host__ __device__ __forceinline__ DecodeSplit decode_split(int U, int grid, int W) {
+  DecodeSplit s{};
+  s.ctas = (U + W - 1) / W < grid ? (U + W - 1) / W : grid;
+  if (s.ctas > 0) {
+    s.per = U / (s.ctas * W);
+    s.extra = U % (s.ctas * W);
+  }
+  return s;
+}
+
 // The largest b with s_indptr[b] <= x, over batch sequences; by one warp.
 __device__ __forceinline__ int find_in(const int32_t* s_indptr, int batch, int x, int lane) {
   int lo = 0, hi = batch;
@@ -154,40 +165,42 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   const int r = lane >> 2, c = lane & 3;
   const int batch = p.tab.batch;
 
-  // This CTA's and this warp's range of units, for a table of ``pages`` entries:
-  // U = warps * per + extra units, one more for each of the first ``extra`` warps.
-  const int group = blockIdx.x % p.groups;                 // of the heads of one kv head
-  const int cta = blockIdx.x / p.groups;
-  int P = 0, ctas = 0, per = 0, extra = 0, u = 0, u_end = 0, pv = 0;
-  auto range_start = [&](int w) { return w * per + min(w, extra); };
+  // the first of the table's entries that this thread checks
+  int first = 0, first_next = 0, first_len = 0;
+  if (tid <= batch) first = p.tab.page_indptr[tid];
+  if (tid < batch) {
+    first_next = p.tab.page_indptr[tid + 1];
+    first_len = p.tab.length_info[tid];
+  }
+  // This CTA's and this warp's range of units: U = warps * per + extra units,
+  // one more for each of the first ``extra`` warps.  The table is usually as
+  // long as its array, for which the host has divided: its first entries are
+  // on their way while its offsets arrive.
+  const int group = blockIdx.y, cta = blockIdx.x;          // group: of the heads of one kv head
+  int P = p.tab.nnz_pages, u = 0, u_end = 0, pv = 0;
+  DecodeSplit sp = p.split;
+  auto range_start = [&](int w) { return w * sp.per + min(w, sp.extra); };
   // physical pages of the 32 units from x on, one per lane
   auto pages_at = [&](int x) {
     return x + lane < u_end ? p.tab.page_values[(x + lane) % P] : 0;
   };
-  auto plan = [&](int pages) {
-    P = pages;
-    const int U = pages * p.h_kv;
-    ctas = min((int)gridDim.x / p.groups, (U + W - 1) / W);
-    u = u_end = 0;
-    if (cta >= ctas) return;
-    per = U / (ctas * W);
-    extra = U % (ctas * W);
+  auto set_range = [&]() {
+    if (cta >= sp.ctas) return;
     u = range_start(cta * W + warp);
     u_end = range_start(cta * W + warp + 1);
     pv = pages_at(u);
   };
-  // the table is usually as long as its array: its first entries are on their
-  // way while its offsets arrive
-  plan(p.tab.nnz_pages);
+  set_range();
 
   // the page table's offsets and last lengths, checked as a whole
   bool bad = false;
   for (int i = tid; i <= batch; i += S::kThreads) {
-    const int a = p.tab.page_indptr[i];
+    const int a = i == tid ? first : p.tab.page_indptr[i];
     s_indptr[i] = a;
     bad |= i == 0 ? a != 0 : a < 0 || a > p.tab.nnz_pages;
     if (i < batch) {
-      const int e = p.tab.page_indptr[i + 1], len = p.tab.length_info[i];
+      const int e = i == tid ? first_next : p.tab.page_indptr[i + 1];
+      const int len = i == tid ? first_len : p.tab.length_info[i];
       bad |= e < a || (e > a && (len < 1 || len > kPageSize));
       s_len[i] = (uint8_t)len;
     }
@@ -198,15 +211,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
     return;
   }
-  if (s_indptr[batch] != P) plan(s_indptr[batch]);
+  if (s_indptr[batch] != P) {
+    P = s_indptr[batch];
+    sp = decode_split(P * p.h_kv, gridDim.x, W);
+    u = u_end = 0;
+    set_range();
+  }
   // sequences without rows
-  for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+  for (int b = group * gridDim.x + cta; b < batch; b += gridDim.x * gridDim.y) {
     if (s_indptr[b] != s_indptr[b + 1]) continue;
     uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.h_q * D);
     for (int i = tid; i < p.h_q * (D / 8); i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < p.h_q; i += S::kThreads) p.lse[(size_t)b * p.h_q + i] = -INFINITY;
   }
-  if (cta >= ctas) return;
+  if (cta >= sp.ctas) return;
   const int head0 = group * S::kHeads;                     // of the kv head's g
   const int u_first = u;
   const bool work = u < u_end;
@@ -302,8 +320,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       if (slot >= 0) {
         // the CTAs that hold a part of it
         auto cta_of = [&](int x) {
-          const int wide = extra * (per + 1);
-          return (x < wide ? x / (per + 1) : extra + (x - wide) / per) / W;
+          const int wide = sp.extra * (sp.per + 1);
+          return (x < wide ? x / (sp.per + 1) : sp.extra + (x - wide) / sp.per) / W;
         };
         const int first = cta_of(lo);
         s_shared[slot] = make_int4(seg.x, seg.y, first, cta_of(hi - 1) - first + 1);
@@ -479,6 +497,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         pack2<BF16>(a.o.x * inv, a.o.y * inv), pack2<BF16>(a.o.z * inv, a.o.w * inv));
     if (i == 0) p.lse[row] = a.m + log2f(a.l);
   };
+  auto part_of = [&](int c, int slot) {    // of CTA c of this head group, in the workspace
+    return p.parts + (((size_t)group * gridDim.x + c) * 2 + slot) * S::kState;
+  };
   const int n_groups = s_groups;
   for (int e = tid; e < n_groups * items; e += S::kThreads) {
     const int h = e % items / V4, i = e % V4;
@@ -501,7 +522,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (grp.z < 0) {
       finish(s_group_at[e / items], h, i, a);
     } else {
-      float* st = p.parts + (size_t)(blockIdx.x * 2 + grp.z) * S::kState;
+      float* st = part_of(cta, grp.z);
       __stcg(reinterpret_cast<float4*>(st + h * D) + i, a.o);
       if (i == 0) {
         __stcg(st + S::kHeads * D + h, a.m);
@@ -517,7 +538,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const int4 sh = s_shared[tid];
     int merge = 0;
     if (sh.w > 0) {
-      int* n = p.counters + ((size_t)sh.y * batch + sh.x) * p.groups + group;
+      int* n = p.counters + ((size_t)sh.y * batch + sh.x) * gridDim.y + group;
       // the parts that this CTA's threads wrote before the barrier, then the
       // others': cumulative, and weaker (quicker) than __threadfence()
       asm volatile("fence.acq_rel.gpu;" ::: "memory");
@@ -543,7 +564,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const int x = y0 % items, h = x / V4, i = x % V4;
     // of its CTAs the first holds the sequence's start, its second part
     auto part = [&](int k) {
-      return p.parts + (size_t)(((size_t)(sh.z + k) * p.groups + group) * 2 + (k == 0 ? 1 : 0)) * S::kState;
+      return part_of(sh.z + k, k == 0);
     };
     Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     constexpr int kBatch = 8;
@@ -601,8 +622,10 @@ cudaError_t launch(const DecodeParams& p, int nsm, cudaStream_t stream) {
   const cudaError_t e = allow_shared(
       (const void*)kern, S::kPieces * S::kState * 4 + kMaxCacheBatch * 5 + 4, allowed);
   if (e != cudaSuccess) return e;
-  const int per = ctas_per_group(nsm, p.groups);
-  return launch_pdl(kern, dim3(per * p.groups), dim3(S::kThreads), smem, stream, p);
+  const int per_group = ctas_per_group(nsm, p.groups);
+  DecodeParams dp = p;
+  dp.split = decode_split(p.tab.nnz_pages * p.h_kv, per_group, S::kWarps);
+  return launch_pdl(kern, dim3(per_group, p.groups), dim3(S::kThreads), smem, stream, dp);
 }
 
 template <int D, bool BF16>

@@ -155,6 +155,12 @@ struct AppendParams {
   uint64_t turns[64];
 };
 
+// The units of one-token attention over its CTAs: CTA c < ctas has warps c * W
+// and so on, warp w the units from w * per + min(w, extra) on.
+struct DecodeSplit {
+  int ctas, per, extra;
+};
+
 struct DecodeParams {
   const uint16_t* q;
   const uint16_t* pages;
@@ -166,6 +172,7 @@ struct DecodeParams {
   int* counters;            // per (kv head, sequence, head group): its CTAs done; 0 between calls
   int h_q, h_kv, g;
   int groups;               // head groups per kv head (one CTA handles one)
+  DecodeSplit split;        // for a table of nnz_pages entries (set by launch_decode)
   float scale_log2;         // sm_scale * log2(e)
 };
 
