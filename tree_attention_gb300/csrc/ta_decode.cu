@@ -30,6 +30,13 @@
 //   merged in shared memory, and of one that spans CTAs by the last of its
 //   CTAs to finish (a counter), in CTA order, so results do not depend on
 //   timing.
+//
+// Measured (h_q 64, h_kv 8, d 128, bf16, 64 sequences of 16 to 16,384 rows,
+// 880 MB): 133.5 us, 6.6 TB/s, the rate of a plain copy; 4 sequences of 33,000
+// rows: 85.0 us, 6.4 TB/s; one of 4,096 rows (16 kv heads): 11.6 us, of which 2
+// are the chain of loads before the first page and 4 the merges.  16 heads per
+// kv head run at 53 % of the memory rate (two tiles of heads leave 8 warps per
+// SM), 32 heads, whose pages two CTAs read, at 35 %.
 #include <cuda_runtime.h>
 
 #include <atomic>
