@@ -143,6 +143,33 @@ def test_decode_largest_batch():
         ta.PagedCache(s.pool, i32(np.zeros(16386)), i32([0]), i32(np.zeros(16385)), h_q=2)
 
 
+def test_decode_many_pages_per_warp():
+    """A range of 70 pages per warp: page indices are fetched 32 at a time.  The
+    reference is torch in float64 on the GPU; a weighted sum adds up to 70 pages
+    one after the other, 2^-23 each."""
+    n, h = 170_000, 16
+    s = Setup([1], h, h, 64, "bf16", seed=15)
+    pages = -(-n // 16)
+    g = torch.Generator("cuda").manual_seed(3)
+    pool = torch.randn((pages + 4, 2, h, 16, 64), generator=g, device="cuda", dtype=s.dtype)
+    perm = torch.randperm(pages + 4, generator=g, device="cuda")[:pages]
+    c = ta.PagedCache(pool, i32([0, pages]), perm.int(), i32([n - (pages - 1) * 16]), h_q=h)
+    q = s.randn(1, h, 64)
+    out, lse = c.decode(q, 0.125)
+    assert c.device_status() == ta.TA_OK
+    kv = pool[perm].permute(1, 2, 0, 3, 4).reshape(2, h, -1, 64)[:, :, :n]
+    for i in range(h):
+        k, v, x = kv[0, i].double(), kv[1, i].double(), q[0, i].double()
+        sc = (k * x).sum(1) * 0.125
+        w = torch.softmax(sc, 0)[:, None]
+        want, mag = (w * v).sum(0), (w * v.abs()).sum(0)
+        serr = 68 * 2.0 ** -23 * ((k * x).abs().sum(1).max() * 0.125 / np.log(2))
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -16 + 80 * 2.0 ** -23 + 2 * serr) * mag
+        assert ((out[0, i].double() - want).abs() <= tol).all()
+        rl = torch.logsumexp(sc, 0) / np.log(2)
+        assert (lse[0, i].double() - rl).abs() <= serr + 2.0 ** -20 + 2.0 ** -22 * rl.abs()
+
+
 def test_decode_without_any_page():
     pool = torch.full((2, 2, 2, 16, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
     c = ta.PagedCache(pool, i32([0, 0, 0]), i32([]), i32([0, 0]), h_q=4)
@@ -321,6 +348,23 @@ def test_append(name, far):
     got = f64(s.pool)
     same = np.isnan(want) & np.isnan(got)
     assert (same | (np.abs(got - want) <= tol)).all()        # zero tolerance off the new keys
+
+
+def test_append_many_tokens_per_warp():
+    """120,000 tokens of single heads: 40 tokens per warp, looked up 32 at a time."""
+    new = [60001, 1, 0, 47, 59951]
+    s = Setup(np.add(new, [3, 0, 7, 30, 0]), 1, 1, 64, "fp16", seed=16, fill=0.0)
+    q, k, v = append_inputs(s, new, True)
+    ai = np.concatenate([[0], np.cumsum(new)])
+    pos = np.concatenate([np.arange(n) for n in new])
+    before = s.pool.clone()
+    qo = s.cache.append(q, k, v, i32(ai), i32(pos), rope=ta.Rope("half", 64))
+    assert s.cache.device_status() == ta.TA_OK
+    (yq, tq), (yk, tk) = append_reference(s, q, k, pos, "half", 64, 1e4, 1.0, None, None, 0.0)
+    assert (np.abs(f64(qo) - yq) <= tq).all()
+    want = ref.append(f64(before), yk, f64(v), ai, *s.table)
+    tol = ref.append(np.zeros(before.shape), tk, 0 * f64(v), ai, *s.table)
+    assert (np.abs(f64(s.pool) - want) <= tol).all()
 
 
 def test_append_in_place_and_magnitude_and_frequencies():
