@@ -67,8 +67,18 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
   constexpr bool kHalves = LAYOUT == 1;
   __shared__ uint4 s_ring[kAppendThreads / 32][kAppendDepth][2][32];
   __shared__ __align__(16) float2 s_cos_sin[kAppendThreads / 32][D / 2];
+  __shared__ uint64_t s_turns[64];
+  __shared__ uint4 s_weight[2][D / 8];     // of queries, of keys
+  // lanes that index the parameters apart are served one by one: once per CTA
+  static_assert(kAppendThreads >= 64 + D / 4, "a thread per frequency and per vector of weights");
+  if (LAYOUT != 0 && threadIdx.x < 64) s_turns[threadIdx.x] = p.turns[threadIdx.x];
   pdl_wait();
   pdl_trigger();
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + D / 4) {
+    const int i = threadIdx.x - 64;
+    const uint16_t* w = i < D / 8 ? p.q_weight : p.k_weight;
+    if (w != nullptr) s_weight[i / (D / 8)][i % (D / 8)] = reinterpret_cast<const uint4*>(w)[i % (D / 8)];
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % kLanes, lane_row = lane / kLanes;
   // this lane's chunks of 8 elements, such that the lanes of a row hold runs of
@@ -90,7 +100,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
   const int gw = blockIdx.x * (kAppendThreads / 32) + warp;
   const int lo = gw * p.steps_per_warp + min(gw, p.steps_extra);
   int left = p.steps_per_warp + (gw < p.steps_extra);
-  if (left == 0) return;
   int t = lo / all, begin = lo - t * all;
   auto first_step = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? steps_q : steps_q + steps_kv; };
 
@@ -125,13 +134,11 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll 1
-  for (int i = 0; i < kAppendDepth; ++i) fetch();
-
   // Positions and cache slots of the next 32 tokens, one per lane: one chain of
-  // dependent loads for all tokens that a warp comes by, and it runs while the
-  // first rows arrive.
-  const int t_end = (lo + left - 1) / all + 1;
+  // dependent loads for all tokens that a warp comes by.  It goes first: behind
+  // the rows of all warps in the memory's queues each of its loads took 1,500
+  // cycles instead of 700.
+  const int t_end = left > 0 ? (lo + left - 1) / all + 1 : t;
   int m_from = t, m_pos = 0;
   long long m_slot = -1;                   // element offset of a token's K slot, head 0; -1: none
   auto look_up = [&]() {
@@ -165,7 +172,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
     }
     if (m_slot < 0) report_bad_tables(p.error);
   };
-  look_up();
+  if (left > 0) look_up();
+#pragma unroll 1
+  for (int i = 0; i < kAppendDepth; ++i) fetch();
+  __syncthreads();                         // s_turns, s_weight
 
   int ring = 0;
   for (; left > 0; ++t, begin = 0) {
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
         const int j = lane + 32 * i;
         if (j < rd / 2) {
           // the fraction of a turn, exact modulo 1, then one rounding to float32
-          const uint64_t ph = (uint64_t)pos * p.turns[j];
+          const uint64_t ph = (uint64_t)pos * s_turns[j];
           const float half_turns = (float)(int64_t)ph * 0x1p-63f;   // in [-1, 1]
           float sn, cs;
           sincospif(half_turns, &sn, &cs);
@@ -208,14 +218,12 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
       if (kind != 0 && slot < 0) row = rows;           // nothing is written
       // x * own + partner * other, times 1 / rms
       float2 own0[4], own1[4], other0[4], other1[4];
-      const uint16_t* w = kind == 0 ? p.q_weight : p.k_weight;
-      const bool norm = w != nullptr;
+      const bool norm = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) own0[i] = own1[i] = make_float2(1.f, 1.f);
       if (kind < 2) {
         if (norm) {
-          const uint4 a = reinterpret_cast<const uint4*>(w)[c0];
-          const uint4 b = reinterpret_cast<const uint4*>(w)[c1];
+          const uint4 a = s_weight[kind][c0], b = s_weight[kind][c1];
           own0[0] = unpack2<BF16>(a.x), own0[1] = unpack2<BF16>(a.y);
           own0[2] = unpack2<BF16>(a.z), own0[3] = unpack2<BF16>(a.w);
           own1[0] = unpack2<BF16>(b.x), own1[1] = unpack2<BF16>(b.y);
