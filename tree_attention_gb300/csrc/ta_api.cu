@@ -975,17 +975,20 @@ ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
   ap.h_q = dims->h_q;
   ap.h_kv = dims->h_kv;
   ap.eps = norm_eps;
-  // CTAs of 4 warps: one resident wave, or a warp per step (512 / head_dim heads
-  // of one token's q, k or v) where there are fewer
+  // CTAs of 4 warps: one resident wave; fewer, with a warp per step (512 /
+  // head_dim heads of one token's q, k or v), where there is less to do; more,
+  // of kAppendMaxSteps steps per warp, where there is more
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_failure();
   const int rows = 512 / dims->head_dim;
-  const int64_t steps = ta::ceil_div(dims->h_q, rows) + 2 * ta::ceil_div(dims->h_kv, rows);
-  if (total_new * steps > INT32_MAX) return TA_ERR_UNSUPPORTED;
-  const int grid = (int)std::min<int64_t>((int64_t)ta::kAppendCtas * nsm,
-                                          ta::ceil_div(total_new * steps, 4));
-  ap.steps_per_warp = (int)(total_new * steps / (4 * grid));
-  ap.steps_extra = (int)(total_new * steps % (4 * grid));
+  const int64_t steps =
+      total_new * (ta::ceil_div(dims->h_q, rows) + 2 * ta::ceil_div(dims->h_kv, rows));
+  if (steps > INT32_MAX) return TA_ERR_UNSUPPORTED;
+  const int grid = (int)std::max<int64_t>(
+      std::min<int64_t>((int64_t)ta::kAppendCtas * nsm, ta::ceil_div(steps, 4)),
+      ta::ceil_div(steps, 4 * ta::kAppendMaxSteps));
+  ap.steps_per_warp = (int)(steps / (4LL * grid));
+  ap.steps_extra = (int)(steps % (4LL * grid));
   if (rope) {
     ap.rope_layout = rope->layout;
     ap.rotary_dim = rope->rotary_dim;

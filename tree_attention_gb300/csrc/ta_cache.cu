@@ -43,7 +43,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 }
 
 // A step is 32 * 16 elements of one token's queries, keys or values; the steps
-// of all tokens are cut evenly over the warps of one resident wave.  A row (one
+// of all tokens are cut evenly over the warps, a dozen steps each at most.  A row (one
 // head's d elements) belongs to d / 16 lanes; each holds two 16-byte chunks of
 // it, chosen so that both elements of every rotated pair are in one lane.
 //
@@ -57,9 +57,9 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // ends of tokens, and the arithmetic is in pairs of float32.
 //
 // Measured: 9,478 tokens of 64 + 8 + 8 heads of 128, with norms and interleaved
-// pairs (388 MB): 71.4 us, 5.4 TB/s; without norm and rotation 66.3 us, so the
+// pairs (388 MB): 62.1 us, 6.3 TB/s; without norm and rotation 59.9 us, so the
 // memory, in rows of 256 bytes, is what bounds it.  2,048 tokens of 32 + 8 + 8:
-// 13.8 us, bound by the look-ups and the latency of eight steps per warp.
+// 11.5 us, bound by the look-ups and the latency of eight steps per warp.
 template <int D, bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;           // lanes per row
