@@ -282,12 +282,14 @@ typedef struct {
 
 /* Bytes of device workspace each of the calls below needs for these dims (a
  * multiple of 256; 0 on invalid or unsupported dims).  It holds the device
- * status word (tree_attn_device_status) and, for tree_attn_decode_paged, the
- * partial states of sequences that several CTAs share.  tree_attn's workspace
+ * status word (tree_attn_device_status), for tree_attn_decode_paged the partial
+ * states of sequences that several CTAs share, and for tree_attn_copy_pages a
+ * mark per page of the pool.  tree_attn's workspace
  * rules apply: 256-byte aligned, zero-filled once before its first use, left
  * ready for the next call by every call, one workspace per set of calls that
  * may overlap on the GPU (two graphs that may replay at once are such calls).
- * It depends on the dims and the current device's SM count only. */
+ * It depends on the dims and the current device's SM count only; calls that
+ * share one may differ in batch_size and nnz_pages (it holds the largest). */
 size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims);
 
 typedef enum {

@@ -513,7 +513,8 @@ def test_compact_keeps_the_rows_of_a_bad_path(path):
 # --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("n,pages,heads", [(1, 2, (2, 64)), (7, 20, (3, 128)), (300, 700, (1, 64)),
-                                           (1500, 3100, (8, 128)), (5000, 10001, (1, 64))])
+                                           (1500, 3100, (8, 128)), (2040, 4100, (10, 128)),
+                                           (5000, 10001, (1, 64))])
 def test_copy_pages(n, pages, heads):
     s = Setup([16], heads[0], heads[0], heads[1], seed=31, spare=pages - 1)
     s.pool.copy_(torch.randn(s.pool.shape, device="cuda"))
@@ -544,9 +545,10 @@ def test_copy_pages_skips_conflicting_pairs():
     assert s.cache.device_status() == ta.TA_OK and torch.equal(s.pool, want)
 
 
-def test_copy_pages_finds_conflicts_anywhere_in_a_long_list():
+@pytest.mark.parametrize("n", [1900, 5000])
+def test_copy_pages_finds_conflicts_anywhere_in_a_long_list(n):
     rng = np.random.default_rng(33)
-    pages, n = 12000, 5000
+    pages = 12000
     s = Setup([16], 1, 1, 64, seed=33, spare=pages - 1)
     s.pool.copy_(torch.randn(s.pool.shape, device="cuda"))
     p = rng.permutation(pages)
@@ -566,6 +568,9 @@ def test_copy_pages_finds_conflicts_anywhere_in_a_long_list():
     s.cache.copy_pages(i32(src), i32(dst))
     assert s.cache.device_status() == ta.TA_ERR_INVALID_ARGUMENT
     assert torch.equal(s.pool, want)
+    # the next call, on the sound pairs alone, finds nothing of this one
+    s.cache.copy_pages(i32(src[good]), i32(dst[good]))
+    assert s.cache.device_status() == ta.TA_OK and torch.equal(s.pool, want)
 
 
 # --------------------------------------------------------------------------

@@ -889,6 +889,10 @@ ta::PageTable page_table(const ta_cache_dims* d, const int32_t* page_indptr,
                        d->num_pages};
 }
 
+ta::CacheWorkspace cache_layout(const ta_cache_dims* d, int nsm) {
+  return ta::cache_workspace(d->batch_size, d->num_pages, d->h_kv, d->h_q / d->h_kv, d->head_dim, nsm);
+}
+
 unsigned int* error_word(void* workspace) { return &static_cast<WsHeader*>(workspace)->error; }
 
 }  // namespace
@@ -897,8 +901,7 @@ extern "C" {
 
 size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims) {
   if (!cache_dims_valid(dims) || cache_dims_supported(dims) != TA_OK) return 0;
-  return ta::decode_workspace(dims->batch_size, dims->h_kv, dims->h_q / dims->h_kv, dims->head_dim,
-                              std::max(1, sm_count())).total;
+  return cache_layout(dims, std::max(1, sm_count())).total;
 }
 
 ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim, double theta,
@@ -1023,8 +1026,7 @@ ta_status tree_attn_decode_paged(const void* q, const void* pages, const int32_t
   dp.scale_log2 = sm_scale * 1.4426950408889634f;
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_failure();
-  const ta::DecodeWorkspace w =
-      ta::decode_workspace(dims->batch_size, dims->h_kv, dp.g, dims->head_dim, nsm);
+  const ta::CacheWorkspace w = cache_layout(dims, nsm);
   dp.groups = w.groups;
   dp.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_parts);
   dp.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + w.off_counters);
@@ -1088,9 +1090,9 @@ ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int3
   cp.n = n;
   cp.num_pages = dims->num_pages;
   cp.page_lines = dims->h_kv * dims->head_dim / 64;   // 2 planes x 16 slots x 2 bytes
-  // a CTA for every two lines while they fit the GPU at once (5 CTAs per SM)
-  const int grid = (int)std::min<int64_t>(ta::ceil_div((int64_t)n * cp.page_lines, 2), 5LL * nsm);
-  return cuda_status(ta::launch_copy_pages(cp, grid, static_cast<cudaStream_t>(stream)));
+  cp.marks = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(workspace) +
+                                             cache_layout(dims, nsm).off_marks);
+  return cuda_status(ta::launch_copy_pages(cp, nsm, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -473,6 +473,7 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyDepth = 4;        // lines a CTA has in flight
 constexpr int kCopyPairs = 256;      // pairs a CTA checks at a time
 constexpr int kCopyFilter = 4096;    // bits
+constexpr int kCopyMarkedLines = 32768, kCopyMarkedPairs = 2048;   // see launch_copy_pages
 
 // A position in the list of lines: pair k of this round's, line ``line`` of its page.
 struct CopyAt {
@@ -485,16 +486,50 @@ struct CopyAt {
   }
 };
 
+// Marks of the pages that a list of pairs names, in the workspace: how often a
+// page is a destination, and whether it is a source.  They are zero between
+// calls; CLEAR puts them back.
+constexpr unsigned int kMarkSource = 1u << 31;
+template <bool CLEAR>
+__global__ void __launch_bounds__(kCopyThreads) mark_pages_kernel(const CopyParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int stride = gridDim.x * kCopyThreads;
+  for (int64_t i = blockIdx.x * kCopyThreads + threadIdx.x; i < p.n; i += stride) {
+    const int s = p.src[i], d = p.dst[i];
+    if (s >= 0 && s < p.num_pages) {
+      if (CLEAR)
+        p.marks[s] = 0;
+      else
+        atomicOr(p.marks + s, kMarkSource);
+    }
+    if (d >= 0 && d < p.num_pages && s != d) {
+      if (CLEAR)
+        p.marks[d] = 0;
+      else
+        atomicAdd(p.marks + d, 1u);
+    }
+  }
+}
+
 // The n pages are one list of 4 KB lines (a page is h_kv * d / 64 of them: one
 // 16-byte vector per thread each), cut evenly over the CTAs.  Lines pass
 // through a ring in shared memory by cp.async, each thread reading back only
 // what it fetched itself, so nothing waits for anything but its own data: four
-// lines in flight in each of five CTAs keep 80 KB of loads on the way to an
-// SM (ten lines measured the same on large copies and slower on small ones).  Before its first store a CTA looks for its
-// pairs' destinations among all other pairs' sources and destinations, through
-// a bit filter in shared memory (a hit is then looked up exactly), while the
-// first lines arrive.  Measured: 4,096 pages of 64 KB: 94.5 us, 5.7 TB/s, 4 of
-// them the look through the list (a contiguous copy of as much: 86 us).
+// lines in flight in each of five CTAs keep 80 KB of loads on the way to an SM
+// (ten measured the same on large copies and slower on small ones).
+//
+// Before its first store, while the first lines arrive, a CTA finds out which
+// of its pairs must not be copied.  MARKED: from the marks of the list, made by
+// a kernel before this one; CTAs are short (16 lines), as SMs reach the memory
+// at different speeds and equal shares of one wave end with the slowest.  Else,
+// without another launch: it looks for its pairs' destinations among all other
+// pairs' sources and destinations, through a bit filter in shared memory (a hit
+// is then looked up exactly), work that grows with n in every CTA.
+// Measured, marked / not, us: 300 pages of 64 KB 9.0 / 7.3, 1,000 26.1 / 24.3,
+// 4,096 84.9 / 94.0 (6.3 TB/s; a contiguous copy of as much takes torch 86),
+// 16,000 310 / 381; of 8 KB, 1,500 pages 8.1 / 6.5, 16,000 45.5 / 88.
+template <bool MARKED>
 __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyParams p) {
   __shared__ uint4 s_ring[kCopyDepth][kCopyThreads];
   __shared__ unsigned int s_filter[kCopyFilter / 32];
@@ -513,19 +548,21 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
   for (int64_t base = first; base <= last; base += kCopyPairs) {
     const int m = (int)min((int64_t)kCopyPairs, last - base + 1);
     __syncthreads();
-    for (int i = tid; i < kCopyFilter / 32; i += kCopyThreads) s_filter[i] = 0;
+    if (!MARKED)
+      for (int i = tid; i < kCopyFilter / 32; i += kCopyThreads) s_filter[i] = 0;
     int s = 0, d = 0;
+    bool out = false;
     if (tid < m) {
       s = p.src[base + tid];
       d = p.dst[base + tid];
     }
     __syncthreads();
     if (tid < m) {
-      const bool out = s < 0 || s >= p.num_pages || d < 0 || d >= p.num_pages;
+      out = s < 0 || s >= p.num_pages || d < 0 || d >= p.num_pages;
       s_src[tid] = s;
       s_dst[tid] = d;
       s_skip[tid] = out || s == d;
-      if (s != d) atomicOr(&s_filter[(d & (kCopyFilter - 1)) >> 5], 1u << (d & 31));
+      if (!MARKED && s != d) atomicOr(&s_filter[(d & (kCopyFilter - 1)) >> 5], 1u << (d & 31));
       if (out) report_bad_tables(p.error);
     }
     __syncthreads();
@@ -547,17 +584,25 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
     };
     for (int l = 0; l < kCopyDepth; ++l) fetch(l);
     __syncthreads();                   // s_skip is read above and written below
+    if (MARKED) {
+      // one destination, this pair's, and no source
+      if (tid < m && !out && s != d && p.marks[d] != 1) {
+        s_skip[tid] = 1;
+        report_bad_tables(p.error);
+      }
+    } else {
 #pragma unroll 4
-    for (int i = tid; i < p.n; i += kCopyThreads) {
-      const int w[2] = {p.src[i], p.dst[i]};
+      for (int i = tid; i < p.n; i += kCopyThreads) {
+        const int w[2] = {p.src[i], p.dst[i]};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!(s_filter[(w[x] & (kCopyFilter - 1)) >> 5] >> (w[x] & 31) & 1)) continue;
-        for (int k = 0; k < m; ++k)
-          if (s_dst[k] == w[x] && base + k != i && s_src[k] != s_dst[k]) {
-            s_skip[k] = 1;
-            report_bad_tables(p.error);
-          }
+        for (int x = 0; x < 2; ++x) {
+          if (!(s_filter[(w[x] & (kCopyFilter - 1)) >> 5] >> (w[x] & 31) & 1)) continue;
+          for (int k = 0; k < m; ++k)
+            if (s_dst[k] == w[x] && base + k != i && s_src[k] != s_dst[k]) {
+              s_skip[k] = 1;
+              report_bad_tables(p.error);
+            }
+        }
       }
     }
     __syncthreads();
@@ -598,8 +643,24 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   return launch_pdl(compact_kernel, g, dim3(kCompactThreads), 0, stream, p);
 }
 
-cudaError_t launch_copy_pages(const CopyParams& p, int grid, cudaStream_t stream) {
-  return launch_pdl(copy_pages_kernel, dim3(grid), dim3(kCopyThreads), 0, stream, p);
+cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream) {
+  const int64_t lines = (int64_t)p.n * p.page_lines;
+  const dim3 threads(kCopyThreads);
+  // Marking costs two more launches, about 2 us; searching the list costs every
+  // CTA 1 us per 1,000 pairs and long equal shares a tenth of a large copy.
+  if (lines < kCopyMarkedLines && p.n < kCopyMarkedPairs) {
+    const int64_t grid = (lines + 1) / 2 < 5 * nsm ? (lines + 1) / 2 : 5 * nsm;
+    return launch_pdl(copy_pages_kernel<false>, dim3((unsigned)grid), threads, 0, stream, p);
+  }
+  const int64_t blocks = ((int64_t)p.n + kCopyThreads - 1) / kCopyThreads;
+  const dim3 marking((unsigned)(blocks < 4 * nsm ? blocks : 4 * nsm));
+  cudaError_t e = launch_pdl(mark_pages_kernel<false>, marking, threads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (lines + 15) / 16;
+  if (grid > INT32_MAX) grid = INT32_MAX;
+  e = launch_pdl(copy_pages_kernel<true>, dim3((unsigned)grid), threads, 0, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(mark_pages_kernel<true>, marking, threads, 0, stream, p);
 }
 
 }  // namespace ta

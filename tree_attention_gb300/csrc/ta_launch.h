@@ -176,14 +176,15 @@ struct DecodeParams {
   float scale_log2;         // sm_scale * log2(e)
 };
 
-// Workspace of launch_decode: header | parts | counters.  The parts come first,
-// as their size does not follow from the batch: calls with another batch size
-// find the counters in the same place.
-struct DecodeWorkspace {
+// Workspace of the paged-cache calls: header | launch_decode's parts |
+// launch_copy_pages's marks | launch_decode's counters.  What follows from the
+// batch comes last: calls with another batch size find the rest, and the
+// counters, in the same place.
+struct CacheWorkspace {
   int groups;
-  int64_t off_parts, off_counters, total;
+  int64_t off_parts, off_marks, off_counters, total;
 };
-DecodeWorkspace decode_workspace(int batch, int h_kv, int g, int head_dim, int nsm);
+CacheWorkspace cache_workspace(int batch, int num_pages, int h_kv, int g, int head_dim, int nsm);
 
 struct CompactParams {
   uint4* pages;
@@ -202,6 +203,7 @@ struct CopyParams {
   unsigned int* error;
   int n, num_pages;
   int page_lines;                         // 4 KB lines per page
+  unsigned int* marks;                    // [num_pages], zero between calls
 };
 
 // Plan kernel: sequence/tile enumeration, tile classification and LPT
@@ -244,7 +246,7 @@ cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int ns
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
 // pages[dst[i]] = pages[src[i]].
-cudaError_t launch_copy_pages(const CopyParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream);
 
 // Persistent tree-attention kernel.
 template <int D, bool BF16, bool PAGED>
