@@ -328,7 +328,7 @@ ta_status tree_attn_rope_init(ta_rope* rope, int32_t layout, int32_t rotary_dim,
  *                  8, at least the row), so that views of one fused
  *                  projection need no copy
  *   append_indptr  [B+1] int32, from 0 to total_new
- *   positions      [total_new] int32, any value (NULL iff rope is NULL)
+ *   positions      [total_new] int32, any value (may be NULL iff rope is NULL)
  *   q_weight, k_weight  [head_dim] dtype, or NULL for no norm: per head
  *                  x <- x * w / sqrt(mean(x^2) + norm_eps)
  *   norm_eps       finite, >= 0

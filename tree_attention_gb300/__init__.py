@@ -526,7 +526,8 @@ class PagedCache:
     [B+1]``, ``page_values``, ``length_info [B]`` are CUDA tensors, held and not
     copied: their contents may change between calls.  ``h_q`` is the number of
     query heads.  The handle owns a workspace, so calls on it that may overlap
-    on the GPU need handles of their own (``with_table(..., workspace=None)``);
+    on the GPU need handles of their own (``with_table(..., workspace=None)``;
+    ``workspace`` takes another handle's where that is large enough);
     every call is asynchronous on ``stream`` (default: torch's current
     stream), and ``device_status`` reports inconsistent tables."""
 

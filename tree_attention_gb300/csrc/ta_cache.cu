@@ -23,7 +23,7 @@ __device__ __forceinline__ void report_bad_tables(unsigned int* error) {
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
-constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight
+constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight (3 and 8 measured the same)
 
 // The largest b in [0, batch) with indptr[b] <= t, by one warp: 32 probes cut
 // the range by 33 each round, so 1,000 sequences take two round trips to
@@ -43,9 +43,10 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 }
 
 // A step is 32 * 16 elements of one token's queries, keys or values; the steps
-// of all tokens are cut evenly over the warps, a dozen steps each at most.  A row (one
-// head's d elements) belongs to d / 16 lanes; each holds two 16-byte chunks of
-// it, chosen so that both elements of every rotated pair are in one lane.
+// of all tokens are cut evenly over the warps, a dozen steps each at most.  A
+// row (one head's d elements) belongs to d / 16 lanes; each holds two 16-byte
+// chunks of it, chosen so that both elements of every rotated pair are in one
+// lane.
 //
 // Bound by memory: 4 bytes of traffic per element against the memory's rate
 // leave a lane some 200 instructions for its 16 elements of a step, and the
