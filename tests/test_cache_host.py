@@ -243,3 +243,48 @@ def test_copy_refusals(lib, kw):
 
 def test_copy_of_nothing(lib):
     assert _copy(lib, n=0, src=None, dst=None) == ta.TA_OK
+
+
+# --------------------------------------------------------------------------
+# the compiled argument checks of PagedCache (on CPU tensors: all refused)
+# --------------------------------------------------------------------------
+
+def _handle(d):
+    import torch
+    z = torch.zeros(4, dtype=torch.int32)
+    pages = torch.zeros((12, 2, 2, 16, 128), dtype=torch.bfloat16)
+    return ta._compiled().handle(ctypes.addressof(d), pages, z, torch.zeros(6, dtype=torch.int32),
+                                 z[:3], torch.zeros(256, dtype=torch.uint8))
+
+
+def test_binding_refuses_what_is_not_on_the_handles_device(lib):
+    import torch
+    b, d = ta._compiled(), _dims()
+    h = _handle(d)
+    q = torch.zeros((3, 8, 128), dtype=torch.bfloat16)
+    lse = torch.zeros((3, 8))
+    with pytest.raises(ValueError, match="q must be"):
+        b.decode(h, q, 0.1, q, lse, None)
+    kv = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+    z = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="must be"):
+        b.append(h, q, kv, kv, z, None, None, None, None, 1e-6, q, None)
+    with pytest.raises(ValueError, match="must be"):
+        b.compact(h, z, z, z, z, z, z, z, z, None)
+    with pytest.raises(ValueError, match="must be"):
+        b.copy_pages(h, z, z, None)
+
+
+@pytest.mark.parametrize("call", [
+    lambda b, h: b.decode(h, 1, 0.1, None, None, None),
+    lambda b, h: b.copy_pages(h, None, None, None),
+    lambda b, h: b.append(h, "q", None, None, None, None, None, None, None, 0.0, None, None),
+    lambda b, h: b.decode(h),
+    lambda b, h: b.compact(),
+    lambda b, h: b.handle(1),
+    lambda b, h: b.handle(1, 2, 3, 4, 5, 6),
+    lambda b, h: b.decode(None, 1, 0.1, None, None, None),
+])
+def test_binding_refuses_what_is_no_tensor_or_no_handle(lib, call):
+    with pytest.raises(ValueError):
+        call(ta._compiled(), _handle(_dims()))

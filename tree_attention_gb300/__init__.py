@@ -2,8 +2,9 @@
 library (C ABI in ``include/tree_attn.h``).
 
 The binding only marshals arguments: tensors are passed to the C entry points
-as raw device pointers, every step of the computation runs in the library's
-CUDA kernels, and there is no CPU fallback.  If the library has not been
+as raw device pointers (by ctypes, or, for the calls of ``PagedCache``, by the
+extension module ``_binding``), every step of the computation runs in the
+library's CUDA kernels, and there is no CPU fallback.  If the library has not been
 built, importing works but every call raises ``RuntimeError``.
 
 The operation is ``batch_tree_attn`` of the page "tree_attn.py"
@@ -508,14 +509,24 @@ class Rope:
                                        float(magnitude), table)
         if st != TA_OK:
             raise TreeAttnError(st, "tree_attn_rope_init")
-        self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
-# torch's current device and stream.  The direct ways to them, where this torch
-# has them, take 0.1 us each instead of 0.3 and 2.8.
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
-               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+_binding_module = None
+
+
+def _compiled():
+    """The extension module with the compiled argument checks of PagedCache."""
+    global _binding_module
+    if _binding_module is None:
+        lib()   # raises if it is not built
+        import importlib
+        try:
+            _binding_module = importlib.import_module("tree_attention_gb300._binding")
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built; run tree_attention_gb300.build.build() "
+                               "or __graft_entry__.build()") from e
+    return _binding_module
 
 
 class PagedCache:
@@ -563,17 +574,11 @@ class PagedCache:
                 torch.cuda.current_stream(self._dev).synchronize()
         _check_dev("workspace", workspace)
         self.workspace = workspace
-        # what the calls pass every time
-        L = lib()
-        self._append, self._decode = L.tree_attn_append_paged, L.tree_attn_decode_paged
-        self._compact, self._copy = L.tree_attn_compact_paged, L.tree_attn_copy_pages
-        self._b, self._b1 = (self.batch_size,), (self.batch_size + 1,)
-        self._nnz = (page_values.numel(),)
-        self._q_shape = (self.batch_size, self.h_q, self.head_dim)
-        self._table = (page_indptr.data_ptr(), page_values.data_ptr(), length_info.data_ptr())
-        self._pages = pages.data_ptr()
-        self._tail = (ctypes.byref(self.dims), workspace.data_ptr(),
-                      workspace.numel() * workspace.element_size())
+        # the addresses of these tensors are what the calls pass, so they stay
+        self._held = (pages, page_indptr, page_values, length_info, workspace)
+        self._binding = _compiled()
+        self._handle = self._binding.handle(ctypes.addressof(self.dims), pages, page_indptr,
+                                            page_values, length_info, workspace)
 
     def with_table(self, page_indptr, page_values, length_info, workspace="same"):
         """A handle on the same pool with another page table (as ``compact``
@@ -581,33 +586,6 @@ class PagedCache:
         unless given another one (None: a new one)."""
         return PagedCache(self.pages, page_indptr, page_values, length_info, self.h_q,
                           self.workspace if isinstance(workspace, str) else workspace)
-
-    def _ptr(self, name, t, dtype, shape):
-        """Address of a contiguous tensor argument, checked."""
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == self._dev
-                and t.is_contiguous()):
-            return t.data_ptr()
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} on {self.device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         + ("" if t.is_contiguous() else ", not contiguous"))
-
-    def _rows(self, name, t, shape):
-        """Address and token stride of a [tokens, heads, d] argument."""
-        if t.dtype is not self.dtype or t.shape != shape or t.get_device() != self._dev:
-            raise ValueError(f"{name} must be {self.dtype} {tuple(shape)} on {self.device}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-        token, head, one = t.stride()
-        n, heads, d = shape
-        if one != 1 or (head != d and heads > 1):
-            raise ValueError(f"the rows of one token must be contiguous in {name}")
-        return t.data_ptr(), token if n > 1 else heads * d
-
-    def _stream(self, stream):
-        if _current_device() != self._dev:
-            raise ValueError(f"the cache is on {self.device}, which is not the current device")
-        if stream is None:
-            return _raw_stream(self._dev)
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def _empty(self, shape, dtype, stream):
         """A new output, from the pool of the stream that the call runs on."""
@@ -623,24 +601,13 @@ class PagedCache:
         norm (where a weight is given) and the rotation (with ``rope``, at
         ``positions [tokens]``).  q, k, v are ``[tokens, heads, d]`` and may be
         views of one fused projection."""
-        n, d = q.shape[0], self.head_dim
-        qp, qs = self._rows("q", q, (n, self.h_q, d))
-        kp, ks = self._rows("k", k, (n, self.h_kv, d))
-        vp, vs = self._rows("v", v, (n, self.h_kv, d))
         if rope is not None and positions is None:
             raise ValueError("rope needs positions")
-        st = self._stream(stream)
         if q_out is None:
-            q_out = self._empty((n, self.h_q, d), self.dtype, stream)
-        ptr, i32 = self._ptr, torch.int32
-        st = self._append(
-            qp, qs, kp, ks, vp, vs, n,
-            ptr("append_indptr", append_indptr, i32, self._b1),
-            None if positions is None else ptr("positions", positions, i32, (n,)),
-            None if q_weight is None else ptr("q_weight", q_weight, self.dtype, (d,)),
-            None if k_weight is None else ptr("k_weight", k_weight, self.dtype, (d,)),
-            norm_eps, None if rope is None else rope.ref, self._pages,
-            *self._table, ptr("q_out", q_out, self.dtype, (n, self.h_q, d)), *self._tail, st)
+            q_out = self._empty((q.shape[0], self.h_q, self.head_dim), self.dtype, stream)
+        st = self._binding.append(self._handle, q, k, v, append_indptr, positions,
+                                  None if rope is None else rope.address, q_weight, k_weight,
+                                  norm_eps, q_out, stream)
         if st != TA_OK:
             raise TreeAttnError(st, "tree_attn_append_paged")
         return q_out
@@ -648,16 +615,11 @@ class PagedCache:
     def decode(self, q, sm_scale: float, out=None, lse=None, stream=None):
         """Attention of one new token per sequence, ``q [B, h_q, d]``, over all
         its kv rows; returns ``out`` and the base-2 ``lse [B, h_q]``."""
-        shape = self._q_shape
-        st = self._stream(stream)
-        qp = self._ptr("q", q, self.dtype, shape)
         if out is None:
-            out = self._empty(shape, self.dtype, stream)
+            out = self._empty((self.batch_size, self.h_q, self.head_dim), self.dtype, stream)
         if lse is None:
-            lse = self._empty(shape[:2], torch.float32, stream)
-        st = self._decode(
-            qp, self._pages, *self._table, self._ptr("out", out, self.dtype, shape),
-            self._ptr("lse", lse, torch.float32, shape[:2]), sm_scale, *self._tail, st)
+            lse = self._empty((self.batch_size, self.h_q), torch.float32, stream)
+        st = self._binding.decode(self._handle, q, sm_scale, out, lse, stream)
         if st != TA_OK:
             raise TreeAttnError(st, "tree_attn_decode_paged")
         return out, lse
@@ -670,10 +632,9 @@ class PagedCache:
         behind the prefix.  Returns the new ``page_indptr, page_values,
         length_info`` (for ``with_table``), the freed pages and their number
         ``[1]``, all on the device."""
-        st = self._stream(stream)
-        ptr, i32, b, b1, nnz = self._ptr, torch.int32, self._b, self._b1, self._nnz
+        i32, b, nnz = torch.int32, self.batch_size, self.page_values.numel()
         if new_page_indptr is None:
-            new_page_indptr = self._empty(b1, i32, stream)
+            new_page_indptr = self._empty(b + 1, i32, stream)
         if new_page_values is None:
             new_page_values = self._empty(nnz, i32, stream)
         if new_length_info is None:
@@ -681,17 +642,10 @@ class PagedCache:
         if freed_pages is None:
             freed_pages = self._empty(nnz, i32, stream)
         if num_freed is None:
-            num_freed = self._empty((1,), i32, stream)
-        n = accept_nodes.numel()
-        st = self._compact(
-            self._pages, *self._table, ptr("mn_indptr", mn_indptr, i32, b1),
-            ptr("accept_indptr", accept_indptr, i32, b1),
-            ptr("accept_nodes", accept_nodes, i32, (n,)), n,
-            ptr("new_page_indptr", new_page_indptr, i32, b1),
-            ptr("new_page_values", new_page_values, i32, nnz),
-            ptr("new_length_info", new_length_info, i32, b),
-            ptr("freed_pages", freed_pages, i32, nnz), ptr("num_freed", num_freed, i32, (1,)),
-            *self._tail, st)
+            num_freed = self._empty(1, i32, stream)
+        st = self._binding.compact(self._handle, mn_indptr, accept_indptr, accept_nodes,
+                                   new_page_indptr, new_page_values, new_length_info, freed_pages,
+                                   num_freed, stream)
         if st != TA_OK:
             raise TreeAttnError(st, "tree_attn_compact_paged")
         return new_page_indptr, new_page_values, new_length_info, freed_pages, num_freed
@@ -699,11 +653,7 @@ class PagedCache:
     def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
         """``pages[dst_pages[i]] = pages[src_pages[i]]``; no destination may be
         another pair's source or destination."""
-        st = self._stream(stream)
-        n = (src_pages.numel(),)
-        st = self._copy(
-            self._pages, self._ptr("src_pages", src_pages, torch.int32, n),
-            self._ptr("dst_pages", dst_pages, torch.int32, n), n[0], *self._tail, st)
+        st = self._binding.copy_pages(self._handle, src_pages, dst_pages, stream)
         if st != TA_OK:
             raise TreeAttnError(st, "tree_attn_copy_pages")
 

@@ -1,10 +1,13 @@
-"""Build step for the sm_103a shared library ``libtreeattn.so``.
+"""Build step for the sm_103a shared library ``libtreeattn.so`` and the extension
+module ``_binding.so``.
 
 Compiles the CUDA translation units under ``csrc/`` in parallel with nvcc
 for ``sm_103a`` only and links them (with the static CUDA runtime) into
 ``tree_attention_gb300/libtreeattn.so``.  The driver API is reached at run
 time through ``cudaGetDriverEntryPointByVersion``, so the library loads on a
-machine without a GPU driver.
+machine without a GPU driver.  The extension module (the compiled argument
+checks of ``PagedCache``) is one C++ file against torch's and Python's headers,
+linked to that library.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libtreeattn.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = ["ta_api.cu", "ta_plan.cu", "ta_attn.cu", "ta_merge.cu", "ta_cache.cu", "ta_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -40,10 +45,42 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _torch_dir(name: str) -> str:
+    import torch
+    return os.path.join(os.path.dirname(torch.__file__), name)
+
+
+def _compile_binding() -> str:
+    import torch
+    inc = _torch_dir("include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    obj = os.path.join(BUILD_DIR, "ta_binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+          "-c", os.path.join(CSRC, "ta_binding.cpp"), "-o", obj], "g++ for ta_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING_PATH + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libtreeattn.so", "-Wl,-rpath,$ORIGIN",
+          "-L", _torch_dir("lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+         "linking _binding.so")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -63,14 +100,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH
 
 
