@@ -171,15 +171,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (tokens > INT32_MAX) throw std::invalid_argument("too many tokens");
     const ta_rope* rope = given(a[6]) ? static_cast<const ta_rope*>(PyLong_AsVoidPtr(a[6])) : nullptr;
     if (PyErr_Occurred()) throw PythonError();
-    return (long)tree_attn_append_paged(
-        q, qs, k, ks, v, vs, (int32_t)tokens,
-        ints(h, "append_indptr", a[4], h.dims.batch_size + 1),
-        given(a[5]) ? ints(h, "positions", a[5], tokens) : nullptr,
-        given(a[7]) ? address(h, "q_weight", a[7], h.dtype, {d}) : nullptr,
-        given(a[8]) ? address(h, "k_weight", a[8], h.dtype, {d}) : nullptr, number(a[9]), rope,
-        h.pages, h.indptr, h.values, h.length,
-        address(h, "q_out", a[10], h.dtype, {tokens, h.dims.h_q, d}), &h.dims, h.workspace,
-        h.workspace_bytes, stream_of(h, a[11]));
+    const int32_t* indptr = ints(h, "append_indptr", a[4], h.dims.batch_size + 1);
+    const int32_t* positions = given(a[5]) ? ints(h, "positions", a[5], tokens) : nullptr;
+    const void* qw = given(a[7]) ? address(h, "q_weight", a[7], h.dtype, {d}) : nullptr;
+    const void* kw = given(a[8]) ? address(h, "k_weight", a[8], h.dtype, {d}) : nullptr;
+    const float eps = number(a[9]);
+    void* q_out = address(h, "q_out", a[10], h.dtype, {tokens, h.dims.h_q, d});
+    return (long)tree_attn_append_paged(q, qs, k, ks, v, vs, (int32_t)tokens, indptr, positions, qw,
+                                        kw, eps, rope, h.pages, h.indptr, h.values, h.length, q_out,
+                                        &h.dims, h.workspace, h.workspace_bytes, stream_of(h, a[11]));
   });
 }
 
@@ -188,11 +188,12 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 6, [&] {
     const Handle& h = handle(a[0]);
     const int64_t b = h.dims.batch_size, hq = h.dims.h_q, d = h.dims.head_dim;
-    return (long)tree_attn_decode_paged(
-        address(h, "q", a[1], h.dtype, {b, hq, d}), h.pages, h.indptr, h.values, h.length,
-        address(h, "out", a[3], h.dtype, {b, hq, d}),
-        address<float>(h, "lse", a[4], at::kFloat, {b, hq}), number(a[2]), &h.dims, h.workspace,
-        h.workspace_bytes, stream_of(h, a[5]));
+    const void* q = address(h, "q", a[1], h.dtype, {b, hq, d});
+    const float sm_scale = number(a[2]);
+    void* out = address(h, "out", a[3], h.dtype, {b, hq, d});
+    float* lse = address<float>(h, "lse", a[4], at::kFloat, {b, hq});
+    return (long)tree_attn_decode_paged(q, h.pages, h.indptr, h.values, h.length, out, lse, sm_scale,
+                                        &h.dims, h.workspace, h.workspace_bytes, stream_of(h, a[5]));
   });
 }
 
@@ -204,13 +205,17 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t b = h.dims.batch_size, nnz = h.dims.nnz_pages;
     const int64_t accepted = length("accept_nodes", a[3], 1);
     if (accepted > INT32_MAX) throw std::invalid_argument("too many accepted nodes");
-    return (long)tree_attn_compact_paged(
-        h.pages, h.indptr, h.values, h.length, ints(h, "mn_indptr", a[1], b + 1),
-        ints(h, "accept_indptr", a[2], b + 1), ints(h, "accept_nodes", a[3], accepted),
-        (int32_t)accepted, ints(h, "new_page_indptr", a[4], b + 1),
-        ints(h, "new_page_values", a[5], nnz), ints(h, "new_length_info", a[6], b),
-        ints(h, "freed_pages", a[7], nnz), ints(h, "num_freed", a[8], 1), &h.dims, h.workspace,
-        h.workspace_bytes, stream_of(h, a[9]));
+    const int32_t* mn = ints(h, "mn_indptr", a[1], b + 1);
+    const int32_t* accept = ints(h, "accept_indptr", a[2], b + 1);
+    const int32_t* nodes = ints(h, "accept_nodes", a[3], accepted);
+    int32_t* indptr = ints(h, "new_page_indptr", a[4], b + 1);
+    int32_t* values = ints(h, "new_page_values", a[5], nnz);
+    int32_t* lengths = ints(h, "new_length_info", a[6], b);
+    int32_t* freed = ints(h, "freed_pages", a[7], nnz);
+    int32_t* num_freed = ints(h, "num_freed", a[8], 1);
+    return (long)tree_attn_compact_paged(h.pages, h.indptr, h.values, h.length, mn, accept, nodes,
+                                         (int32_t)accepted, indptr, values, lengths, freed, num_freed,
+                                         &h.dims, h.workspace, h.workspace_bytes, stream_of(h, a[9]));
   });
 }
 
@@ -220,9 +225,10 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Handle& h = handle(a[0]);
     const int64_t pairs = length("src_pages", a[1], 1);
     if (pairs > INT32_MAX) throw std::invalid_argument("too many pages");
-    return (long)tree_attn_copy_pages(h.pages, ints(h, "src_pages", a[1], pairs),
-                                      ints(h, "dst_pages", a[2], pairs), (int32_t)pairs, &h.dims,
-                                      h.workspace, h.workspace_bytes, stream_of(h, a[3]));
+    const int32_t* src = ints(h, "src_pages", a[1], pairs);
+    const int32_t* dst = ints(h, "dst_pages", a[2], pairs);
+    return (long)tree_attn_copy_pages(h.pages, src, dst, (int32_t)pairs, &h.dims, h.workspace,
+                                      h.workspace_bytes, stream_of(h, a[3]));
   });
 }
 
