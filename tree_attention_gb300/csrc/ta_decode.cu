@@ -32,9 +32,9 @@
 //   timing.
 //
 // Measured (h_q 64, h_kv 8, d 128, bf16, 64 sequences of 16 to 16,384 rows,
-// 880 MB): 133.5 us, 6.6 TB/s, the rate of a plain copy; 4 sequences of 33,000
-// rows: 85.0 us, 6.4 TB/s; one of 4,096 rows (16 kv heads): 11.6 us, of which 2
-// are the chain of loads before the first page and 4 the merges.  16 heads per
+// 880 MB): 131.5 us, 6.7 TB/s, the rate of a plain copy; 4 sequences of 33,000
+// rows: 83.2 us, 6.5 TB/s; one of 4,096 rows (16 kv heads): 11.1 us, of which 2
+// are the chain of loads before the first page and 3 the merges.  16 heads per
 // kv head run at 53 % of the memory rate (two tiles of heads leave 8 warps per
 // SM), 32 heads, whose pages two CTAs read, at 35 %.
 #include <cuda_runtime.h>
@@ -546,22 +546,26 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     int merge = 0;
     if (sh.w > 0) {
       int* n = p.counters + ((size_t)sh.y * batch + sh.x) * gridDim.y + group;
-      // the parts that this CTA's threads wrote before the barrier, then the
-      // others': cumulative, and weaker (quicker) than __threadfence()
-      asm volatile("fence.acq_rel.gpu;" ::: "memory");
-      merge = atomicAdd(n, 1) == sh.w - 1;
-      asm volatile("fence.acq_rel.gpu;" ::: "memory");
+      // releases the parts that this CTA's threads wrote before the barrier and
+      // acquires the others' (fences around a plain atomic took 0.3 us more)
+      int before;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                   : "=r"(before)
+                   : "l"(n)
+                   : "memory");
+      merge = before == sh.w - 1;
       if (merge) *n = 0;
     }
     s_merge[tid] = merge;
   }
   __syncthreads();
   if (!s_merge[0] && !s_merge[1]) return;
-  // The threads share the parts of an element where there are more threads than
-  // elements, and each has several parts' loads in flight.
+  // A thread has kBatch parts of an element in flight at once; more parts go to
+  // more threads, as far as there are any.
+  constexpr int kBatch = 8;
   const int most = max(1, S::kThreads / (items * (s_merge[0] + s_merge[1])));
-  const int share0 = s_merge[0] ? min(s_shared[0].w, most) : 0;
-  const int share1 = s_merge[1] ? min(s_shared[1].w, most) : 0;
+  const int share0 = s_merge[0] ? min((s_shared[0].w + kBatch - 1) / kBatch, most) : 0;
+  const int share1 = s_merge[1] ? min((s_shared[1].w + kBatch - 1) / kBatch, most) : 0;
   float* s_ml = s_state;                                                // [share][items][2]
   float4* s_o = reinterpret_cast<float4*>(s_state + 2 * S::kThreads);   // [share][items]
   for (int e = tid; e < items * (share0 + share1); e += S::kThreads) {
@@ -574,7 +578,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       return part_of(sh.z + k, k == 0);
     };
     Acc a{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    constexpr int kBatch = 8;
     for (int k0 = y0 / items; k0 < sh.w; k0 += share * kBatch) {
       float pm[kBatch], pl[kBatch];
       float4 y[kBatch];
