@@ -23,7 +23,7 @@ __device__ __forceinline__ void report_bad_tables(unsigned int* error) {
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
-constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight (3 and 8 measured the same)
+constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight (3: 3 % slower, 8 no faster)
 
 // The largest b in [0, batch) with indptr[b] <= t, by one warp: 32 probes cut
 // the range by 33 each round, so 1,000 sequences take two round trips to
@@ -105,29 +105,31 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
   auto first_step = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? steps_q : steps_q + steps_kv; };
 
   // The fetches: their token, step, and of the step's rows this lane's.
-  int f_left = left, f_t = t, f_step = begin, f_next_kind = begin, f_row = 0, f_rows = 0, f_slot = 0;
-  const uint16_t* f_src = nullptr;
+  int f_left = left, f_t = t, f_step = begin, f_next_kind = begin;
+  int f_rows = 0;                          // rows from this lane's on to the kind's last
+  const uint16_t* f_src = nullptr;         // this lane's first chunk
+  const int apart = 8 * (c1 - c0);         // its second, from there
+  const uint32_t ring0 = smem_u32(&s_ring[warp][0][0][lane]);
+  uint32_t f_to = ring0;
   auto fetch = [&]() {
     if (f_left > 0) {
       --f_left;
       if (f_step == f_next_kind) {         // the first step, or the first of another kind
         const int kind = f_step < steps_q ? 0 : f_step < steps_q + steps_kv ? 1 : 2;
-        f_row = (f_step - first_step(kind)) * kRows + lane_row;
-        f_rows = kind == 0 ? p.h_q : p.h_kv;
-        f_src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + f_row * D +
+        const int row = (f_step - first_step(kind)) * kRows + lane_row;
+        f_rows = (kind == 0 ? p.h_q : p.h_kv) - row;
+        f_src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + row * D + 8 * c0 +
                 f_t * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
         f_next_kind = kind == 2 ? 0 : first_step(kind + 1);
       }
-      if (f_row < f_rows) {
-        const uint32_t to = smem_u32(&s_ring[warp][f_slot][0][lane]);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(f_src + 8 * c0)
-                     : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(f_src + 8 * c1)
+      if (f_rows > 0) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(f_to), "l"(f_src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(f_to + 512), "l"(f_src + apart)
                      : "memory");
       }
-      f_row += kRows;
+      f_rows -= kRows;
       f_src += kRows * D;
-      f_slot = f_slot + 1 == kAppendDepth ? 0 : f_slot + 1;
+      f_to = f_to == ring0 + (kAppendDepth - 1) * 1024 ? ring0 : f_to + 1024;
       if (++f_step == all) {
         f_step = 0;
         ++f_t;
