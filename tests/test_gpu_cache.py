@@ -708,6 +708,60 @@ def test_a_speculative_step_and_a_decoding_step():
     check_decode(ref_s, qd, od, ld, d ** -0.5)
 
 
+def test_two_streams_with_workspaces_of_their_own():
+    """The same cache read by two handles at once: each has its own workspace."""
+    s = Setup([7000, 3, 900, 0, 2500], 8, 2, 128, seed=62, fill=0.0)
+    q = s.randn(5, 8, 128)
+    want = [t.clone() for t in s.cache.decode(q, 0.1)]
+    other = s.cache.with_table(*[i32(x) for x in s.table], workspace=None)
+    assert other.workspace.data_ptr() != s.cache.workspace.data_ptr()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[(torch.empty_like(want[0]), torch.empty_like(want[1])) for _ in range(30)]
+            for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for c, st, o in zip((s.cache, other), streams, outs):
+            c.decode(q, 0.1, *o[i], stream=st)
+    torch.cuda.synchronize()
+    for o in outs:
+        for out, lse in o:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert s.cache.device_status() == ta.TA_OK and other.device_status() == ta.TA_OK
+
+
+def test_a_captured_decoding_step_follows_its_inputs():
+    """append and decode captured once: tokens, positions and lengths change in
+    place between replays, and each replay does what the eager calls do."""
+    s = Setup([100, 40, 33], 8, 2, 64, "bf16", seed=63, fill=0.0)
+    eager = Setup([100, 40, 33], 8, 2, 64, "bf16", seed=63, fill=0.0)
+    x = s.randn(3, 12, 64)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    ai, pos, rope = i32([0, 1, 2, 3]), i32([0, 0, 0]), ta.Rope("half", 64)
+    s.cache.length_info.copy_(i32([1, 1, 1]))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        s.cache.decode(s.cache.append(q, k, v, ai, pos, rope=rope), 0.125)
+    torch.cuda.synchronize()
+    s.pool.copy_(eager.pool)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qo = s.cache.append(q, k, v, ai, pos, rope=rope)
+        out, lse = s.cache.decode(qo, 0.125)
+    for step in range(1, 5):
+        lens = i32([3 + step, 7 + step, step])
+        x.copy_(s.randn(3, 12, 64))
+        pos.copy_(i32([99 + step, 1000 * step, 32 + step]))
+        s.cache.length_info.copy_(lens)
+        graph.replay()
+        eager.cache.length_info.copy_(lens)
+        e_qo = eager.cache.append(q, k, v, ai, pos, rope=rope)
+        e_out, e_lse = eager.cache.decode(e_qo, 0.125)
+        torch.cuda.synchronize()
+        assert torch.equal(qo, e_qo) and torch.equal(out, e_out) and torch.equal(lse, e_lse)
+        assert torch.equal(s.pool, eager.pool)
+    assert s.cache.device_status() == ta.TA_OK
+
+
 def test_calls_on_a_side_stream():
     """Work queued on another stream than torch's current one keeps its order."""
     s = Setup([500, 60], 8, 2, 128, seed=61, fill=0.0)

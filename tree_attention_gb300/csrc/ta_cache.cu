@@ -58,9 +58,9 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // ends of tokens, and the arithmetic is in pairs of float32.
 //
 // Measured: 9,478 tokens of 64 + 8 + 8 heads of 128, with norms and interleaved
-// pairs (388 MB): 62.1 us, 6.3 TB/s; without norm and rotation 59.9 us, so the
+// pairs (388 MB): 61.3 us, 6.3 TB/s; without norm and rotation 59.9 us, so the
 // memory, in rows of 256 bytes, is what bounds it.  2,048 tokens of 32 + 8 + 8:
-// 11.5 us, bound by the look-ups and the latency of eight steps per warp.
+// 11.2 us, bound by the look-ups and the latency of eight steps per warp.
 template <int D, bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;           // lanes per row
