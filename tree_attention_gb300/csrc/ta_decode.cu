@@ -32,7 +32,7 @@
 //   timing.
 //
 // Measured (h_q 64, h_kv 8, d 128, bf16, 64 sequences of 16 to 16,384 rows,
-// 880 MB): 131.5 us, 6.7 TB/s, the rate of a plain copy; 4 sequences of 33,000
+// 880 MB): 131 to 134 us, 6.6 TB/s, the rate of a plain copy; 4 sequences of 33,000
 // rows: 83.2 us, 6.5 TB/s; one of 4,096 rows (16 kv heads): 11.1 us, of which 2
 // are the chain of loads before the first page and 3 the merges.  16 heads per
 // kv head run at 53 % of the memory rate (two tiles of heads leave 8 warps per
