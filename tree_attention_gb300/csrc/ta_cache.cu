@@ -357,11 +357,12 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactParams& p, int i)
 // reads what it has overwritten.
 // CTA (b, 0) also writes sequence b's part of the new table, whose place it
 // finds by summing the pages the sequences before it keep.
-// A few rows per sequence: bound by the chain of dependent loads (tables,
-// nodes, pages, rows), so the independent ones are issued together and the
-// registers leave room for four CTAs per SM.  Measured: 512 sequences, paths of
-// up to 24 nodes, 8 kv heads of 128: 12.2 us (16.5 with 16 rows in flight per
-// thread and two CTAs per SM), 4.1 TB/s; 32 sequences: 3.8 us.
+// Few sequences: bound by the chain of dependent loads (tables, nodes, pages,
+// rows), so the independent ones are issued together; many: by the memory, as a
+// row is pieces of d * 2 bytes a page's head apart.  The registers leave room for
+// four CTAs per SM.  Measured: 512 sequences, paths of up to 24 nodes, 8 kv heads
+// of 128: 12.2 us (16.5 with 16 rows in flight per thread and two CTAs per SM),
+// 4.1 TB/s; 32 sequences: 3.8 us.
 __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const CompactParams p) {
   __shared__ long long s_src[kCompactThreads], s_dst[kCompactThreads];
   __shared__ int s_sum[kCompactThreads / 32];
