@@ -232,6 +232,22 @@ def test_decode_is_repeatable_and_leaves_its_workspace_ready():
     assert s.cache.workspace[:256].eq(ws[:256]).all()
 
 
+@pytest.mark.parametrize("kv,h_q,h_kv,d", [([32768], 32, 8, 128), ([16384, 16384], 32, 8, 128),
+                                           ([9000], 8, 2, 128), ([20000, 9000], 8, 4, 64)])
+def test_decode_does_not_depend_on_which_cta_ends_last(kv, h_q, h_kv, d):
+    """Sequences over dozens of CTAs, whose borders with the next sequence or kv
+    head lie within a CTA: it may be the last of one of its two or of both."""
+    s = Setup(kv, h_q, h_kv, d, seed=17, fill=0.0)
+    q = s.randn(len(kv), h_q, d)
+    out, lse = [t.clone() for t in s.cache.decode(q, d ** -0.5)]
+    differ = 0
+    for _ in range(300):
+        a, b = s.cache.decode(q, d ** -0.5)
+        differ += (a != out).any().long() + (b != lse).any().long()
+    assert int(differ) == 0
+    check_decode(s, q, out, lse, d ** -0.5)
+
+
 def test_decode_follows_a_changed_table():
     """One handle, lengths that change in place between calls (a decoding loop),
     also under a captured graph."""

@@ -93,7 +93,7 @@ struct Shape {
   static constexpr int kState = kHeads * D + 2 * kHeads;   // floats: O, then m, then l
   static constexpr int kPieces = 2 * kWarps;               // parts a CTA can hold
   static_assert(kPieces <= 32, "one lane per part");
-  static_assert(kPieces * kState >= 6 * kThreads, "the last merge's sums fit");
+  static_assert(kPieces * kState >= 12 * kThreads, "the last merge's sums of two sequences fit");
 };
 
 // U units over up to ``grid`` CTAs of W warps, a unit per warp at least.
@@ -561,13 +561,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   __syncthreads();
   if (!s_merge[0] && !s_merge[1]) return;
   // A thread has kBatch parts of an element in flight at once; more parts go to
-  // more threads, as far as there are any.
+  // more threads, as far as one sequence's elements leave any: whether this CTA
+  // merges one sequence or both depends on which CTAs end last, and the order of
+  // the sums must not.
   constexpr int kBatch = 8;
-  const int most = max(1, S::kThreads / (items * (s_merge[0] + s_merge[1])));
+  const int most = max(1, S::kThreads / items);
   const int share0 = s_merge[0] ? min((s_shared[0].w + kBatch - 1) / kBatch, most) : 0;
   const int share1 = s_merge[1] ? min((s_shared[1].w + kBatch - 1) / kBatch, most) : 0;
   float* s_ml = s_state;                                                // [share][items][2]
-  float4* s_o = reinterpret_cast<float4*>(s_state + 2 * S::kThreads);   // [share][items]
+  float4* s_o = reinterpret_cast<float4*>(s_state + 4 * S::kThreads);   // [share][items]
   for (int e = tid; e < items * (share0 + share1); e += S::kThreads) {
     const int slot = e >= items * share0;
     const int4 sh = s_shared[slot];
