@@ -288,8 +288,8 @@ typedef struct {
  * rules apply: 256-byte aligned, zero-filled once before its first use, left
  * ready for the next call by every call, one workspace per set of calls that
  * may overlap on the GPU (two graphs that may replay at once are such calls).
- * It depends on the dims and the current device's SM count only; calls that
- * share one may differ in batch_size and nnz_pages (it holds the largest). */
+ * It depends on the dims and the current device's SM count only; calls of this
+ * section that share one may differ in any of the dims (it holds the largest). */
 size_t tree_attn_cache_workspace_size(const ta_cache_dims* dims);
 
 typedef enum {

@@ -245,6 +245,23 @@ def test_copy_of_nothing(lib):
     assert _copy(lib, n=0, src=None, dst=None) == ta.TA_OK
 
 
+def test_workspace_leaves_the_same_room_for_parts_whatever_the_heads(lib):
+    """Handles that share a workspace differ in marks (4 bytes per page) and
+    counters only, both zero between calls: what is left of the size, 256 bytes
+    apart, is one number."""
+    up = lambda n: -(-n // 256) * 256
+    rest = set()
+    for h_q, h_kv in ((8, 2), (32, 8), (32, 2), (18, 2), (128, 1), (40, 8), (256, 2)):
+        for d in (64, 128):
+            for pages, batch in ((12, 3), (5000, 700)):
+                g = h_q // h_kv
+                groups = 1 if g <= 8 else -(-g // 16)
+                n = ta.cache_workspace_size(_dims(h_q=h_q, h_kv=h_kv, head_dim=d, num_pages=pages,
+                                                  batch_size=batch))
+                rest.add(n - up(4 * pages) - up(4 * batch * h_kv * groups))
+    assert len(rest) == 1
+
+
 # --------------------------------------------------------------------------
 # the compiled argument checks of PagedCache (on CPU tensors: all refused)
 # --------------------------------------------------------------------------

@@ -641,6 +641,37 @@ def test_handle_refusals():
         ta.PagedCache(s.pool, *[i32(x) for x in s.table], h_q=5)
 
 
+def test_a_workspace_shared_by_caches_of_other_heads():
+    """A draft's and a target's cache: head counts, head_dim and pools differ.
+    After a decode of either, the other's sequences over several CTAs are merged
+    and its copies made."""
+    kv = [6000] + [300 + 7 * i for i in range(31)]
+    a = Setup(kv, 32, 2, 128, "bf16", seed=72, fill=0.0)
+    others = [Setup(kv, 32, 8, 128, "bf16", seed=73, spare=2500, fill=0.0),
+              Setup(kv, 8, 2, 64, "fp16", seed=74, spare=300, fill=0.0),
+              Setup(kv, 128, 1, 64, "bf16", seed=75, spare=2500, fill=0.0)]
+    big = torch.zeros(8 << 20, dtype=torch.uint8, device="cuda")
+    caches = [ta.PagedCache(s.pool, *[i32(x) for x in s.table], h_q=s.h_q, workspace=big)
+              for s in [a] + others]
+    assert all(c.workspace is big for c in caches)
+    for i in (0, 1, 0, 2, 3, 0, 1, 3, 2):
+        s, c = ([a] + others)[i], caches[i]
+        q = s.randn(len(kv), s.h_q, s.d)
+        out = torch.full_like(q, 7.0)
+        lse = torch.full(q.shape[:2], 7.0, device="cuda")
+        c.decode(q, s.d ** -0.5, out=out, lse=lse)
+        check_decode(s, q, out, lse, s.d ** -0.5)
+        for o, oc in zip(others, caches[1:]):       # enough pairs for marks in the workspace
+            free = np.setdiff1d(np.arange(o.pool.shape[0]), o.values)
+            src = np.resize(o.values[:-2], 2100)
+            if len(free) < 2100:
+                continue
+            oc.copy_pages(i32(src), i32(free[:2100]))
+            assert oc.device_status() == ta.TA_OK
+            assert torch.equal(o.pool[free[:2100]], o.pool[src])
+        assert c.device_status() == ta.TA_OK
+
+
 def test_a_speculative_step_and_a_decoding_step():
     """Prompt, draft trees, their verification, compaction, a fork, one more
     token: the calls as a decoding loop makes them, on one stream without a

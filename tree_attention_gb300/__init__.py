@@ -537,10 +537,11 @@ class PagedCache:
     [B+1]``, ``page_values``, ``length_info [B]`` are CUDA tensors, held and not
     copied: their contents may change between calls.  ``h_q`` is the number of
     query heads.  The handle owns a workspace, so calls on it that may overlap
-    on the GPU need handles of their own (``with_table(..., workspace=None)``;
-    ``workspace`` takes another handle's where that is large enough);
-    every call is asynchronous on ``stream`` (default: torch's current
-    stream), and ``device_status`` reports inconsistent tables."""
+    on the GPU need handles of their own (``with_table(..., workspace=None)``).
+    ``workspace`` takes another handle's, whatever that one's heads and pool,
+    where it is large enough; where it is not, a new one is made.  Every call is
+    asynchronous on ``stream`` (default: torch's current stream), and
+    ``device_status`` reports inconsistent tables."""
 
     def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, workspace=None):
         if pages.dim() != 5 or pages.shape[1] != 2 or pages.shape[3] != 16:

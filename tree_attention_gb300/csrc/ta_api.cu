@@ -890,7 +890,7 @@ ta::PageTable page_table(const ta_cache_dims* d, const int32_t* page_indptr,
 }
 
 ta::CacheWorkspace cache_layout(const ta_cache_dims* d, int nsm) {
-  return ta::cache_workspace(d->batch_size, d->num_pages, d->h_kv, d->h_q / d->h_kv, d->head_dim, nsm);
+  return ta::cache_workspace(d->batch_size, d->num_pages, d->h_kv, d->h_q / d->h_kv, nsm);
 }
 
 unsigned int* error_word(void* workspace) { return &static_cast<WsHeader*>(workspace)->error; }

@@ -647,13 +647,16 @@ cudaError_t launch_heads(const DecodeParams& p, int nsm, cudaStream_t stream) {
 
 }  // namespace
 
-CacheWorkspace cache_workspace(int batch, int num_pages, int h_kv, int g, int head_dim, int nsm) {
+CacheWorkspace cache_workspace(int batch, int num_pages, int h_kv, int g, int nsm) {
+  constexpr int kGroups = kMaxGroup / 16;   // most head groups
   CacheWorkspace w{};
   const int heads = g <= 8 ? 8 : 16;
   w.groups = (g + heads - 1) / heads;
-  const int64_t ctas = (int64_t)ctas_per_group(nsm, w.groups) * w.groups;
   w.off_parts = 256;
-  w.off_marks = w.off_parts + round_up(ctas * 2 * (heads * (int64_t)head_dim + 2 * heads) * 4, 256);
+  // room for any heads: parts of one call must not lie over another's marks or
+  // counters, which have to be zero
+  const int64_t ctas = nsm > kGroups ? nsm : kGroups;
+  w.off_marks = w.off_parts + round_up(ctas * 2 * Shape<128, 2>::kState * 4, 256);
   w.off_counters = w.off_marks + round_up((int64_t)num_pages * 4, 256);
   w.total = w.off_counters + round_up((int64_t)batch * h_kv * w.groups * 4, 256);
   return w;

@@ -177,14 +177,14 @@ struct DecodeParams {
 };
 
 // Workspace of the paged-cache calls: header | launch_decode's parts |
-// launch_copy_pages's marks | launch_decode's counters.  What follows from the
-// batch comes last: calls with another batch size find the rest, and the
-// counters, in the same place.
+// launch_copy_pages's marks | launch_decode's counters.  The parts have the same
+// place and room whatever the dims, and only they hold anything between calls,
+// so calls with any dims find their marks and counters zero.
 struct CacheWorkspace {
   int groups;
   int64_t off_parts, off_marks, off_counters, total;
 };
-CacheWorkspace cache_workspace(int batch, int num_pages, int h_kv, int g, int head_dim, int nsm);
+CacheWorkspace cache_workspace(int batch, int num_pages, int h_kv, int g, int nsm);
 
 struct CompactParams {
   uint4* pages;
