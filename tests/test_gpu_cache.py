@@ -672,6 +672,12 @@ def test_a_workspace_shared_by_caches_of_other_heads():
         assert c.device_status() == ta.TA_OK
 
 
+def test_a_workspace_has_to_be_on_the_pools_device():
+    s = Setup([20], 4, 2, 64, seed=76)
+    with pytest.raises(ValueError, match="workspace"):
+        s.cache.with_table(*[i32(x) for x in s.table], workspace=torch.zeros(8 << 20, dtype=torch.uint8))
+
+
 def test_a_speculative_step_and_a_decoding_step():
     """Prompt, draft trees, their verification, compaction, a fork, one more
     token: the calls as a decoding loop makes them, on one stream without a

@@ -567,13 +567,16 @@ class PagedCache:
             need = cache_workspace_size(self.dims)
         if need == 0:
             raise TreeAttnError(TA_ERR_UNSUPPORTED, "tree_attn_cache_workspace_size")
+        if workspace is not None:
+            _check_dev("workspace", workspace)
+            if workspace.get_device() != self._dev:
+                raise ValueError("workspace must be on the device of pages")
         if workspace is None or workspace.numel() * workspace.element_size() < need:
             # zero-filled once, before a call on any stream: the library keeps its
             # counters consistent afterwards
             workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream(self._dev).synchronize()
-        _check_dev("workspace", workspace)
         self.workspace = workspace
         # the addresses of these tensors are what the calls pass, so they stay
         self._held = (pages, page_indptr, page_values, length_info, workspace)
