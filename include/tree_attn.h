@@ -362,8 +362,11 @@ ta_status tree_attn_append_paged(const void* q, int64_t q_stride, const void* k,
  * [B, h_q] (a sequence without kv rows gets out = 0 and lse = -inf).  The kv
  * rows of the whole batch are split evenly over the GPU, whatever the
  * sequences' lengths, and the parts merged through their lse; the result does
- * not depend on timing.  A page index outside the pool reads zeros and slots
- * past a sequence's length are never used, as in tree_attn_paged.
+ * not depend on timing.  Weights count as positive however small: where an
+ * element of a sequence's values is infinite or NaN in some rows, the element
+ * of out is the sum of those, and all others are as without them.  A page
+ * index outside the pool reads zeros and slots past a sequence's length are
+ * never used, as in tree_attn_paged.
  * Inconsistent page tables are reported by tree_attn_device_status and
  * nothing is computed.  h_q / h_kv <= 128; q, pages and out 16-byte aligned.
  * Asynchronous on stream. */

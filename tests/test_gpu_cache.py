@@ -211,6 +211,52 @@ def test_decode_many_equal_small_weights():
     check_decode(s, q, out, lse, 1.0)
 
 
+@pytest.mark.parametrize("ramp", [False, True])
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", [(8, 2, 128, "bf16"), (8, 2, 64, "fp16"),
+                                              (32, 2, 128, "fp16"), (40, 1, 64, "bf16")])
+def test_decode_values_that_are_not_finite(h_q, h_kv, d, dtype, ramp):
+    """Weights are positive: an element whose column of values has an infinity
+    is that infinity, NaN with a NaN or infinities of both signs, for every
+    head; all others, and the lse, are those of the values without them.  With
+    ramp, scores rise or fall by 550 powers of two along a sequence."""
+    kv = [40, 3, 5000, 700, 2600]
+    s = Setup(kv, h_q, h_kv, d, dtype, seed=18)
+    if ramp:
+        for b in (0, 2, 3, 4):
+            pid, sl = ref.slots(*s.table, b)
+            r = torch.linspace(-6, 6, kv[b]) * (128 / d) * (-1 if b in (2, 3) else 1)
+            s.pool[pid, 0, :, sl] = r[:, None, None].to(s.dtype).expand(kv[b], h_kv, d).cuda()
+    q = s.randn(len(kv), h_q, d) if not ramp else torch.ones((len(kv), h_q, d), dtype=s.dtype,
+                                                             device="cuda")
+    sm = 0.25 if ramp else d ** -0.5
+    clean = s.pool.clone()
+    inf, nan = float("inf"), float("nan")
+    want = {}
+    # sequence, row, kv head, element, value
+    for b, r, h, e, x in [(0, 0, 0, 5, inf), (0, 39, 0, 6, -inf), (0, 17, h_kv - 1, d - 1, nan),
+                          (0, 2, 0, 9, inf), (0, 36, 0, 9, -inf),
+                          (1, 2, 0, 0, -inf), (1, 1, 0, 1, inf), (1, 0, 0, 1, inf),
+                          (2, 0, 0, 3, inf), (2, 4999, 0, 4, -inf), (2, 2500, 0, 63, inf),
+                          (2, 10, h_kv - 1, 40, inf), (2, 4000, h_kv - 1, 40, nan),
+                          (3, 699, 0, 8, inf), (3, 0, 0, 11, -inf), (4, 1300, 0, 20, -inf),
+                          (4, 0, 0, 21, inf), (4, 2599, 0, 22, inf)]:
+        pid, sl = ref.slots(*s.table, b)
+        s.pool[pid[r], 1, h, sl[r], e] = x
+        clean[pid[r], 1, h, sl[r], e] = 0
+        want[b, h, e] = x if want.get((b, h, e), x) == x else nan
+    out, lse = s.cache.decode(q, sm)
+    dirty, s.pool = s.pool, clean
+    s.cache = s.handle()
+    base, base_lse = s.cache.decode(q, sm)
+    check_decode(s, q, base, base_lse, sm)
+    assert torch.equal(lse, base_lse)
+    g, expect = h_q // h_kv, base.clone()
+    for (b, h, e), x in want.items():
+        expect[b, h * g:(h + 1) * g, e] = x
+    assert torch.equal(torch.isnan(out), torch.isnan(expect))
+    assert torch.equal(out.nan_to_num(7, inf, -inf), expect.nan_to_num(7, inf, -inf))
+
+
 def test_decode_page_outside_the_pool_reads_zeros():
     s = Setup([50, 20], 4, 2, 128, seed=3)
     s.values[1], s.values[4] = 10 ** 6, -1

@@ -83,6 +83,15 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// Of two packed numbers, the infinite and NaN ones (all exponent bits set).
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite_of(uint32_t u) {
+  constexpr uint32_t kExponent = BF16 ? 0x7f807f80u : 0x7c007c00u;
+  return u & __vcmpeq2(u & kExponent, kExponent);
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
 // NT tiles of 8 heads per warp.  The warps per CTA follow from the registers a
 // lane needs (a page of K and of V, Q, O: 32 + 32 + 16 NT + 32 NT for d = 128).
 template <int D, int NT>
@@ -144,6 +153,26 @@ struct Acc {
       o.z += y[k].z * w;
       o.w += y[k].w * w;
     }
+  }
+  // Where the sum over the states ``o_of(k)``, k = from, from + step .. below to,
+  // is not finite: factors are positive, but may have underflowed to zero, so it
+  // is the sum of the states' infinities and NaNs, if there are any.
+  template <typename F>
+  __device__ __forceinline__ void keep_infinities(int from, int to, int step, F o_of) {
+    if (__builtin_expect(finite(o.x) && finite(o.y) && finite(o.z) && finite(o.w), 1)) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k = from; k < to; k += step) {
+      const float4 y = o_of(k);
+      s.x += finite(y.x) ? 0.f : y.x;
+      s.y += finite(y.y) ? 0.f : y.y;
+      s.z += finite(y.z) ? 0.f : y.z;
+      s.w += finite(y.w) ? 0.f : y.w;
+    }
+    o.x = finite(s.x) ? o.x : s.x;
+    o.y = finite(s.y) ? o.y : s.y;
+    o.z = finite(s.z) ? o.z : s.z;
+    o.w = finite(s.w) ? o.w : s.w;
   }
 };
 
@@ -457,6 +486,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
           float z = l[n][j];
 #pragma unroll
           for (int i = 4; i <= 16; i <<= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
+          l[n][j] = z;
           const int h = n * 8 + 2 * c + j;
           if (whole) {
             if (head0 + h < p.g) {
@@ -489,6 +519,62 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
             }
           }
         }
+      // A sum that is not finite: weights are positive, so it is the sum of its
+      // column's infinities and NaNs, if there are any, but the products above
+      // need not give that, as a weight's second part may be zero or negative and
+      // small weights and factors round to zero.  The segment's values are read
+      // again, a tile of elements at a time, with weights of one.  (To look at every
+      // value before its product cost 1 to 5 %, to look at the sums 0.2 us a call)
+      float2 odd = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < 4 * VH; ++t) {
+          odd = ffma2(make_float2(o[n][t][0], o[n][t][1]), make_float2(0.f, 0.f), odd);
+          odd = ffma2(make_float2(o[n][t][2], o[n][t][3]), make_float2(0.f, 0.f), odd);
+        }
+      if (__builtin_expect(__any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f), 0)) {
+        constexpr uint32_t kOnes = BF16 ? 0x3f803f80u : 0x3c003c00u;
+        const int at0 = max(seg_lo, u_first) - kvh_now * P, at1 = u - kvh_now * P;
+#pragma unroll 1
+        for (int t = 0; t < 4 * VH; ++t) {
+          const int elem = 64 * (t / 4) + 8 * r + 2 * (t % 4);      // and the next one
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int at = at0; at < at1; ++at) {
+            const int page = p.tab.page_values[at];
+            const int in = page < 0 || page >= p.tab.num_pages  ? 0
+                           : at + 1 == s_indptr[b_now + 1] ? s_len[b_now] : kPageSize;
+            const uint16_t* v =
+                p.pages + (((int64_t)page * 2 + 1) * p.h_kv + kvh_now) * (kPageSize * D) + elem;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
+              w[i] = tok < in ? not_finite_of<BF16>(*reinterpret_cast<const uint32_t*>(v + tok * D)) : 0;
+            }
+            mma16816<BF16>(y, __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                           __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), kOnes, kOnes);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int h = n * 8 + 2 * c + j;
+              if (whole) {
+                // as above; a row whose sum of weights is NaN stays NaN
+                uint16_t* out = p.out + ((size_t)b_now * p.h_q + (size_t)kvh_now * p.g + head0 + h) * D + elem;
+                const uint32_t both = pack2<BF16>(y[j] + 0.f * l[n][j], y[j + 2] + 0.f * l[n][j]);
+                if (head0 + h < p.g && !finite(y[j])) out[0] = (uint16_t)both;
+                if (head0 + h < p.g && !finite(y[j + 2])) out[1] = (uint16_t)(both >> 16);
+              } else {
+                float* st = s_state + piece * S::kState + h * D + elem;
+                if (!finite(y[j])) st[0] = y[j];
+                if (!finite(y[j + 2])) st[1] = y[j + 2];
+              }
+            }
+        }
+      }
       if (!more) break;
       reset();
     }
@@ -526,6 +612,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       }
       a.add(pm, pl, y);
     }
+    a.keep_infinities(grp.x, grp.y, 1, [&](int k) {
+      return reinterpret_cast<const float4*>(s_state + s_part[k] * S::kState + h * D)[i];
+    });
     if (grp.z < 0) {
       finish(s_group_at[e / items], h, i, a);
     } else {
@@ -597,6 +686,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       }
       a.add(pm, pl, y);
     }
+    a.keep_infinities(y0 / items, sh.w, share, [&](int k) {
+      return __ldcg(reinterpret_cast<const float4*>(part(k) + h * D) + i);
+    });
     if (share == 1) {
       finish(make_int2(sh.x, sh.y), h, i, a);
     } else {
@@ -616,6 +708,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       const int e = e0 + k * items;
       a.add({s_ml[2 * e]}, {s_ml[2 * e + 1]}, {s_o[e]});
     }
+    a.keep_infinities(0, share, 1, [&](int k) { return s_o[e0 + k * items]; });
     finish(make_int2(s_shared[slot].x, s_shared[slot].y), x % items / V4, x % V4, a);
   }
 }
