@@ -874,3 +874,68 @@ def test_calls_on_a_side_stream():
     out, lse = s.cache.decode(q.contiguous(), 0.1, stream=side)
     side.synchronize()
     check_decode(s, q.contiguous(), out, lse, 0.1)
+
+
+STREAM_AS = {"object": lambda s: s, "address": lambda s: s.cuda_stream}
+
+
+@pytest.mark.parametrize("form", list(STREAM_AS))
+def test_calls_run_on_the_stream_they_are_given(form):
+    """Inputs that a busy side stream is still to write: calls on any other
+    stream would read what was there before."""
+    s = Setup([500, 60], 8, 2, 128, seed=64, fill=0.0)
+    side = torch.cuda.Stream()
+    x = s.randn(2, 12, 128)
+    q, k, v = x[:, :8], x[:, 8:10], x[:, 10:]
+    new, ai, src, dst = s.randn(2, 12, 128), i32([0, 1, 2]), i32([0]), i32([0])
+    free = np.setdiff1d(np.arange(s.pool.shape[0]), s.values)[:1]
+    want = s.pool.clone()
+    for b, t in ((0, 499), (1, 59)):
+        pid, sl = ref.slots(*s.table, b)
+        want[pid[t], 0, :, sl[t]], want[pid[t], 1, :, sl[t]] = new[b, 8:10], new[b, 10:]
+    want[free] = want[s.values[:1]]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        x.copy_(new)
+        src.fill_(int(s.values[0]))
+        dst.fill_(int(free[0]))
+    at = STREAM_AS[form](side)
+    qo = s.cache.append(q, k, v, ai, stream=at)
+    out, lse = s.cache.decode(qo, 0.1, stream=at)
+    s.cache.copy_pages(src, dst, stream=at)
+    tables = s.cache.compact(i32([0, 0, 0]), i32([0, 0, 0]), i32([]), stream=at)
+    side.synchronize()
+    assert torch.equal(qo, new[:, :8]) and torch.equal(s.pool, want)
+    check_decode(s, qo, out, lse, 0.1)
+    assert tables[0].tolist() == s.indptr.tolist() and s.cache.device_status(at) == ta.TA_OK
+
+
+@pytest.mark.parametrize("form", list(STREAM_AS))
+def test_outputs_come_from_the_pool_of_the_calls_stream(form):
+    """Memory that the current stream still reads is not given to a call on
+    another stream."""
+    s = Setup([500, 60], 8, 2, 128, seed=65, fill=0.0)
+    side = torch.cuda.Stream()
+    q = s.randn(2, 8, 128)
+    x = torch.full((2, 8, 128), 3.0, dtype=s.dtype, device="cuda")
+    at = x.data_ptr()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    y = x * 2
+    del x
+    out, lse = s.cache.decode(q, 0.1, stream=STREAM_AS[form](side))
+    assert out.data_ptr() != at
+    side.synchronize()
+    check_decode(s, q, out, lse, 0.1)
+    assert (y == 6).all()
+
+
+@pytest.mark.parametrize("address", [0, 1, 2])
+def test_calls_on_the_default_streams_by_address(address):
+    s = Setup([500, 60], 8, 2, 128, seed=66, fill=0.0)
+    q = s.randn(2, 8, 128)
+    torch.cuda.synchronize()
+    out, lse = s.cache.decode(q, 0.1, stream=address)
+    torch.cuda.synchronize()
+    check_decode(s, q, out, lse, 0.1)

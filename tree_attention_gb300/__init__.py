@@ -593,10 +593,15 @@ class PagedCache:
 
     def _empty(self, shape, dtype, stream):
         """A new output, from the pool of the stream that the call runs on."""
-        if isinstance(stream, torch.cuda.Stream):
-            with torch.cuda.stream(stream):
-                return torch.empty(shape, dtype=dtype, device=self.device)
-        return torch.empty(shape, dtype=dtype, device=self.device)
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if not isinstance(stream, torch.cuda.Stream):
+            address = int(getattr(stream, "cuda_stream", stream))
+            # 0 and 1 are CUDA's names of the legacy default stream
+            stream = (torch.cuda.ExternalStream(address, device=self.device) if address > 1
+                      else torch.cuda.default_stream(self.device))
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     def append(self, q, k, v, append_indptr, positions=None, *, rope: Optional[Rope] = None,
                q_weight=None, k_weight=None, norm_eps: float = 1e-6, q_out=None, stream=None):
