@@ -939,3 +939,29 @@ def test_calls_on_the_default_streams_by_address(address):
     out, lse = s.cache.decode(q, 0.1, stream=address)
     torch.cuda.synchronize()
     check_decode(s, q, out, lse, 0.1)
+
+
+def test_a_dropped_handles_workspace_outlives_its_calls():
+    """On a stream object and on the current stream: the handle's own workspace
+    is not given to another tensor before the calls are done."""
+    s = Setup([3000, 60], 8, 2, 128, seed=67, fill=0.0)
+    q = s.randn(2, 8, 128)
+    want = [t.clone() for t in s.cache.decode(q, 0.1)]
+    for given in (True, False):
+        side = torch.cuda.Stream()
+        c = s.cache.with_table(*[i32(x) for x in s.table], workspace=None)
+        at, n = c.workspace.data_ptr(), c.workspace.numel()
+        out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            c.decode(q, 0.1, out=out, lse=lse, stream=side if given else None)
+            if given:
+                c.decode(q, 0.1, out=out, lse=lse, stream=side)
+        del c
+        other = torch.empty(n, dtype=torch.uint8, device="cuda")
+        assert other.data_ptr() != at
+        other.fill_(255)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert (other == 255).all()

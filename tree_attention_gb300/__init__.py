@@ -541,7 +541,8 @@ class PagedCache:
     ``workspace`` takes another handle's, whatever that one's heads and pool,
     where it is large enough; where it is not, a new one is made.  Every call is
     asynchronous on ``stream`` (default: torch's current stream), and
-    ``device_status`` reports inconsistent tables."""
+    ``device_status`` reports inconsistent tables.  The handle may be dropped
+    while its calls run, unless on a stream that is not one of torch's."""
 
     def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, workspace=None):
         if pages.dim() != 5 or pages.shape[1] != 2 or pages.shape[3] != 16:

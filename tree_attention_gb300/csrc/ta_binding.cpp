@@ -7,13 +7,17 @@
 // 3 to 6 us per call (append 9.0 us of host time in all), here 0.3.
 #include <Python.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <sstream>
 #include <stdexcept>
+#include <vector>
 
 #include "tree_attn.h"
 
@@ -28,6 +32,8 @@ struct Handle {
   size_t workspace_bytes;
   int device;
   at::ScalarType dtype;
+  at::Tensor workspace_tensor;
+  mutable std::vector<cudaStream_t> streams;   // that hold_workspace has seen
 };
 
 const char* const kCapsule = "tree_attention_gb300.cache";
@@ -85,6 +91,18 @@ int64_t length(const char* name, PyObject* o, int dim) {
 
 struct PythonError {};   // a Python exception is set
 
+// Keeps the workspace's memory from being reused, after the handle is gone,
+// before the work on ``stream`` is done: the caller never sees this tensor.  Not
+// on streams that torch did not make (their id is their address): they may be
+// destroyed before the memory is freed.
+void hold_workspace(const Handle& h, c10::cuda::CUDAStream stream) {
+  cudaStream_t s = stream.stream();
+  if (std::find(h.streams.begin(), h.streams.end(), s) != h.streams.end()) return;
+  if (stream.id() == 0 || stream.id() != reinterpret_cast<int64_t>(s))
+    c10::cuda::CUDACachingAllocator::recordStream(h.workspace_tensor.storage().data_ptr(), stream);
+  h.streams.push_back(s);
+}
+
 // The stream of a call: torch's current one, a stream object, or an address.
 void* stream_of(const Handle& h, PyObject* o) {
   if (c10::cuda::current_device() != h.device) {
@@ -92,7 +110,21 @@ void* stream_of(const Handle& h, PyObject* o) {
     s << "the cache is on cuda:" << h.device << ", which is not the current device";
     throw std::invalid_argument(s.str());
   }
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(h.device).stream();
+  if (o == Py_None) {
+    const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(h.device);
+    hold_workspace(h, stream);
+    return stream.stream();
+  }
+  if (THPStream_Check(o)) {
+    const THPStream* t = reinterpret_cast<const THPStream*>(o);
+    const c10::cuda::CUDAStream stream = c10::cuda::CUDAStream::unpack3(
+        t->stream_id, static_cast<c10::DeviceIndex>(t->device_index),
+        static_cast<c10::DeviceType>(t->device_type));
+    if (stream.device_index() != h.device)
+      throw std::invalid_argument("stream must be on the device of the cache");
+    hold_workspace(h, stream);
+    return stream.stream();
+  }
   PyObject* a = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
                                                          : PyNumber_Long(o);
   if (!a) throw PythonError();
@@ -150,7 +182,7 @@ PyObject* make_handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto ptr = [&](int i) { return static_cast<int32_t*>(THPVariable_Unpack(a[i]).data_ptr()); };
   Handle* h = new Handle{*static_cast<ta_cache_dims*>(dims), pages.data_ptr(), ptr(2), ptr(3), ptr(4),
                          ws.data_ptr(), static_cast<size_t>(ws.nbytes()),
-                         static_cast<int>(pages.get_device()), pages.scalar_type()};
+                         static_cast<int>(pages.get_device()), pages.scalar_type(), ws, {}};
   PyObject* c = PyCapsule_New(h, kCapsule, [](PyObject* o) {
     delete static_cast<Handle*>(PyCapsule_GetPointer(o, kCapsule));
   });
