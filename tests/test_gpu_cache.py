@@ -965,3 +965,50 @@ def test_a_dropped_handles_workspace_outlives_its_calls():
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
         assert (other == 255).all()
+
+
+def test_a_handle_made_in_a_captured_graph():
+    """Its workspace is in memory that another graph has left dirty.  Calls
+    outside the graph, in another one, and in its own, before and after the
+    replays of each."""
+    s = Setup([6000, 60, 900], 8, 2, 128, seed=68, fill=0.0)
+    q = s.randn(3, 8, 128)
+    tables = [i32(x) for x in s.table]
+    want = [t.clone() for t in s.cache.decode(q, 0.1)]
+    outs = [(torch.empty_like(want[0]), torch.empty_like(want[1])) for _ in range(3)]
+    torch.cuda.synchronize()
+    dirty, first, second = (torch.cuda.CUDAGraph() for _ in range(3))
+    with torch.cuda.graph(dirty):
+        x = torch.full((64 << 20,), 127, dtype=torch.uint8, device="cuda")
+    dirty.replay()
+    torch.cuda.synchronize()
+    pool = dirty.pool()
+    del x
+    with torch.cuda.graph(first, pool=pool):
+        tmp = torch.full((64 << 20,), 126, dtype=torch.uint8, device="cuda")
+        del tmp
+        c = s.cache.with_table(*tables, workspace=None)
+        c.decode(q, 0.1, *outs[0])
+    with torch.cuda.graph(second):
+        c.decode(q, 0.1, *outs[1])
+
+    def check(*which):
+        torch.cuda.synchronize()
+        assert c.device_status() == ta.TA_OK
+        for i in which:
+            assert torch.equal(outs[i][0], want[0]) and torch.equal(outs[i][1], want[1])
+            outs[i][0].fill_(7)
+            outs[i][1].fill_(7)
+
+    assert bool((c.workspace == 0).all())
+    c.decode(q, 0.1, *outs[2])
+    check(2)
+    second.replay()
+    check(1)
+    first.replay()
+    check(0)
+    second.replay()
+    check(1)
+    c.decode(q, 0.1, *outs[2])
+    first.replay()
+    check(0, 2)

@@ -564,6 +564,7 @@ class PagedCache:
         self.dims = CacheDims(batch_size=self.batch_size, h_q=self.h_q, h_kv=self.h_kv,
                               head_dim=self.head_dim, dtype=_dtype_code(pages.dtype),
                               num_pages=pages.shape[0], nnz_pages=page_values.numel())
+        self._binding = _compiled()
         with torch.cuda.device(self._dev):
             need = cache_workspace_size(self.dims)
         if need == 0:
@@ -574,14 +575,17 @@ class PagedCache:
                 raise ValueError("workspace must be on the device of pages")
         if workspace is None or workspace.numel() * workspace.element_size() < need:
             # zero-filled once, before a call on any stream: the library keeps its
-            # counters consistent afterwards
+            # counters consistent afterwards.  While a graph is captured the filling
+            # goes into it, as its replays may have other tensors in this memory
+            # first, and is done at once too, for calls outside the graph
             workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
-            if not torch.cuda.is_current_stream_capturing():
+            if torch.cuda.is_current_stream_capturing():
+                self._binding.zero_now(workspace)
+            else:
                 torch.cuda.current_stream(self._dev).synchronize()
         self.workspace = workspace
         # the addresses of these tensors are what the calls pass, so they stay
         self._held = (pages, page_indptr, page_values, length_info, workspace)
-        self._binding = _compiled()
         self._handle = self._binding.handle(ctypes.addressof(self.dims), pages, page_indptr,
                                             page_values, length_info, workspace)
 

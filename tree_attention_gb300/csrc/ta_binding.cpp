@@ -8,7 +8,9 @@
 #include <Python.h>
 
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -264,6 +266,21 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// zero_now(tensor): zero-fills a CUDA tensor before it returns, also while the
+// current stream is captured into a graph.
+PyObject* zero_now(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 1, [&] {
+    if (!THPVariable_Check(a[0])) throw std::invalid_argument("a tensor expected");
+    const at::Tensor& t = THPVariable_Unpack(a[0]);
+    if (!t.is_cuda() || !t.is_contiguous()) throw std::invalid_argument("a contiguous CUDA tensor expected");
+    c10::cuda::CUDAStreamCaptureModeGuard relaxed{cudaStreamCaptureModeRelaxed};
+    const c10::cuda::CUDAStream stream = c10::cuda::getStreamFromPool(false, t.device().index());
+    C10_CUDA_CHECK(cudaMemsetAsync(t.data_ptr(), 0, t.nbytes(), stream));
+    C10_CUDA_CHECK(cudaStreamSynchronize(stream));
+    return 0L;
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F)), METH_FASTCALL, nullptr};
@@ -271,7 +288,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<make_handle>("handle"), method<append>("append"),
                            method<decode>("decode"),      method<compact>("compact"),
-                           method<copy_pages>("copy_pages"), {nullptr, nullptr, 0, nullptr}};
+                           method<copy_pages>("copy_pages"), method<zero_now>("zero_now"),
+                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
