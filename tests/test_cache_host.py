@@ -305,3 +305,45 @@ def test_binding_refuses_what_is_not_on_the_handles_device(lib):
 def test_binding_refuses_what_is_no_tensor_or_no_handle(lib, call):
     with pytest.raises(ValueError):
         call(ta._compiled(), _handle(_dims()))
+
+
+# --------------------------------------------------------------------------
+# building the extension module
+# --------------------------------------------------------------------------
+
+def test_module_is_rebuilt_for_another_torch(lib, monkeypatch):
+    assert ta_build.binding_up_to_date() and ta_build.up_to_date()
+    monkeypatch.setattr("torch.__version__", "0.0")
+    assert not ta_build.binding_up_to_date() and not ta_build.up_to_date()
+
+
+@pytest.mark.parametrize("fails", ["_compile_binding", "_link_binding"])
+def test_library_is_linked_though_the_module_fails(lib, monkeypatch, tmp_path, fails):
+    def fail(*a):
+        raise RuntimeError("no headers")
+    for name, file in (("LIB_PATH", "l.so"), ("BINDING_PATH", "b.so"), ("BINDING_STAMP", "b.txt"),
+                       ("BUILD_DIR", "")):
+        monkeypatch.setattr(ta_build, name, str(tmp_path / file))
+    monkeypatch.setattr(ta_build, "SOURCES", ["ta_merge.cu"])     # the shortest
+    monkeypatch.setattr(ta_build, "_compile_binding", lambda: "b.o")
+    monkeypatch.setattr(ta_build, fails, fail)
+    with pytest.raises(RuntimeError, match="no headers"):
+        ta_build.build()
+    assert (tmp_path / "l.so").exists() and not (tmp_path / "b.so").exists()
+    monkeypatch.setattr(ta_build, "_compile_binding", lambda: "b.o")
+    monkeypatch.setattr(ta_build, "_link_binding", lambda o: (tmp_path / "b.so").touch())
+    monkeypatch.setattr(ta_build, "_link_library", fail)          # already there
+    ta_build.build()
+
+
+@pytest.mark.parametrize("there,says", [(True, "cannot be loaded"), (False, "is not built")])
+def test_a_module_that_does_not_load_is_told_from_one_that_is_not_there(lib, monkeypatch, there,
+                                                                        says):
+    import importlib
+    def fail(name):
+        raise ImportError("undefined symbol")
+    monkeypatch.setattr(ta, "_binding_module", None)
+    monkeypatch.setattr(importlib, "import_module", fail)
+    monkeypatch.setattr(ta.os.path, "exists", lambda p: there)
+    with pytest.raises(RuntimeError, match=says + r" \(undefined symbol\)"):
+        ta._compiled()

@@ -524,7 +524,9 @@ def _compiled():
         try:
             _binding_module = importlib.import_module("tree_attention_gb300._binding")
         except ImportError as e:
-            raise RuntimeError("_binding.so is not built; run tree_attention_gb300.build.build() "
+            state = ("cannot be loaded" if os.path.exists(os.path.join(_PKG, "_binding.so"))
+                     else "is not built")
+            raise RuntimeError(f"_binding.so {state} ({e}); run tree_attention_gb300.build.build() "
                                "or __graft_entry__.build()") from e
     return _binding_module
 

@@ -24,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libtreeattn.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "binding.txt")
 SOURCES = ["ta_api.cu", "ta_plan.cu", "ta_attn.cu", "ta_merge.cu", "ta_cache.cu", "ta_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -44,11 +45,30 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+def _newer_than_inputs(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path)
+                                        for f in _inputs())
+
+
+def _binding_for() -> str:
+    """What the extension module is compiled against, beside its sources."""
+    import torch
+    return f"torch {torch.__version__} {torch.__file__}\npython {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
+def binding_up_to_date() -> bool:
+    if not _newer_than_inputs(BINDING_PATH) or not os.path.exists(BINDING_STAMP):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    try:
+        want = _binding_for()
+    except ImportError:   # no torch: building the module will say so
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() == want
+
+
+def up_to_date() -> bool:
+    return _newer_than_inputs(LIB_PATH) and binding_up_to_date()
 
 
 def _run(cmd, what):
@@ -81,11 +101,24 @@ def _link_binding(obj: str) -> None:
           "-L", _torch_dir("lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
          "linking _binding.so")
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_for())
+
+
+def _link_library(nvcc: str, objs) -> None:
+    tmp = LIB_PATH + ".tmp"
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"], "link")
+    os.replace(tmp, LIB_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library; returns its path."""
-    if not force and not extra_flags and up_to_date():
+    """Compile and link the library and the extension module; returns the
+    library's path.  The library is in place before a failure of the module,
+    which alone needs torch's headers, is raised."""
+    all_of_it = force or bool(extra_flags)
+    library = all_of_it or not _newer_than_inputs(LIB_PATH)
+    module = all_of_it or not binding_up_to_date()
+    if not library and not module:
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -101,16 +134,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
-    tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj)
+        binding = ex.submit(_compile_binding) if module else None
+        if library:
+            _link_library(nvcc, list(ex.map(compile_one, SOURCES)))
+    if module:
+        _link_binding(binding.result())
     return LIB_PATH
 
 
