@@ -429,6 +429,26 @@ def test_append_many_tokens_per_warp():
     assert (np.abs(f64(s.pool) - want) <= tol).all()
 
 
+def test_append_warps_over_several_sequences():
+    """Single heads, three steps per token: a warp's dozen steps begin in the
+    middle of a token and go over five, of as many sequences."""
+    rng = np.random.default_rng(19)
+    new = rng.integers(0, 6, 16000)
+    s = Setup(new + rng.integers(0, 20, 16000), 1, 1, 64, "bf16", seed=19, fill=0.0)
+    q, k, v = append_inputs(s, new, True)
+    assert len(q) * 3 > 12 * 4 * 5 * torch.cuda.get_device_properties(0).multi_processor_count
+    ai = np.concatenate([[0], np.cumsum(new)])
+    pos = rng.integers(-2 ** 31, 2 ** 31, len(q))
+    before = s.pool.clone()
+    qo = s.cache.append(q, k, v, i32(ai), i32(pos), rope=ta.Rope("interleaved", 32))
+    assert s.cache.device_status() == ta.TA_OK
+    (yq, tq), (yk, tk) = append_reference(s, q, k, pos, "interleaved", 32, 1e4, 1.0, None, None, 0.0)
+    assert (np.abs(f64(qo) - yq) <= tq).all()
+    want = ref.append(f64(before), yk, f64(v), ai, *s.table)
+    tol = ref.append(np.zeros(before.shape), tk, 0 * f64(v), ai, *s.table)
+    assert (np.abs(f64(s.pool) - want) <= tol).all()
+
+
 def test_append_in_place_and_magnitude_and_frequencies():
     """q_out may be q; a table of frequencies and a factor of cos and sin."""
     s = Setup([40], 4, 2, 64, "bf16", seed=12)

@@ -23,6 +23,8 @@ __device__ __forceinline__ void report_bad_tables(unsigned int* error) {
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
+constexpr int kAppendTokens = 8;  // tokens that a warp comes by, at most
+static_assert((kAppendMaxSteps - 1) / 3 + 2 <= kAppendTokens, "a token has three steps at least");
 constexpr int kAppendDepth = 5;   // steps (1 KB) a warp has in flight (3: 3 % slower, 8 no faster)
 
 // The largest b in [0, batch) with indptr[b] <= t, by one warp: 32 probes cut
@@ -70,6 +72,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
   __shared__ __align__(16) float2 s_cos_sin[kAppendThreads / 32][D / 2];
   __shared__ uint64_t s_turns[64];
   __shared__ uint4 s_weight[2][D / 8];     // of queries, of keys
+  __shared__ long long s_slot[kAppendThreads / 32][kAppendTokens];   // see look_up
+  __shared__ int s_pos[kAppendThreads / 32][kAppendTokens];
   // lanes that index the parameters apart are served one by one: once per CTA
   static_assert(kAppendThreads >= 64 + D / 4, "a thread per frequency and per vector of weights");
   if (LAYOUT != 0 && threadIdx.x < 64) s_turns[threadIdx.x] = p.turns[threadIdx.x];
@@ -137,19 +141,16 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // Positions and cache slots of the next 32 tokens, one per lane: one chain of
-  // dependent loads for all tokens that a warp comes by.  It goes first: behind
-  // the rows of all warps in the memory's queues each of its loads took 1,500
-  // cycles instead of 700.
-  const int t_end = left > 0 ? (lo + left - 1) / all + 1 : t;
-  int m_from = t, m_pos = 0;
-  long long m_slot = -1;                   // element offset of a token's K slot, head 0; -1: none
+  // Positions and cache slots of this warp's tokens, token x's at x % kAppendTokens,
+  // looked up one per lane: one chain of dependent loads for all of them.  It goes
+  // first: behind the rows of all warps in the memory's queues each of its loads
+  // took 1,500 cycles instead of 700.
   auto look_up = [&]() {
-    const int tt = m_from + lane;
-    const bool mine = tt < t_end;
-    if (LAYOUT != 0 && mine) m_pos = p.positions[tt];
+    const int tt = t + lane;
+    const bool mine = lane < kAppendTokens && tt <= (lo + left - 1) / all;
+    const int pos = LAYOUT != 0 && mine ? p.positions[tt] : 0;
     // the sequence of the first token, then of the others behind it
-    int b = find_sequence(p.append_indptr, p.tab.batch, m_from, lane);
+    int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
     if (mine && tt >= p.append_indptr[b + 1]) {
       int hi = p.tab.batch;                // the largest b with append_indptr[b] <= tt
       while (hi - b > 1) {
@@ -160,37 +161,35 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(con
           hi = mid;
       }
     }
-    m_slot = -1;
     if (!mine) return;
     const int a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
     const int p0 = p.tab.page_indptr[b], p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
+    long long slot = -1;                   // element offset of its K slot, head 0; -1: none
     if (a0 >= 0 && tt >= a0 && tt < a1 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
         p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize) {
       const int kv = (p1 - p0 - 1) * kPageSize + last, row = kv - (a1 - tt);
       if (kv >= a1 - a0) {
         const int page = p.tab.page_values[p0 + row / kPageSize];
         if (page >= 0 && page < p.tab.num_pages)
-          m_slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
+          slot = ((long long)page * 2 * p.h_kv * kPageSize + row % kPageSize) * D;
       }
     }
-    if (m_slot < 0) report_bad_tables(p.error);
+    if (slot < 0) report_bad_tables(p.error);
+    s_slot[warp][tt % kAppendTokens] = slot;
+    if (LAYOUT != 0) s_pos[warp][tt % kAppendTokens] = pos;
   };
   if (left > 0) look_up();
 #pragma unroll 1
   for (int i = 0; i < kAppendDepth; ++i) fetch();
-  __syncthreads();                         // s_turns, s_weight
+  __syncthreads();                         // s_turns, s_weight, s_slot, s_pos
 
   int ring = 0;
   for (; left > 0; ++t, begin = 0) {
     const int end = min(all, begin + left);
     left -= end - begin;
-    if (t - m_from == 32) {
-      m_from = t;
-      look_up();
-    }
-    const long long slot = __shfl_sync(0xffffffffu, m_slot, t - m_from);
+    const long long slot = s_slot[warp][t % kAppendTokens];
     if (LAYOUT != 0) {
-      const int64_t pos = __shfl_sync(0xffffffffu, m_pos, t - m_from);
+      const int64_t pos = s_pos[warp][t % kAppendTokens];
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
