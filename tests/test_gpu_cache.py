@@ -549,6 +549,21 @@ def test_compact(name, heads):
     assert int(nf) == len(rf) and fr[:len(rf)].tolist() == rf
 
 
+def test_compact_largest_batch():
+    """16,384 sequences of 0 to 20 rows; trees and paths of any size."""
+    rng = np.random.default_rng(25)
+    kv = rng.integers(0, 21, 16384)
+    nodes = [int(rng.integers(0, n + 1)) for n in kv]
+    paths = [sorted(rng.permutation(n)[:rng.integers(0, n + 1)]) for n in nodes]
+    s = Setup(kv, 1, 1, 64, seed=26)
+    _, (ni, nv, nl, fr, nf), (pool, ri, rv, rl, rf), st = run_compact(s, nodes, paths)
+    assert st == ta.TA_OK
+    np.testing.assert_array_equal(f64(s.pool), pool)
+    assert ni.tolist() == ri and nl.tolist() == rl
+    assert nv[:ri[-1]].tolist() == rv
+    assert int(nf) == len(rf) and fr[:len(rf)].tolist() == rf
+
+
 def test_compact_leaves_the_arrays_tails():
     s = Setup([40, 20], 4, 2, 64, seed=22)
     nnz = len(s.values)
@@ -1032,3 +1047,46 @@ def test_a_handle_made_in_a_captured_graph():
     c.decode(q, 0.1, *outs[2])
     first.replay()
     check(0, 2)
+
+
+def test_captured_compaction_and_copies_follow_their_inputs():
+    """Paths, node counts and page lists that change in place between replays;
+    a list for either way of finding conflicts."""
+    s = Setup([100, 64, 40], 8, 2, 64, seed=69, spare=6000, fill=0.0)
+    s.pool.copy_(torch.randn(s.pool.shape, device="cuda"))
+    mn, ai, an = i32([0, 30, 80, 90]), i32([0, 4, 6, 7]), i32([0, 3, 9, 20, 1, 40, 5])
+    free = np.setdiff1d(np.arange(s.pool.shape[0]), s.values)
+    lists = [(i32(free[:n]), i32(free[n:2 * n])) for n in (40, 2500)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for a, b in lists:
+            s.cache.copy_pages(a, a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        new = s.cache.compact(mn, ai, an)
+        for a, b in lists:
+            s.cache.copy_pages(a, b)
+    for step in range(3):
+        nodes = [[30, 50, 10], [1, 64, 0], [7, 16, 33]][step]
+        paths = [[[0, 3, 9, 20], [1, 40], [5]], [[0], list(range(58, 64)), []],
+                 [[1, 6], [0, 1, 2, 3], [32]]][step]
+        ai_now = np.concatenate([[0], np.cumsum([len(p) for p in paths])])
+        mn.copy_(i32(np.concatenate([[0], np.cumsum(nodes)])))
+        ai.copy_(i32(ai_now))
+        an.copy_(i32(np.concatenate([np.asarray(p, dtype=int) for p in paths])))
+        rng = np.random.default_rng(step)
+        for a, b in lists:
+            p = rng.permutation(free)
+            a.copy_(i32(p[:len(a)]))
+            b.copy_(i32(p[len(a):2 * len(a)]))
+        want, ri, rv, rl, rf = ref.compact(f64(s.pool), *s.table, f64(mn).astype(int), ai_now,
+                                           f64(an).astype(int))
+        for a, b in lists:
+            want[f64(b).astype(int)] = want[f64(a).astype(int)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert s.cache.device_status() == ta.TA_OK
+        np.testing.assert_array_equal(f64(s.pool), want)
+        assert new[0].tolist() == ri and new[2].tolist() == rl and int(new[4]) == len(rf)
+        assert new[1][:ri[-1]].tolist() == rv and new[3][:len(rf)].tolist() == rf
