@@ -60,9 +60,9 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // ends of tokens, and the arithmetic is in pairs of float32.
 //
 // Measured: 9,478 tokens of 64 + 8 + 8 heads of 128, with norms and interleaved
-// pairs (388 MB): 61.3 us, 6.3 TB/s; without norm and rotation 59.9 us, so the
+// pairs (388 MB): 61.2 us, 6.3 TB/s; without norm and rotation 59.9 us, so the
 // memory, in rows of 256 bytes, is what bounds it.  2,048 tokens of 32 + 8 + 8:
-// 11.2 us, bound by the look-ups and the latency of eight steps per warp.
+// 11.0 us, bound by the look-ups and the latency of eight steps per warp.
 template <int D, bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas) append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 16;           // lanes per row
@@ -357,11 +357,16 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactParams& p, int i)
 // CTA (b, 0) also writes sequence b's part of the new table, whose place it
 // finds by summing the pages the sequences before it keep.
 // Few sequences: bound by the chain of dependent loads (tables, nodes, pages,
-// rows), so the independent ones are issued together; many: by the memory, as a
-// row is pieces of d * 2 bytes a page's head apart.  The registers leave room for
-// four CTAs per SM.  Measured: 512 sequences, paths of up to 24 nodes, 8 kv heads
-// of 128: 12.2 us (16.5 with 16 rows in flight per thread and two CTAs per SM),
-// 4.1 TB/s; 32 sequences: 3.8 us.
+// rows), so the independent ones are issued together.  More: by the batches of
+// the longest paths, as a batch's loads wait for the stores before it (512
+// sequences, clock stamps: tables and nodes 4,500 cycles, then 3,700 for paths of
+// up to 6 nodes, 9,300 up to 12, 12,700 up to 18, 16,900 up to 24).  Many
+// thousands: by the tables, which every CTA reads whole, work that grows with the
+// square of the batch.  The registers leave room for four CTAs per SM.
+// Measured: 512 sequences, paths of up to 24 nodes, 8 kv heads of 128: 12.2 us
+// (16.5 with 16 rows in flight per thread and two CTAs per SM), 4.1 TB/s; 32
+// sequences: 3.8 us; with trees of 8 nodes, 4,096 sequences 50 us, 16,384
+// sequences 596 us.
 __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const CompactParams p) {
   __shared__ long long s_src[kCompactThreads], s_dst[kCompactThreads];
   __shared__ int s_sum[kCompactThreads / 32];

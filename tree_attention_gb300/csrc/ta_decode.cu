@@ -32,11 +32,15 @@
 //   timing.
 //
 // Measured (h_q 64, h_kv 8, d 128, bf16, 64 sequences of 16 to 16,384 rows,
-// 880 MB): 131 to 134 us, 6.6 TB/s, the rate of a plain copy; 4 sequences of 33,000
-// rows: 83.2 us, 6.5 TB/s; one of 4,096 rows (16 kv heads): 11.1 us, of which 2
-// are the chain of loads before the first page and 3 the merges.  16 heads per
-// kv head run at 53 % of the memory rate (two tiles of heads leave 8 warps per
-// SM), 32 heads, whose pages two CTAs read, at 35 %.
+// 880 MB): 134 us, 6.6 TB/s, the rate of a plain copy; 4 sequences of 33,000
+// rows: 84.5 us, 6.4 TB/s; one of 4,096 rows (16 kv heads): 12.5 us, of which 2
+// are the chain of loads before the first page and 3 the merges; 256 of about 110
+// rows (h 32 / 8): 27 us, 66 % of the memory rate: 3 us before the first page, 16
+// for eight pages per warp, and 3 for the merges, as nearly every warp ends with
+// parts of two sequences and an SM with those of 13.  9 to 16 heads per kv head
+// run at 52 to 55 % of the memory rate (two tiles of heads leave 8 warps per SM);
+// above, every 16 heads' CTAs read the pages again: 32 heads 34 %, 40 heads 28 %,
+// 64 heads 23 %, 128 heads 13 %.
 #include <cuda_runtime.h>
 
 #include <atomic>
