@@ -1090,3 +1090,24 @@ def test_captured_compaction_and_copies_follow_their_inputs():
         np.testing.assert_array_equal(f64(s.pool), want)
         assert new[0].tolist() == ri and new[2].tolist() == rl and int(new[4]) == len(rf)
         assert new[1][:ri[-1]].tolist() == rv and new[3][:len(rf)].tolist() == rf
+
+
+def test_a_dropped_handles_table_outlives_its_calls():
+    """A table whose last references go with the handle."""
+    s = Setup([3000, 60], 8, 2, 128, seed=70, fill=0.0)
+    q = s.randn(2, 8, 128)
+    want = [t.clone() for t in s.cache.decode(q, 0.1)]
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    side = torch.cuda.Stream()
+    c = s.cache.with_table(*[i32(x) for x in s.table])
+    tables = [(t.data_ptr(), t.numel()) for t in (c.page_indptr, c.page_values, c.length_info)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    c.decode(q, 0.1, out=out, lse=lse, stream=side)
+    del c
+    others = [torch.full((n,), 99, dtype=torch.int32, device="cuda") for _ in range(8)
+              for _, n in tables]
+    assert not {o.data_ptr() for o in others} & {at for at, _ in tables}
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -34,8 +34,8 @@ struct Handle {
   size_t workspace_bytes;
   int device;
   at::ScalarType dtype;
-  at::Tensor workspace_tensor;
-  mutable std::vector<cudaStream_t> streams;   // that hold_workspace has seen
+  std::vector<at::Tensor> held;                // pages, table, workspace
+  mutable std::vector<cudaStream_t> streams;   // that the allocator knows they are used on
 };
 
 const char* const kCapsule = "tree_attention_gb300.cache";
@@ -93,15 +93,16 @@ int64_t length(const char* name, PyObject* o, int dim) {
 
 struct PythonError {};   // a Python exception is set
 
-// Keeps the workspace's memory from being reused, after the handle is gone,
-// before the work on ``stream`` is done: the caller never sees this tensor.  Not
-// on streams that torch did not make (their id is their address): they may be
-// destroyed before the memory is freed.
-void hold_workspace(const Handle& h, c10::cuda::CUDAStream stream) {
+// Keeps the memory of what the handle holds from being reused, after the handle
+// is gone, before the work on ``stream`` is done: it may have had the last
+// reference.  Not on streams that torch did not make (their id is their
+// address): they may be destroyed before the memory is freed.
+void hold_on(const Handle& h, c10::cuda::CUDAStream stream) {
   cudaStream_t s = stream.stream();
+  if (stream.id() != 0 && stream.id() == reinterpret_cast<int64_t>(s)) return;
   if (std::find(h.streams.begin(), h.streams.end(), s) != h.streams.end()) return;
-  if (stream.id() == 0 || stream.id() != reinterpret_cast<int64_t>(s))
-    c10::cuda::CUDACachingAllocator::recordStream(h.workspace_tensor.storage().data_ptr(), stream);
+  for (const at::Tensor& t : h.held)
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), stream);
   h.streams.push_back(s);
 }
 
@@ -114,7 +115,7 @@ void* stream_of(const Handle& h, PyObject* o) {
   }
   if (o == Py_None) {
     const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(h.device);
-    hold_workspace(h, stream);
+    hold_on(h, stream);
     return stream.stream();
   }
   if (THPStream_Check(o)) {
@@ -124,7 +125,7 @@ void* stream_of(const Handle& h, PyObject* o) {
         static_cast<c10::DeviceType>(t->device_type));
     if (stream.device_index() != h.device)
       throw std::invalid_argument("stream must be on the device of the cache");
-    hold_workspace(h, stream);
+    hold_on(h, stream);
     return stream.stream();
   }
   PyObject* a = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
@@ -184,7 +185,8 @@ PyObject* make_handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
   auto ptr = [&](int i) { return static_cast<int32_t*>(THPVariable_Unpack(a[i]).data_ptr()); };
   Handle* h = new Handle{*static_cast<ta_cache_dims*>(dims), pages.data_ptr(), ptr(2), ptr(3), ptr(4),
                          ws.data_ptr(), static_cast<size_t>(ws.nbytes()),
-                         static_cast<int>(pages.get_device()), pages.scalar_type(), ws, {}};
+                         static_cast<int>(pages.get_device()), pages.scalar_type(), {}, {}};
+  for (int i = 1; i < 6; ++i) h->held.push_back(THPVariable_Unpack(a[i]));
   PyObject* c = PyCapsule_New(h, kCapsule, [](PyObject* o) {
     delete static_cast<Handle*>(PyCapsule_GetPointer(o, kCapsule));
   });
