@@ -307,6 +307,23 @@ def test_binding_refuses_what_is_no_tensor_or_no_handle(lib, call):
         call(ta._compiled(), _handle(_dims()))
 
 
+def test_binding_refuses_tensors_without_memory(lib):
+    """torch throws on the address of a batched tensor: a Python error, not the
+    end of the process."""
+    import torch
+    d, z = _dims(), torch.zeros(4, dtype=torch.int32)
+    said = []
+
+    def make(pages):
+        with pytest.raises(RuntimeError) as e:
+            ta._compiled().handle(ctypes.addressof(d), pages, z, z, z, z)
+        said.append(str(e.value))
+        return pages
+
+    torch.func.vmap(make)(torch.zeros((2, 12, 2, 2, 16, 128), dtype=torch.bfloat16))
+    assert len(said) == 1
+
+
 # --------------------------------------------------------------------------
 # building the extension module
 # --------------------------------------------------------------------------

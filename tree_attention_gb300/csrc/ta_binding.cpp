@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <memory>
 #include <sstream>
 #include <stdexcept>
 #include <vector>
@@ -149,13 +150,13 @@ const Handle& handle(PyObject* o) {
   return *static_cast<Handle*>(p);
 }
 
-// Runs ``body`` on ``n`` arguments, of which there must be ``want``; the status
-// it returns goes to Python as an int, its exceptions as Python's.
+// Runs ``body`` on ``n`` arguments, of which there must be ``want``; it returns a
+// Python object, and its exceptions become Python's.
 template <typename F>
-PyObject* call(Py_ssize_t n, Py_ssize_t want, F body) {
+PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F body) {
   try {
     if (n != want) throw std::invalid_argument("wrong number of arguments");
-    return PyLong_FromLong(body());
+    return body();
   } catch (const PythonError&) {
   } catch (const std::invalid_argument& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
@@ -165,33 +166,36 @@ PyObject* call(Py_ssize_t n, Py_ssize_t want, F body) {
   return nullptr;
 }
 
+// The same for a ``body`` that returns a status.
+template <typename F>
+PyObject* call(Py_ssize_t n, Py_ssize_t want, F body) {
+  return guarded(n, want, [&] { return PyLong_FromLong(body()); });
+}
+
 bool given(PyObject* o) { return o != Py_None; }
 
 // handle(dims address, pages, page_indptr, page_values, length_info, workspace)
 PyObject* make_handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_ValueError, "wrong number of arguments");
-    return nullptr;
-  }
-  void* dims = PyLong_AsVoidPtr(a[0]);
-  if (!dims) return nullptr;
-  for (int i = 1; i < 6; ++i)
-    if (!THPVariable_Check(a[i])) {
-      PyErr_SetString(PyExc_ValueError, "tensors expected");
-      return nullptr;
+  return guarded(n, 6, [&] {
+    const void* dims = PyLong_AsVoidPtr(a[0]);
+    if (PyErr_Occurred()) throw PythonError();
+    if (!dims) throw std::invalid_argument("the address of the dims expected");
+    std::vector<at::Tensor> t;
+    for (int i = 1; i < 6; ++i) {
+      if (!THPVariable_Check(a[i])) throw std::invalid_argument("tensors expected");
+      t.push_back(THPVariable_Unpack(a[i]));
     }
-  const at::Tensor& pages = THPVariable_Unpack(a[1]);
-  const at::Tensor& ws = THPVariable_Unpack(a[5]);
-  auto ptr = [&](int i) { return static_cast<int32_t*>(THPVariable_Unpack(a[i]).data_ptr()); };
-  Handle* h = new Handle{*static_cast<ta_cache_dims*>(dims), pages.data_ptr(), ptr(2), ptr(3), ptr(4),
-                         ws.data_ptr(), static_cast<size_t>(ws.nbytes()),
-                         static_cast<int>(pages.get_device()), pages.scalar_type(), {}, {}};
-  for (int i = 1; i < 6; ++i) h->held.push_back(THPVariable_Unpack(a[i]));
-  PyObject* c = PyCapsule_New(h, kCapsule, [](PyObject* o) {
-    delete static_cast<Handle*>(PyCapsule_GetPointer(o, kCapsule));
+    auto ints = [&](int i) { return static_cast<int32_t*>(t[i].data_ptr()); };
+    std::unique_ptr<Handle> h(new Handle{
+        *static_cast<const ta_cache_dims*>(dims), t[0].data_ptr(), ints(1), ints(2), ints(3),
+        t[4].data_ptr(), static_cast<size_t>(t[4].nbytes()), static_cast<int>(t[0].get_device()),
+        t[0].scalar_type(), t, {}});
+    PyObject* c = PyCapsule_New(h.get(), kCapsule, [](PyObject* o) {
+      delete static_cast<Handle*>(PyCapsule_GetPointer(o, kCapsule));
+    });
+    if (c) h.release();
+    return c;
   });
-  if (!c) delete h;
-  return c;
 }
 
 // append(handle, q, k, v, append_indptr, positions, rope address, q_weight,
