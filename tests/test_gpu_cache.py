@@ -257,6 +257,44 @@ def test_decode_values_that_are_not_finite(h_q, h_kv, d, dtype, ramp):
     assert torch.equal(out.nan_to_num(7, inf, -inf), expect.nan_to_num(7, inf, -inf))
 
 
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", [(8, 2, 128, "bf16"), (36, 2, 64, "fp16")])
+def test_decode_scores_that_are_not_finite(h_q, h_kv, d, dtype):
+    """NaN queries and keys reach their heads and kv heads only; a row whose
+    score is -inf counts as if it were not there."""
+    kv = [40, 2000, 17, 600]
+    s = Setup(kv, h_q, h_kv, d, dtype, seed=20, fill=0.0)
+    q = s.randn(len(kv), h_q, d)
+    q[3] = q[3].abs()
+    base = [t.clone() for t in s.cache.decode(q, d ** -0.5)]
+    g, nan = h_q // h_kv, torch.zeros((len(kv), h_q), dtype=torch.bool)
+    bad_q = q.clone()
+    bad_q[1, 3, 7] = float("nan")
+    nan[1, 3] = True
+    for b, r, h in ((0, 39, 1), (1, 999, 1)):
+        pid, sl = ref.slots(*s.table, b)
+        s.pool[pid[r], 0, h, sl[r], 5] = float("nan")
+        nan[b, h * g:(h + 1) * g] = True
+    # the last 100 rows of sequence 3, kv head 0; the same sequence without them
+    pid, sl = ref.slots(*s.table, 3)
+    cut = Setup([500], h_q, h_kv, d, dtype, seed=21, fill=0.0)
+    to, tl = ref.slots(*cut.table, 0)
+    cut.pool[to, :, :, tl] = s.pool[pid[:500], :, :, sl[:500]]
+    s.pool[pid[500:], 0, 0, sl[500:], 3] = -float("inf")
+    out, lse = s.cache.decode(bad_q, d ** -0.5)
+    nan = nan.cuda()
+    assert torch.equal(torch.isnan(lse), nan) and torch.equal(torch.isnan(out).all(-1), nan)
+    same = ~nan
+    same[3, :g] = False
+    assert torch.equal(out[same], base[0][same]) and torch.equal(lse[same], base[1][same])
+    ro, rl, mag, smag = ref.decode(f64(q[3:]), f64(cut.pool), *cut.table, d ** -0.5)
+    half = torch.finfo(s.dtype).eps / 2
+    serr = (d + 4) * 2.0 ** -23 * smag
+    tol = half * np.abs(ro) + (half ** 2 + 2.0 ** -18 + 2 * serr[..., None]) * mag \
+        + torch.finfo(s.dtype).smallest_normal * half * 2
+    assert (np.abs(f64(out[3:]) - ro) <= tol)[:, :g].all()
+    assert (np.abs(f64(lse[3:]) - rl) <= serr + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl))[:, :g].all()
+
+
 def test_decode_page_outside_the_pool_reads_zeros():
     s = Setup([50, 20], 4, 2, 128, seed=3)
     s.values[1], s.values[4] = 10 ** 6, -1
