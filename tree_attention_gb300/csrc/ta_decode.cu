@@ -163,7 +163,7 @@ struct Acc {
   // is the sum of the states' infinities and NaNs, if there are any.
   template <typename F>
   __device__ __forceinline__ void keep_infinities(int from, int to, int step, F o_of) {
-    if (__builtin_expect(finite(o.x) && finite(o.y) && finite(o.z) && finite(o.w), 1)) return;
+    if (__builtin_expect(finite((o.x + o.y) + (o.z + o.w)), 1)) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int k = from; k < to; k += step) {
@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       // need not give that, as a weight's second part may be zero or negative and
       // small weights and factors round to zero.  The segment's values are read
       // again, a tile of elements at a time, with weights of one.  (To look at every
-      // value before its product cost 1 to 5 %, to look at the sums 0.2 us a call)
+      // value before its product cost 1 to 5 %, to look at the sums here and where
+      // parts are merged 0.4 us a call at most)
       float2 odd = make_float2(0.f, 0.f);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
