@@ -224,6 +224,10 @@ def prepare(case, seed):
         s["sm_scale"] = 1.0 / math.sqrt(d + rope)
         s["out"] = torch.empty((nq, h, d), dtype=dt, device=DEV)
         s["lse"] = torch.empty((nq, h), dtype=torch.float32, device=DEV)
+        if own:
+            import tree_attention_gb300 as ta
+            dims = ta.make_expanded_dims(s["q"], s["k"], s["q_indptr"])
+            s["workspace"] = torch.zeros(ta.expanded_workspace_size(dims), dtype=torch.uint8, device=DEV)
         return s
     rank = case["rank"]
     s.update(_table(case, size["kv"], seed, gen))
@@ -271,8 +275,8 @@ def run(s):
     if own:
         if op == "expand":
             import tree_attention_gb300 as ta
-            ta.tree_attn_expanded(s["q"], s["k"], s["k_rope"], s["v"], s["q_indptr"], s["kv_indptr"],
-                                  s["sm_scale"], out=s["out"], lse=s["lse"])
+            ta.tree_attn_expanded(s["q"], s["q_indptr"], s["k"], s["k_rope"], s["v"], s["kv_indptr"],
+                                  s["out"], s["lse"], s["sm_scale"], s["workspace"])
             return s["out"], s["lse"]
         c = s["cache"]
         if op == "append":
