@@ -417,6 +417,174 @@ ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int3
                                int32_t n, const ta_cache_dims* dims, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* ---- Latent attention --------------------------------------------------------
+ * Attention whose keys and values come from one shared vector a token: a latent
+ * of ``rank`` elements and, behind it, a rotary key of ``rope_dim`` elements
+ * that all heads share.  The pages have no counterpart; page table, tree layout
+ * and base-2 LSE are those above.  Two forms:
+ *   absorbed  the projection of the latent to a head's keys is applied to its
+ *             queries instead (q = [q_nope W_k^T | q_rope]) and that to its
+ *             values to the output, so that all heads read the row as it is:
+ *               s_j = sm_scale q . row_j,  out = sum_j softmax(s)_j latent_j.
+ *             It runs over a paged latent cache (one token per sequence, draft
+ *             trees), whose rows are h_q times smaller than keys and values;
+ *   expanded  keys and values per head (the latents times both projections),
+ *             with fewer operations per pair of tokens, for prompts
+ *             (tree_attn_expanded).
+ * The cache:
+ *   pages        [num_pages, 16, rank + rope_dim] dtype, one row per token
+ *   page_indptr, page_values, length_info   as for tree_attn_append_paged
+ * Sizes:
+ *   batch_size   B, 1..16384
+ *   h_q          heads, 1..128
+ *   rank         256 or 512
+ *   rope_dim     16, 32, 48 or 64
+ *   dtype, num_pages, nnz_pages   as in ta_cache_dims */
+typedef struct {
+  int32_t batch_size;
+  int32_t h_q;
+  int32_t rank;
+  int32_t rope_dim;
+  ta_dtype dtype;
+  int32_t num_pages;
+  int32_t nnz_pages;
+} ta_latent_dims;
+
+/* Bytes of device workspace each call on a latent cache needs (a multiple of
+ * 256; 0 on invalid or unsupported dims).  tree_attn_cache_workspace_size's
+ * rules apply: 256-byte aligned, zero-filled once, one workspace per set of
+ * calls that may overlap on the GPU, any dims may take turns on one that is
+ * large enough.  It holds the device status word, a mark per page of the pool and
+ * the partial states of sequences that several SMs share. */
+size_t tree_attn_latent_workspace_size(const ta_latent_dims* dims);
+
+/* Appends tokens to a latent cache.  The page table describes the cache after
+ * the call: the last append_indptr[b+1] - append_indptr[b] rows of sequence b
+ * receive its new tokens, in order.
+ *   latent         [total_new, rank], latent_stride elements from token to token
+ *   k_rope         [total_new, rope_dim], k_rope_stride from token to token
+ *   q_rope         the queries' rotary parts [total_new, h_q, rope_dim],
+ *                  q_token_stride and q_head_stride elements apart; NULL (with
+ *                  q_out) where there are none
+ *   append_indptr  [B+1] int32, from 0 to total_new
+ *   positions      [total_new] int32 (may be NULL iff rope is NULL)
+ *   weight         [rank] dtype, or NULL for no norm:
+ *                  x <- x * w / sqrt(mean(x^2) + norm_eps) of the latent
+ *   norm_eps       finite, >= 0
+ *   rope           a filled ta_rope with rotary_dim == rope_dim, or NULL: the
+ *                  rotation of k_rope and of every head's q_rope
+ *   q_out          [total_new, h_q, rope_dim] with strides of its own (the last
+ *                  elements of the absorbed queries, say); it may be q_rope
+ *                  itself with the same strides, else it overlaps no input
+ *   rows_out       [total_new, rank + rope_dim] contiguous, or NULL: the rows
+ *                  written to the cache, in order (for the expanded form)
+ * All strides are multiples of 8, at least a row (a head's rows at least rope_dim
+ * apart, a token's heads within its stride or the other way round); pointers
+ * 16-byte aligned.  Arithmetic, rounding and the treatment of inconsistent
+ * tables are those of tree_attn_append_paged.  Asynchronous on stream. */
+ta_status tree_attn_append_latent(const void* latent, int64_t latent_stride, const void* k_rope,
+                                  int64_t k_rope_stride, const void* q_rope,
+                                  int64_t q_token_stride, int64_t q_head_stride,
+                                  int32_t total_new, const int32_t* append_indptr,
+                                  const int32_t* positions, const void* weight, float norm_eps,
+                                  const ta_rope* rope, void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  void* q_out, int64_t q_out_token_stride,
+                                  int64_t q_out_head_stride, void* rows_out,
+                                  const ta_latent_dims* dims, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Absorbed attention of one token per sequence over a latent cache: q [B, h_q,
+ * rank + rope_dim], out [B, h_q, rank], base-2 lse [B, h_q] (a sequence without
+ * rows gets out = 0 and lse = -inf).  A page index outside the pool reads zeros,
+ * slots past a sequence's length are never used, a row whose score is -inf
+ * counts as if it were not there, one whose score is NaN or +inf makes its head's
+ * out NaN.  Weights are rounded to dtype before they meet the values (their sum
+ * is of the rounded ones), all else is float32.  The result does not depend on timing.
+ * Inconsistent page tables are reported by tree_attn_device_status and nothing
+ * is computed.  q, pages and out 16-byte aligned.  Asynchronous on stream. */
+ta_status tree_attn_decode_latent(const void* q, const void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  void* out, float* lse, float sm_scale,
+                                  const ta_latent_dims* dims, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Absorbed tree attention over a latent cache: q rows, trees and mask are those
+ * of tree_attn_paged (q_indptr, mn_indptr [B+1] from 0 to total_q, total_tree;
+ * tree_order [total_tree][2]; the last nodes' rows are the q rows, the last rows
+ * of a sequence its nodes), with q [total_q, h_q, rank + rope_dim], out
+ * [total_q, h_q, rank], lse [total_q, h_q]; all else is as for
+ * tree_attn_decode_latent.  What a q row does not see has no part in its result,
+ * whatever it holds.  total_q * h_q must fit an int32. */
+ta_status tree_attn_latent(const void* q, const int32_t* q_indptr, int32_t total_q,
+                           const void* pages, const int32_t* page_indptr,
+                           const int32_t* page_values, const int32_t* length_info,
+                           const int32_t* mn_indptr, const int32_t* tree_order,
+                           int32_t total_tree, void* out, float* lse, float sm_scale,
+                           const ta_latent_dims* dims, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* tree_attn_compact_paged and tree_attn_copy_pages for a latent cache. */
+ta_status tree_attn_compact_latent(void* pages, const int32_t* page_indptr,
+                                   const int32_t* page_values, const int32_t* length_info,
+                                   const int32_t* mn_indptr, const int32_t* accept_indptr,
+                                   const int32_t* accept_nodes, int32_t total_accept,
+                                   int32_t* new_page_indptr, int32_t* new_page_values,
+                                   int32_t* new_length_info, int32_t* freed_pages,
+                                   int32_t* num_freed, const ta_latent_dims* dims,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+ta_status tree_attn_copy_pages_latent(void* pages, const int32_t* src_pages,
+                                      const int32_t* dst_pages, int32_t n,
+                                      const ta_latent_dims* dims, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Sizes of tree_attn_expanded:
+ *   batch_size   B, 1..16384
+ *   total_q, total_kv   rows (q_indptr[B], kv_indptr[B])
+ *   heads        1..1024, total_q * heads <= INT32_MAX
+ *   head_dim     64 or 128: elements of k (without the rotary part) and of v
+ *   rope_dim     16, 32, 48 or 64 */
+typedef struct {
+  int32_t batch_size;
+  int32_t total_q;
+  int32_t total_kv;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t rope_dim;
+  ta_dtype dtype;
+} ta_expanded_dims;
+
+/* Bytes of device workspace tree_attn_expanded needs (a multiple of 256; 0 on
+ * invalid or unsupported dims): the device status word, zero-filled once.  Calls
+ * that overlap may share it. */
+size_t tree_attn_expanded_workspace_size(const ta_expanded_dims* dims);
+
+/* Causal attention in the expanded form: the q rows of sequence b are its last
+ * kv rows and see the rows up to their own (0 <= qo <= kv; the rows before them
+ * are a part that was computed earlier),
+ *   s = sm_scale (q[:head_dim] . k + q[head_dim:] . k_rope),  out = softmax(s) v.
+ *   q        [total_q, heads, head_dim + rope_dim]
+ *   k, v     [total_kv, heads, head_dim]
+ *   k_rope   [total_kv, rope_dim], shared by the heads
+ *   out      [total_q, heads, head_dim] contiguous (written)
+ *   lse      [total_q, heads] float32, base 2 (written); states over further
+ *            rows merge with it (tree_attn_merge_states)
+ * Every *_token_stride and *_head_stride in elements, multiples of 8, at least a
+ * row, so that k and v may be views of one projection of the latents.  What a
+ * q row does not see has no part in its result, whatever it holds.  Weights are
+ * rounded to dtype before they meet the values (their sum is of the rounded
+ * ones), all else is float32.  A row whose score is -inf counts as if it were not
+ * there; one of NaN or +inf makes the result NaN.  Inconsistent indptr arrays are
+ * reported by tree_attn_device_status and nothing is computed.  Pointers 16-byte
+ * aligned.  Asynchronous on stream. */
+ta_status tree_attn_expanded(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const int32_t* q_indptr, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                             const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             const int32_t* kv_indptr, void* out, float* lse, float sm_scale,
+                             const ta_expanded_dims* dims, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* ---- Split-KV ------------------------------------------------------------
  * The same tree attention with the kv tiles of long (sequence, q tile) pairs
  * cut into chunks that run as separate work items, so that a batch of few

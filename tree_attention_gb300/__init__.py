@@ -2,8 +2,8 @@
 library (C ABI in ``include/tree_attn.h``).
 
 The binding only marshals arguments: tensors are passed to the C entry points
-as raw device pointers (by ctypes, or, for the calls of ``PagedCache``, by the
-extension module ``_binding``), every step of the computation runs in the
+as raw device pointers (by ctypes, or, for the calls of ``PagedCache`` and
+``LatentCache``, by the extension module ``_binding``), every step of the computation runs in the
 library's CUDA kernels, and there is no CPU fallback.  If the library has not been
 built, importing works but every call raises ``RuntimeError``.
 
@@ -29,7 +29,9 @@ __all__ = [
     "TreeAttention", "PagedDims", "make_paged_dims", "paged_workspace_size", "tree_attn_paged",
     "MAX_CHUNKS", "split_workspace_size", "tree_attn_split", "merge_states", "last_cuda_error",
     "folds_rotation", "noalloc_device_status", "set_wait_hooks", "auto_split_chunks",
-    "set_scheduler", "CacheDims", "Rope", "PagedCache", "cache_workspace_size",
+    "set_scheduler", "CacheDims", "Rope", "PagedCache", "cache_workspace_size", "LatentDims",
+    "LatentCache", "latent_workspace_size", "ExpandedDims", "make_expanded_dims",
+    "expanded_workspace_size", "tree_attn_expanded",
 ]
 
 TA_OK = 0
@@ -75,6 +77,20 @@ class CacheDims(ctypes.Structure):
                 ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32),
                 ("nnz_pages", ctypes.c_int32)]
+
+
+class LatentDims(ctypes.Structure):
+    _fields_ = [("batch_size", ctypes.c_int32), ("h_q", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32),
+                ("nnz_pages", ctypes.c_int32)]
+
+
+class ExpandedDims(ctypes.Structure):
+    _fields_ = [("batch_size", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("total_kv", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int)]
 
 
 class _RopeStruct(ctypes.Structure):
@@ -163,6 +179,28 @@ def lib() -> ctypes.CDLL:
     L.tree_attn_compact_paged.restype = ctypes.c_int
     L.tree_attn_copy_pages.argtypes = [vp, i32p, i32p, i32, cdims, vp, sz, vp]
     L.tree_attn_copy_pages.restype = ctypes.c_int
+    ldims, edims = ctypes.POINTER(LatentDims), ctypes.POINTER(ExpandedDims)
+    L.tree_attn_latent_workspace_size.argtypes = [ldims]
+    L.tree_attn_latent_workspace_size.restype = sz
+    L.tree_attn_append_latent.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, i32p, i32p, vp, f32,
+                                          rope, vp, i32p, i32p, i32p, vp, i64, i64, vp, ldims, vp,
+                                          sz, vp]
+    L.tree_attn_append_latent.restype = ctypes.c_int
+    L.tree_attn_decode_latent.argtypes = [vp, vp, i32p, i32p, i32p, vp, vp, f32, ldims, vp, sz, vp]
+    L.tree_attn_decode_latent.restype = ctypes.c_int
+    L.tree_attn_latent.argtypes = [vp, i32p, i32, vp, i32p, i32p, i32p, i32p, i32p, i32, vp, vp, f32,
+                                   ldims, vp, sz, vp]
+    L.tree_attn_latent.restype = ctypes.c_int
+    L.tree_attn_compact_latent.argtypes = [vp, i32p, i32p, i32p, i32p, i32p, i32p, i32, i32p, i32p,
+                                           i32p, i32p, i32p, ldims, vp, sz, vp]
+    L.tree_attn_compact_latent.restype = ctypes.c_int
+    L.tree_attn_copy_pages_latent.argtypes = [vp, i32p, i32p, i32, ldims, vp, sz, vp]
+    L.tree_attn_copy_pages_latent.restype = ctypes.c_int
+    L.tree_attn_expanded_workspace_size.argtypes = [edims]
+    L.tree_attn_expanded_workspace_size.restype = sz
+    L.tree_attn_expanded.argtypes = [vp, i64, i64, i32p, vp, i64, i64, vp, i64, vp, i64, i64, i32p, vp,
+                                     vp, f32, edims, vp, sz, vp]
+    L.tree_attn_expanded.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -531,24 +569,12 @@ def _compiled():
     return _binding_module
 
 
-class PagedCache:
-    """A paged KV cache and its page table, with the calls of a decoding loop
-    on it (``include/tree_attn.h``, "Serving a paged KV cache").
+class _Cache:
+    """What ``PagedCache`` and ``LatentCache`` have in common: the pool, its page
+    table and the workspace.  A subclass names its dims' size function and the
+    extension module's calls."""
 
-    ``pages [num_pages, 2, h_kv, 16, d]`` and the int32 table ``page_indptr
-    [B+1]``, ``page_values``, ``length_info [B]`` are CUDA tensors, held and not
-    copied: their contents may change between calls.  ``h_q`` is the number of
-    query heads.  The handle owns a workspace, so calls on it that may overlap
-    on the GPU need handles of their own (``with_table(..., workspace=None)``).
-    ``workspace`` takes another handle's, whatever that one's heads and pool,
-    where it is large enough; where it is not, a new one is made.  Every call is
-    asynchronous on ``stream`` (default: torch's current stream), and
-    ``device_status`` reports inconsistent tables.  The handle may be dropped
-    while its calls run, unless on a stream that is not one of torch's."""
-
-    def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, workspace=None):
-        if pages.dim() != 5 or pages.shape[1] != 2 or pages.shape[3] != 16:
-            raise ValueError("pages must be [num_pages, 2, h_kv, 16, head_dim]")
+    def _attach(self, pages, page_indptr, page_values, length_info, dims, workspace):
         _check_dev("pages", pages)
         for name, t in (("page_indptr", page_indptr), ("page_values", page_values),
                         ("length_info", length_info)):
@@ -561,16 +587,13 @@ class PagedCache:
         self.page_values, self.length_info = page_values, length_info
         self.dtype, self.device = pages.dtype, pages.device
         self._dev = pages.get_device()
-        self.batch_size, self.h_q = length_info.numel(), int(h_q)
-        self.h_kv, self.head_dim = pages.shape[2], pages.shape[4]
-        self.dims = CacheDims(batch_size=self.batch_size, h_q=self.h_q, h_kv=self.h_kv,
-                              head_dim=self.head_dim, dtype=_dtype_code(pages.dtype),
-                              num_pages=pages.shape[0], nnz_pages=page_values.numel())
+        self.batch_size = length_info.numel()
+        self.dims = dims()
         self._binding = _compiled()
         with torch.cuda.device(self._dev):
-            need = cache_workspace_size(self.dims)
+            need = self._workspace_size(self.dims)
         if need == 0:
-            raise TreeAttnError(TA_ERR_UNSUPPORTED, "tree_attn_cache_workspace_size")
+            raise TreeAttnError(TA_ERR_UNSUPPORTED, self._size_name)
         if workspace is not None:
             _check_dev("workspace", workspace)
             if workspace.get_device() != self._dev:
@@ -588,15 +611,10 @@ class PagedCache:
         self.workspace = workspace
         # the addresses of these tensors are what the calls pass, so they stay
         self._held = (pages, page_indptr, page_values, length_info, workspace)
-        self._handle = self._binding.handle(ctypes.addressof(self.dims), pages, page_indptr,
-                                            page_values, length_info, workspace)
-
-    def with_table(self, page_indptr, page_values, length_info, workspace="same"):
-        """A handle on the same pool with another page table (as ``compact``
-        writes); it shares this handle's workspace where that is large enough,
-        unless given another one (None: a new one)."""
-        return PagedCache(self.pages, page_indptr, page_values, length_info, self.h_q,
-                          self.workspace if isinstance(workspace, str) else workspace)
+        self._handle = getattr(self._binding, self._prefix + "handle")(
+            ctypes.addressof(self.dims), pages, page_indptr, page_values, length_info, workspace)
+        self._compact = getattr(self._binding, self._prefix + "compact")
+        self._copy_pages = getattr(self._binding, self._prefix + "copy_pages")
 
     def _empty(self, shape, dtype, stream):
         """A new output, from the pool of the stream that the call runs on."""
@@ -609,6 +627,78 @@ class PagedCache:
                       else torch.cuda.default_stream(self.device))
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def compact(self, mn_indptr, accept_indptr, accept_nodes, *, new_page_indptr=None,
+                new_page_values=None, new_length_info=None, freed_pages=None, num_freed=None,
+                stream=None):
+        """Keep the accepted nodes (``accept_nodes`` ascending per sequence) of
+        the trees that end the sequences (``mn_indptr``), moving their rows down
+        behind the prefix.  Returns the new ``page_indptr, page_values,
+        length_info`` (for ``with_table``), the freed pages and their number
+        ``[1]``, all on the device."""
+        i32, b, nnz = torch.int32, self.batch_size, self.page_values.numel()
+        if new_page_indptr is None:
+            new_page_indptr = self._empty(b + 1, i32, stream)
+        if new_page_values is None:
+            new_page_values = self._empty(nnz, i32, stream)
+        if new_length_info is None:
+            new_length_info = self._empty(b, i32, stream)
+        if freed_pages is None:
+            freed_pages = self._empty(nnz, i32, stream)
+        if num_freed is None:
+            num_freed = self._empty(1, i32, stream)
+        st = self._compact(self._handle, mn_indptr, accept_indptr, accept_nodes, new_page_indptr,
+                           new_page_values, new_length_info, freed_pages, num_freed, stream)
+        if st != TA_OK:
+            raise TreeAttnError(st, self._names[0])
+        return new_page_indptr, new_page_values, new_length_info, freed_pages, num_freed
+
+    def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
+        """``pages[dst_pages[i]] = pages[src_pages[i]]``; no destination may be
+        another pair's source or destination."""
+        st = self._copy_pages(self._handle, src_pages, dst_pages, stream)
+        if st != TA_OK:
+            raise TreeAttnError(st, self._names[1])
+
+    def device_status(self, stream=None) -> int:
+        """Synchronise the stream and return (and clear) the device status."""
+        return device_status(self.workspace, stream)
+
+
+class PagedCache(_Cache):
+    """A paged KV cache and its page table, with the calls of a decoding loop
+    on it (``include/tree_attn.h``, "Serving a paged KV cache").
+
+    ``pages [num_pages, 2, h_kv, 16, d]`` and the int32 table ``page_indptr
+    [B+1]``, ``page_values``, ``length_info [B]`` are CUDA tensors, held and not
+    copied: their contents may change between calls.  ``h_q`` is the number of
+    query heads.  The handle owns a workspace, so calls on it that may overlap
+    on the GPU need handles of their own (``with_table(..., workspace=None)``).
+    ``workspace`` takes another handle's, whatever that one's heads and pool,
+    where it is large enough; where it is not, a new one is made.  Every call is
+    asynchronous on ``stream`` (default: torch's current stream), and
+    ``device_status`` reports inconsistent tables.  The handle may be dropped
+    while its calls run, unless on a stream that is not one of torch's."""
+
+    _prefix, _size_name = "", "tree_attn_cache_workspace_size"
+    _names = ("tree_attn_compact_paged", "tree_attn_copy_pages")
+    _workspace_size = staticmethod(cache_workspace_size)
+
+    def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, workspace=None):
+        if pages.dim() != 5 or pages.shape[1] != 2 or pages.shape[3] != 16:
+            raise ValueError("pages must be [num_pages, 2, h_kv, 16, head_dim]")
+        self.h_q, self.h_kv, self.head_dim = int(h_q), pages.shape[2], pages.shape[4]
+        self._attach(pages, page_indptr, page_values, length_info, lambda: CacheDims(
+            batch_size=length_info.numel(), h_q=self.h_q, h_kv=self.h_kv, head_dim=self.head_dim,
+            dtype=_dtype_code(pages.dtype), num_pages=pages.shape[0],
+            nnz_pages=page_values.numel()), workspace)
+
+    def with_table(self, page_indptr, page_values, length_info, workspace="same"):
+        """A handle on the same pool with another page table (as ``compact``
+        writes); it shares this handle's workspace where that is large enough,
+        unless given another one (None: a new one)."""
+        return PagedCache(self.pages, page_indptr, page_values, length_info, self.h_q,
+                          self.workspace if isinstance(workspace, str) else workspace)
 
     def append(self, q, k, v, append_indptr, positions=None, *, rope: Optional[Rope] = None,
                q_weight=None, k_weight=None, norm_eps: float = 1e-6, q_out=None, stream=None):
@@ -640,39 +730,146 @@ class PagedCache:
             raise TreeAttnError(st, "tree_attn_decode_paged")
         return out, lse
 
-    def compact(self, mn_indptr, accept_indptr, accept_nodes, *, new_page_indptr=None,
-                new_page_values=None, new_length_info=None, freed_pages=None, num_freed=None,
-                stream=None):
-        """Keep the accepted nodes (``accept_nodes`` ascending per sequence) of
-        the trees that end the sequences (``mn_indptr``), moving their rows down
-        behind the prefix.  Returns the new ``page_indptr, page_values,
-        length_info`` (for ``with_table``), the freed pages and their number
-        ``[1]``, all on the device."""
-        i32, b, nnz = torch.int32, self.batch_size, self.page_values.numel()
-        if new_page_indptr is None:
-            new_page_indptr = self._empty(b + 1, i32, stream)
-        if new_page_values is None:
-            new_page_values = self._empty(nnz, i32, stream)
-        if new_length_info is None:
-            new_length_info = self._empty(b, i32, stream)
-        if freed_pages is None:
-            freed_pages = self._empty(nnz, i32, stream)
-        if num_freed is None:
-            num_freed = self._empty(1, i32, stream)
-        st = self._binding.compact(self._handle, mn_indptr, accept_indptr, accept_nodes,
-                                   new_page_indptr, new_page_values, new_length_info, freed_pages,
-                                   num_freed, stream)
-        if st != TA_OK:
-            raise TreeAttnError(st, "tree_attn_compact_paged")
-        return new_page_indptr, new_page_values, new_length_info, freed_pages, num_freed
 
-    def copy_pages(self, src_pages, dst_pages, stream=None) -> None:
-        """``pages[dst_pages[i]] = pages[src_pages[i]]``; no destination may be
-        another pair's source or destination."""
-        st = self._binding.copy_pages(self._handle, src_pages, dst_pages, stream)
-        if st != TA_OK:
-            raise TreeAttnError(st, "tree_attn_copy_pages")
+def latent_workspace_size(dims: LatentDims) -> int:
+    return int(lib().tree_attn_latent_workspace_size(ctypes.byref(dims)))
 
-    def device_status(self, stream=None) -> int:
-        """Synchronise the stream and return (and clear) the device status."""
-        return device_status(self.workspace, stream)
+
+class LatentCache(_Cache):
+    """A paged latent cache and its page table, with the calls of a decoding loop
+    on it (``include/tree_attn.h``, "Latent attention"): one row of ``rank``
+    latent elements and a rotary key per token, which all heads share.
+
+    ``pages [num_pages, 16, rank + rope_dim]``, the table and the workspace are
+    held as ``PagedCache`` holds its own; everything said there holds here."""
+
+    _prefix, _size_name = "latent_", "tree_attn_latent_workspace_size"
+    _names = ("tree_attn_compact_latent", "tree_attn_copy_pages_latent")
+    _workspace_size = staticmethod(latent_workspace_size)
+
+    def __init__(self, pages, page_indptr, page_values, length_info, h_q: int, rank: int,
+                 workspace=None):
+        if pages.dim() != 3 or pages.shape[1] != 16:
+            raise ValueError("pages must be [num_pages, 16, rank + rope_dim]")
+        self.h_q, self.rank, self.rope_dim = int(h_q), int(rank), pages.shape[2] - int(rank)
+        self._attach(pages, page_indptr, page_values, length_info, lambda: LatentDims(
+            batch_size=length_info.numel(), h_q=self.h_q, rank=self.rank, rope_dim=self.rope_dim,
+            dtype=_dtype_code(pages.dtype), num_pages=pages.shape[0],
+            nnz_pages=page_values.numel()), workspace)
+
+    def with_table(self, page_indptr, page_values, length_info, workspace="same"):
+        """A handle on the same pool with another page table (as ``compact``
+        writes); it shares this handle's workspace where that is large enough,
+        unless given another one (None: a new one)."""
+        return LatentCache(self.pages, page_indptr, page_values, length_info, self.h_q, self.rank,
+                           self.workspace if isinstance(workspace, str) else workspace)
+
+    def append(self, latent, k_rope, append_indptr, positions=None, *, q_rope=None,
+               rope: Optional[Rope] = None, weight=None, norm_eps: float = 1e-6, q_out=None,
+               rows_out=None, stream=None):
+        """Write new tokens' rows, ``latent [tokens, rank]`` after its norm (where
+        ``weight`` is given) and ``k_rope [tokens, rope_dim]`` after the rotation
+        (with ``rope``, at ``positions``), to the last rows of their sequences,
+        and return the queries' rotary parts ``q_rope [tokens, h_q, rope_dim]``,
+        rotated (None without any).  All of them, and ``q_out``, may be views with
+        strides; ``rows_out [tokens, rank + rope_dim]`` takes the rows too."""
+        if rope is not None and positions is None:
+            raise ValueError("rope needs positions")
+        if q_rope is None and q_out is not None:
+            raise ValueError("q_out needs q_rope")
+        if q_rope is not None and q_out is None:
+            q_out = self._empty((latent.shape[0], self.h_q, self.rope_dim), self.dtype, stream)
+        st = self._binding.latent_append(self._handle, latent, k_rope, q_rope, append_indptr,
+                                         positions, None if rope is None else rope.address, weight,
+                                         norm_eps, q_out, rows_out, stream)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_append_latent")
+        return q_out
+
+    def decode(self, q, sm_scale: float, out=None, lse=None, stream=None):
+        """Absorbed attention of one new token per sequence, ``q [B, h_q, rank +
+        rope_dim]``, over all its rows; returns ``out [B, h_q, rank]`` and the
+        base-2 ``lse [B, h_q]``."""
+        if out is None:
+            out = self._empty((self.batch_size, self.h_q, self.rank), self.dtype, stream)
+        if lse is None:
+            lse = self._empty((self.batch_size, self.h_q), torch.float32, stream)
+        st = self._binding.latent_decode(self._handle, q, sm_scale, out, lse, stream)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_decode_latent")
+        return out, lse
+
+    def tree_attn(self, q, q_indptr, mn_indptr, tree_order, sm_scale: float, out=None, lse=None,
+                  stream=None):
+        """Absorbed attention of draft trees' nodes, ``q [total_q, h_q, rank +
+        rope_dim]``, over their sequences' rows, of which the last are the trees'
+        (as ``tree_attn_paged``); returns ``out [total_q, h_q, rank]`` and ``lse``."""
+        if out is None:
+            out = self._empty((q.shape[0], self.h_q, self.rank), self.dtype, stream)
+        if lse is None:
+            lse = self._empty((q.shape[0], self.h_q), torch.float32, stream)
+        st = self._binding.latent_tree(self._handle, q, q_indptr, mn_indptr, tree_order, sm_scale,
+                                       out, lse, stream)
+        if st != TA_OK:
+            raise TreeAttnError(st, "tree_attn_latent")
+        return out, lse
+
+
+def make_expanded_dims(q: torch.Tensor, k: torch.Tensor, q_indptr: torch.Tensor) -> ExpandedDims:
+    return ExpandedDims(batch_size=q_indptr.numel() - 1, total_q=q.shape[0], total_kv=k.shape[0],
+                        heads=k.shape[1], head_dim=k.shape[2], rope_dim=q.shape[2] - k.shape[2],
+                        dtype=_dtype_code(q.dtype))
+
+
+def expanded_workspace_size(dims: ExpandedDims) -> int:
+    return int(lib().tree_attn_expanded_workspace_size(ctypes.byref(dims)))
+
+
+def _row_strides(name: str, t: torch.Tensor, dtype, shape):
+    """Token and head strides of a tensor whose rows are contiguous."""
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape} on a CUDA device, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # strides of dimensions of one say nothing
+    head = t.stride(1) if t.dim() == 3 and shape[1] > 1 else shape[-1]
+    return t.stride(0) if shape[0] > 1 else max(head, shape[-1]), head
+
+
+def tree_attn_expanded(q, q_indptr, k, k_rope, v, kv_indptr, out, lse, sm_scale: float,
+                       workspace: torch.Tensor, stream=None) -> None:
+    """Enqueue causal attention in the expanded form of latent attention: ``q
+    [total_q, heads, head_dim + rope_dim]`` (each sequence's last rows), ``k, v
+    [total_kv, heads, head_dim]``, the shared rotary key ``k_rope [total_kv,
+    rope_dim]``; all may be views with strides.  ``out [total_q, heads, head_dim]``
+    and the base-2 ``lse`` are written; ``workspace`` holds
+    ``expanded_workspace_size(dims)`` zero-filled bytes (``device_status``)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must have 3 dimensions")
+    (nq, h, dq), (nk, _, d) = q.shape, k.shape
+    dims = make_expanded_dims(q, k, q_indptr)
+    qt, qh = _row_strides("q", q, q.dtype, (nq, h, dq))
+    kt, kh = _row_strides("k", k, q.dtype, (nk, h, d))
+    vt, vh = _row_strides("v", v, q.dtype, (nk, h, d))
+    rt, _ = _row_strides("k_rope", k_rope, q.dtype, (nk, dq - d))
+    for name, t, dtype, shape in (("out", out, q.dtype, (nq, h, d)),
+                                  ("lse", lse, torch.float32, (nq, h)),
+                                  ("kv_indptr", kv_indptr, torch.int32, (dims.batch_size + 1,)),
+                                  ("q_indptr", q_indptr, torch.int32, (dims.batch_size + 1,))):
+        _check_dev(name, t, dtype)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    _check_dev("workspace", workspace)
+    for name, t in (("k", k), ("v", v), ("k_rope", k_rope), ("out", out), ("lse", lse),
+                    ("q_indptr", q_indptr), ("kv_indptr", kv_indptr), ("workspace", workspace)):
+        if t.get_device() != q.get_device():
+            raise ValueError(f"{name} must be on the device of q")
+    if q.get_device() != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, which is not the current device")
+    st = lib().tree_attn_expanded(_ptr(q), qt, qh, _ptr(q_indptr), _ptr(k), kt, kh, _ptr(k_rope), rt,
+                                  _ptr(v), vt, vh, _ptr(kv_indptr), _ptr(out), _ptr(lse),
+                                  float(sm_scale), ctypes.byref(dims), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    if st != TA_OK:
+        raise TreeAttnError(st, "tree_attn_expanded")

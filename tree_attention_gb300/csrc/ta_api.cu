@@ -895,6 +895,62 @@ ta::CacheWorkspace cache_layout(const ta_cache_dims* d, int nsm) {
 
 unsigned int* error_word(void* workspace) { return &static_cast<WsHeader*>(workspace)->error; }
 
+// tree_attn_compact_paged on pages of ``planes`` blocks of 16 rows.
+ta_status compact_pages(void* pages, const ta::PageTable& tab, const int32_t* mn_indptr,
+                        const int32_t* accept_indptr, const int32_t* accept_nodes,
+                        int32_t total_accept, int32_t* new_page_indptr, int32_t* new_page_values,
+                        int32_t* new_length_info, int32_t* freed_pages, int32_t* num_freed,
+                        int planes, int row_vecs, void* workspace, void* stream) {
+  if (total_accept < 0 || !mn_indptr || !accept_indptr || (total_accept > 0 && !accept_nodes))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (!new_page_indptr || !new_length_info || !num_freed) return TA_ERR_INVALID_ARGUMENT;
+  if (tab.nnz_pages > 0 && (!new_page_values || !freed_pages)) return TA_ERR_INVALID_ARGUMENT;
+  if (new_page_indptr == tab.page_indptr || new_length_info == tab.length_info ||
+      (tab.nnz_pages > 0 && (new_page_values == tab.page_values || freed_pages == tab.page_values ||
+                               freed_pages == new_page_values)))
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::CompactParams cp{};
+  cp.pages = static_cast<uint4*>(pages);
+  cp.tab = tab;
+  cp.mn_indptr = mn_indptr;
+  cp.accept_indptr = accept_indptr;
+  cp.accept_nodes = accept_nodes;
+  cp.new_indptr = new_page_indptr;
+  cp.new_values = new_page_values;
+  cp.new_length = new_length_info;
+  cp.freed = freed_pages;
+  cp.num_freed = num_freed;
+  cp.error = error_word(workspace);
+  cp.total_accept = total_accept;
+  cp.planes = planes;
+  cp.row_vecs = row_vecs;
+  return cuda_status(ta::launch_compact(cp, static_cast<cudaStream_t>(stream)));
+}
+
+// tree_attn_copy_pages on pages of ``page_vecs`` 16-byte vectors; marks_at(SMs): the
+// marks' place in the workspace.
+template <typename F>
+ta_status copy_whole_pages(void* pages, const int32_t* src_pages, const int32_t* dst_pages,
+                           int32_t n, int32_t num_pages, int page_vecs, void* workspace,
+                           F marks_at, void* stream) {
+  if (n < 0) return TA_ERR_INVALID_ARGUMENT;
+  if (n == 0) return TA_OK;
+  if (!src_pages || !dst_pages) return TA_ERR_INVALID_ARGUMENT;
+  const int nsm = sm_count();
+  if (nsm <= 0) return cuda_failure();
+  ta::CopyParams cp{};
+  cp.pages = static_cast<uint4*>(pages);
+  cp.src = src_pages;
+  cp.dst = dst_pages;
+  cp.error = error_word(workspace);
+  cp.n = n;
+  cp.num_pages = num_pages;
+  cp.page_vecs = page_vecs;
+  cp.page_lines = (page_vecs + 255) / 256;
+  cp.marks = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(workspace) + marks_at(nsm));
+  return cuda_status(ta::launch_copy_pages(cp, nsm, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -1046,30 +1102,10 @@ ta_status tree_attn_compact_paged(void* pages, const int32_t* page_indptr,
   if (s != TA_OK) return s;
   s = check_table(dims, page_indptr, page_values, length_info);
   if (s != TA_OK) return s;
-  if (total_accept < 0 || !mn_indptr || !accept_indptr || (total_accept > 0 && !accept_nodes))
-    return TA_ERR_INVALID_ARGUMENT;
-  if (!new_page_indptr || !new_length_info || !num_freed) return TA_ERR_INVALID_ARGUMENT;
-  if (dims->nnz_pages > 0 && (!new_page_values || !freed_pages)) return TA_ERR_INVALID_ARGUMENT;
-  if (new_page_indptr == page_indptr || new_length_info == length_info ||
-      (dims->nnz_pages > 0 && (new_page_values == page_values || freed_pages == page_values ||
-                               freed_pages == new_page_values)))
-    return TA_ERR_INVALID_ARGUMENT;
-  ta::CompactParams cp{};
-  cp.pages = static_cast<uint4*>(pages);
-  cp.tab = page_table(dims, page_indptr, page_values, length_info);
-  cp.mn_indptr = mn_indptr;
-  cp.accept_indptr = accept_indptr;
-  cp.accept_nodes = accept_nodes;
-  cp.new_indptr = new_page_indptr;
-  cp.new_values = new_page_values;
-  cp.new_length = new_length_info;
-  cp.freed = freed_pages;
-  cp.num_freed = num_freed;
-  cp.error = error_word(workspace);
-  cp.total_accept = total_accept;
-  cp.h_kv = dims->h_kv;
-  cp.row_vecs = dims->head_dim / 8;
-  return cuda_status(ta::launch_compact(cp, static_cast<cudaStream_t>(stream)));
+  return compact_pages(pages, page_table(dims, page_indptr, page_values, length_info), mn_indptr,
+                       accept_indptr, accept_nodes, total_accept, new_page_indptr, new_page_values,
+                       new_length_info, freed_pages, num_freed, 2 * dims->h_kv, dims->head_dim / 8,
+                       workspace, stream);
 }
 
 ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int32_t* dst_pages,
@@ -1077,22 +1113,304 @@ ta_status tree_attn_copy_pages(void* pages, const int32_t* src_pages, const int3
                                size_t workspace_bytes, void* stream) {
   const ta_status s = check_cache(dims, pages, workspace, workspace_bytes);
   if (s != TA_OK) return s;
-  if (n < 0) return TA_ERR_INVALID_ARGUMENT;
-  if (n == 0) return TA_OK;
-  if (!src_pages || !dst_pages) return TA_ERR_INVALID_ARGUMENT;
+  return copy_whole_pages(
+      pages, src_pages, dst_pages, n, dims->num_pages, 4 * dims->h_kv * dims->head_dim, workspace,
+      [&](int nsm) { return cache_layout(dims, nsm).off_marks; }, stream);
+}
+
+}  // extern "C"
+
+
+// ---------------------------------------------------------------------------
+// latent attention
+// ---------------------------------------------------------------------------
+namespace {
+
+bool latent_dims_valid(const ta_latent_dims* d) {
+  if (!d) return false;
+  if (d->batch_size < 1 || d->h_q < 1 || d->rank < 1 || d->rope_dim < 1) return false;
+  if (d->dtype != TA_FP16 && d->dtype != TA_BF16) return false;
+  if (d->num_pages < 1 || d->nnz_pages < 0) return false;
+  return (int64_t)d->nnz_pages * ta::kPageSize <= INT32_MAX;
+}
+
+bool rope_dim_supported(int32_t n) { return n >= 16 && n <= 64 && n % 16 == 0; }
+
+ta_status latent_dims_supported(const ta_latent_dims* d) {
+  if (d->rank != 256 && d->rank != 512) return TA_ERR_UNSUPPORTED;
+  if (!rope_dim_supported(d->rope_dim)) return TA_ERR_UNSUPPORTED;
+  if (d->h_q > ta::kMaxGroup || d->batch_size > ta::kMaxCacheBatch) return TA_ERR_UNSUPPORTED;
+  return TA_OK;
+}
+
+ta_status check_latent(const ta_latent_dims* dims, const void* pages, const void* workspace,
+                       size_t workspace_bytes) {
+  if (!latent_dims_valid(dims)) return TA_ERR_INVALID_ARGUMENT;
+  const ta_status sup = latent_dims_supported(dims);
+  if (sup != TA_OK) return sup;
+  if (!pages || !workspace) return TA_ERR_INVALID_ARGUMENT;
+  if (!aligned(pages, 16) || !aligned(workspace, 256)) return TA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < tree_attn_latent_workspace_size(dims)) return TA_ERR_INVALID_ARGUMENT;
+  return TA_OK;
+}
+
+ta_status check_table(const ta_latent_dims* dims, const int32_t* page_indptr,
+                      const int32_t* page_values, const int32_t* length_info) {
+  if (!page_indptr || !length_info) return TA_ERR_INVALID_ARGUMENT;
+  if (dims->nnz_pages > 0 && !page_values) return TA_ERR_INVALID_ARGUMENT;
+  return TA_OK;
+}
+
+ta::PageTable page_table(const ta_latent_dims* d, const int32_t* page_indptr,
+                         const int32_t* page_values, const int32_t* length_info) {
+  return ta::PageTable{page_indptr, page_values, length_info, d->batch_size, d->nnz_pages,
+                       d->num_pages};
+}
+
+// Attention over a latent cache; q_indptr null: one token per sequence.
+ta_status latent_attention(const void* q, const int32_t* q_indptr, int32_t total_q,
+                           const void* pages, const int32_t* page_indptr,
+                           const int32_t* page_values, const int32_t* length_info,
+                           const int32_t* mn_indptr, const int32_t* tree_order,
+                           int32_t total_tree, void* out, float* lse, float sm_scale,
+                           const ta_latent_dims* dims, void* workspace, void* stream) {
+  ta::LatentParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.pages = static_cast<const uint16_t*>(pages);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.tab = page_table(dims, page_indptr, page_values, length_info);
+  p.q_indptr = q_indptr;
+  p.mn_indptr = mn_indptr;
+  p.tree_order = tree_order;
+  p.total_q = total_q;
+  p.total_tree = total_tree;
+  p.error = error_word(workspace);
+  p.h = dims->h_q;
+  p.rank = dims->rank;
+  p.rope_dim = dims->rope_dim;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_failure();
-  ta::CopyParams cp{};
-  cp.pages = static_cast<uint4*>(pages);
-  cp.src = src_pages;
-  cp.dst = dst_pages;
-  cp.error = error_word(workspace);
-  cp.n = n;
-  cp.num_pages = dims->num_pages;
-  cp.page_lines = dims->h_kv * dims->head_dim / 64;   // 2 planes x 16 slots x 2 bytes
-  cp.marks = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(workspace) +
-                                             cache_layout(dims, nsm).off_marks);
-  return cuda_status(ta::launch_copy_pages(cp, nsm, static_cast<cudaStream_t>(stream)));
+  return cuda_status(ta::launch_latent(p, dims->dtype == TA_BF16, nsm,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tree_attn_latent_workspace_size(const ta_latent_dims* dims) {
+  if (!latent_dims_valid(dims) || latent_dims_supported(dims) != TA_OK) return 0;
+  return ta::latent_workspace(dims->num_pages, std::max(1, sm_count())).total;
+}
+
+ta_status tree_attn_append_latent(const void* latent, int64_t latent_stride, const void* k_rope,
+                                  int64_t k_rope_stride, const void* q_rope,
+                                  int64_t q_token_stride, int64_t q_head_stride,
+                                  int32_t total_new, const int32_t* append_indptr,
+                                  const int32_t* positions, const void* weight, float norm_eps,
+                                  const ta_rope* rope, void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  void* q_out, int64_t q_out_token_stride,
+                                  int64_t q_out_head_stride, void* rows_out,
+                                  const ta_latent_dims* dims, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  ta_status s = check_latent(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  if (total_new < 0) return TA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(norm_eps) || norm_eps < 0.f) return TA_ERR_INVALID_ARGUMENT;
+  if (rope && ((rope->layout != TA_ROPE_HALF && rope->layout != TA_ROPE_INTERLEAVED) ||
+               rope->rotary_dim != dims->rope_dim))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (total_new == 0) return TA_OK;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (!latent || !k_rope || !append_indptr || (rope && !positions) || !q_rope != !q_out)
+    return TA_ERR_INVALID_ARGUMENT;
+  if (!aligned(latent, 16) || !aligned(k_rope, 16) || !aligned(q_rope, 16) || !aligned(q_out, 16) ||
+      !aligned(rows_out, 16) || !aligned(weight, 16))
+    return TA_ERR_INVALID_ARGUMENT;
+  const int64_t rd = dims->rope_dim, h = dims->h_q;
+  if (latent_stride % 8 || k_rope_stride % 8 || latent_stride < dims->rank || k_rope_stride < rd)
+    return TA_ERR_INVALID_ARGUMENT;
+  // rows of rope_dim elements that do not overlap, token by token or head by head
+  auto apart = [&](int64_t token, int64_t head) {
+    if (token % 8 || head % 8 || token < rd || head < rd) return false;
+    return token >= (h - 1) * head + rd || head >= (total_new - 1) * token + rd;
+  };
+  if (q_rope && (!apart(q_token_stride, q_head_stride) ||
+                 !apart(q_out_token_stride, q_out_head_stride)))
+    return TA_ERR_INVALID_ARGUMENT;
+  if (q_rope && q_rope == q_out &&
+      (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::LatentAppendParams ap{};
+  ap.latent = static_cast<const uint16_t*>(latent);
+  ap.k_rope = static_cast<const uint16_t*>(k_rope);
+  ap.q_rope = static_cast<const uint16_t*>(q_rope);
+  ap.latent_stride = latent_stride;
+  ap.k_rope_stride = k_rope_stride;
+  ap.q_token_stride = q_token_stride;
+  ap.q_head_stride = q_head_stride;
+  ap.append_indptr = append_indptr;
+  ap.positions = positions;
+  ap.weight = static_cast<const uint16_t*>(weight);
+  ap.pages = static_cast<uint16_t*>(pages);
+  ap.q_out = static_cast<uint16_t*>(q_out);
+  ap.qo_token_stride = q_out_token_stride;
+  ap.qo_head_stride = q_out_head_stride;
+  ap.rows_out = static_cast<uint16_t*>(rows_out);
+  ap.tab = page_table(dims, page_indptr, page_values, length_info);
+  ap.error = error_word(workspace);
+  ap.total_new = total_new;
+  ap.h = dims->h_q;
+  ap.rank = dims->rank;
+  ap.rope_dim = dims->rope_dim;
+  ap.eps = norm_eps;
+  if (rope) {
+    ap.rope_layout = rope->layout;
+    ap.magnitude = rope->magnitude;
+    std::memcpy(ap.turns, rope->turns, sizeof(ap.turns));
+  }
+  return cuda_status(ta::launch_latent_append(ap, dims->dtype == TA_BF16,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+ta_status tree_attn_decode_latent(const void* q, const void* pages, const int32_t* page_indptr,
+                                  const int32_t* page_values, const int32_t* length_info,
+                                  void* out, float* lse, float sm_scale,
+                                  const ta_latent_dims* dims, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  ta_status s = check_latent(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !std::isfinite(sm_scale))
+    return TA_ERR_INVALID_ARGUMENT;
+  return latent_attention(q, nullptr, dims->batch_size, pages, page_indptr, page_values,
+                          length_info, nullptr, nullptr, 0, out, lse, sm_scale, dims, workspace,
+                          stream);
+}
+
+ta_status tree_attn_latent(const void* q, const int32_t* q_indptr, int32_t total_q,
+                           const void* pages, const int32_t* page_indptr,
+                           const int32_t* page_values, const int32_t* length_info,
+                           const int32_t* mn_indptr, const int32_t* tree_order,
+                           int32_t total_tree, void* out, float* lse, float sm_scale,
+                           const ta_latent_dims* dims, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  ta_status s = check_latent(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  if (total_q < 0 || total_tree < 0 || !q_indptr || !mn_indptr || !std::isfinite(sm_scale))
+    return TA_ERR_INVALID_ARGUMENT;
+  if ((int64_t)total_q * dims->h_q > INT32_MAX) return TA_ERR_UNSUPPORTED;
+  if (total_q == 0) return TA_OK;
+  if (!q || !out || !lse || !tree_order || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(tree_order, 8))
+    return TA_ERR_INVALID_ARGUMENT;
+  return latent_attention(q, q_indptr, total_q, pages, page_indptr, page_values, length_info,
+                          mn_indptr, tree_order, total_tree, out, lse, sm_scale, dims, workspace,
+                          stream);
+}
+
+ta_status tree_attn_compact_latent(void* pages, const int32_t* page_indptr,
+                                   const int32_t* page_values, const int32_t* length_info,
+                                   const int32_t* mn_indptr, const int32_t* accept_indptr,
+                                   const int32_t* accept_nodes, int32_t total_accept,
+                                   int32_t* new_page_indptr, int32_t* new_page_values,
+                                   int32_t* new_length_info, int32_t* freed_pages,
+                                   int32_t* num_freed, const ta_latent_dims* dims,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  ta_status s = check_latent(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  s = check_table(dims, page_indptr, page_values, length_info);
+  if (s != TA_OK) return s;
+  return compact_pages(pages, page_table(dims, page_indptr, page_values, length_info), mn_indptr,
+                       accept_indptr, accept_nodes, total_accept, new_page_indptr, new_page_values,
+                       new_length_info, freed_pages, num_freed, 1,
+                       (dims->rank + dims->rope_dim) / 8, workspace, stream);
+}
+
+ta_status tree_attn_copy_pages_latent(void* pages, const int32_t* src_pages,
+                                      const int32_t* dst_pages, int32_t n,
+                                      const ta_latent_dims* dims, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  const ta_status s = check_latent(dims, pages, workspace, workspace_bytes);
+  if (s != TA_OK) return s;
+  return copy_whole_pages(
+      pages, src_pages, dst_pages, n, dims->num_pages, 2 * (dims->rank + dims->rope_dim), workspace,
+      [&](int nsm) { return ta::latent_workspace(dims->num_pages, nsm).off_marks; }, stream);
+}
+
+size_t tree_attn_expanded_workspace_size(const ta_expanded_dims* d) {
+  if (!d || d->batch_size < 1 || d->total_q < 0 || d->total_kv < 0 || d->heads < 1) return 0;
+  if (d->dtype != TA_FP16 && d->dtype != TA_BF16) return 0;
+  if (d->head_dim != 64 && d->head_dim != 128) return 0;
+  if (!rope_dim_supported(d->rope_dim) || d->heads > 1024) return 0;
+  return d->batch_size <= ta::kMaxCacheBatch ? 256 : 0;
+}
+
+ta_status tree_attn_expanded(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const int32_t* q_indptr, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                             const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                             const int32_t* kv_indptr, void* out, float* lse, float sm_scale,
+                             const ta_expanded_dims* dims, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!dims || dims->batch_size < 1 || dims->total_q < 0 || dims->total_kv < 0 ||
+      dims->heads < 1 || dims->head_dim < 1 || dims->rope_dim < 1 ||
+      (dims->dtype != TA_FP16 && dims->dtype != TA_BF16))
+    return TA_ERR_INVALID_ARGUMENT;
+  const size_t need = tree_attn_expanded_workspace_size(dims);
+  if (need == 0) return TA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !q_indptr ||
+      !kv_indptr || !std::isfinite(sm_scale))
+    return TA_ERR_INVALID_ARGUMENT;
+  if ((int64_t)dims->total_q * dims->heads > INT32_MAX) return TA_ERR_UNSUPPORTED;
+  if (dims->total_q == 0) return TA_OK;
+  if (dims->total_kv == 0) return TA_ERR_INVALID_ARGUMENT;   // qo <= kv
+  if (!q || !k || !k_rope || !v || !out || !lse) return TA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) || !aligned(v, 16) ||
+      !aligned(out, 16))
+    return TA_ERR_INVALID_ARGUMENT;
+  const int64_t dk = dims->head_dim, dq = dk + dims->rope_dim;
+  auto good = [](int64_t stride, int64_t row) {
+    return stride % 8 == 0 && stride >= row && stride < (int64_t)1 << 36;
+  };
+  if (!good(q_token_stride, dq) || !good(q_head_stride, dq) || !good(k_token_stride, dk) ||
+      !good(k_head_stride, dk) || !good(k_rope_stride, dims->rope_dim) ||
+      !good(v_token_stride, dk) || !good(v_head_stride, dk))
+    return TA_ERR_INVALID_ARGUMENT;
+  ta::ExpandedParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.k_rope = static_cast<const uint16_t*>(k_rope);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_ts = q_token_stride;
+  p.q_hs = q_head_stride;
+  p.k_ts = k_token_stride;
+  p.k_hs = k_head_stride;
+  p.kr_ts = k_rope_stride;
+  p.v_ts = v_token_stride;
+  p.v_hs = v_head_stride;
+  p.q_indptr = q_indptr;
+  p.kv_indptr = kv_indptr;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.error = error_word(workspace);
+  p.batch = dims->batch_size;
+  p.total_q = dims->total_q;
+  p.total_kv = dims->total_kv;
+  p.h = dims->heads;
+  p.rope_dim = dims->rope_dim;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  const int nsm = sm_count();
+  if (nsm <= 0) return cuda_failure();
+  return cuda_status(ta::launch_expanded(p, dims->head_dim, dims->dtype == TA_BF16, nsm,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

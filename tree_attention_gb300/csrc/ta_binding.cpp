@@ -1,4 +1,4 @@
-// ta_binding.cpp -- the calls of PagedCache as a Python extension module
+// ta_binding.cpp -- the calls of PagedCache and LatentCache as a Python extension module
 // (_binding.so): it checks tensor arguments and passes their addresses to the C
 // entry points of include/tree_attn.h, nothing else.
 //
@@ -26,9 +26,8 @@
 
 namespace {
 
-// What every call on one PagedCache passes; the Python object keeps the tensors.
-struct Handle {
-  ta_cache_dims dims;
+// What every call on one cache passes; the Python object keeps the tensors.
+struct Base {
   void* pages;
   const int32_t *indptr, *values, *length;
   void* workspace;
@@ -39,11 +38,21 @@ struct Handle {
   mutable std::vector<cudaStream_t> streams;   // that the allocator knows they are used on
 };
 
-const char* const kCapsule = "tree_attention_gb300.cache";
+struct Handle : Base {                         // a PagedCache
+  using Dims = ta_cache_dims;
+  static constexpr const char* kCapsule = "tree_attention_gb300.cache";
+  Dims dims;
+};
+
+struct Latent : Base {                         // a LatentCache
+  using Dims = ta_latent_dims;
+  static constexpr const char* kCapsule = "tree_attention_gb300.latent_cache";
+  Dims dims;
+};
 
 // The tensor argument ``o``; throws unless it has this type and shape and is on
 // the handle's device.
-const at::Tensor& tensor(const Handle& h, const char* name, PyObject* o, at::ScalarType type,
+const at::Tensor& tensor(const Base& h, const char* name, PyObject* o, at::ScalarType type,
                          std::initializer_list<int64_t> shape) {
   if (!THPVariable_Check(o)) throw std::invalid_argument(std::string(name) + " must be a tensor");
   const at::Tensor& t = THPVariable_Unpack(o);
@@ -59,14 +68,14 @@ const at::Tensor& tensor(const Handle& h, const char* name, PyObject* o, at::Sca
 
 // Address of a contiguous tensor argument.
 template <typename T = void>
-T* address(const Handle& h, const char* name, PyObject* o, at::ScalarType type,
+T* address(const Base& h, const char* name, PyObject* o, at::ScalarType type,
            std::initializer_list<int64_t> shape) {
   const at::Tensor& t = tensor(h, name, o, type, shape);
   if (!t.is_contiguous()) throw std::invalid_argument(std::string(name) + " must be contiguous");
   return static_cast<T*>(t.data_ptr());
 }
 
-int32_t* ints(const Handle& h, const char* name, PyObject* o, int64_t n) {
+int32_t* ints(const Base& h, const char* name, PyObject* o, int64_t n) {
   return address<int32_t>(h, name, o, at::kInt, {n});
 }
 
@@ -98,7 +107,7 @@ struct PythonError {};   // a Python exception is set
 // is gone, before the work on ``stream`` is done: it may have had the last
 // reference.  Not on streams that torch did not make (their id is their
 // address): they may be destroyed before the memory is freed.
-void hold_on(const Handle& h, c10::cuda::CUDAStream stream) {
+void hold_on(const Base& h, c10::cuda::CUDAStream stream) {
   cudaStream_t s = stream.stream();
   if (stream.id() != 0 && stream.id() == reinterpret_cast<int64_t>(s)) return;
   if (std::find(h.streams.begin(), h.streams.end(), s) != h.streams.end()) return;
@@ -108,7 +117,7 @@ void hold_on(const Handle& h, c10::cuda::CUDAStream stream) {
 }
 
 // The stream of a call: torch's current one, a stream object, or an address.
-void* stream_of(const Handle& h, PyObject* o) {
+void* stream_of(const Base& h, PyObject* o) {
   if (c10::cuda::current_device() != h.device) {
     std::ostringstream s;
     s << "the cache is on cuda:" << h.device << ", which is not the current device";
@@ -144,11 +153,13 @@ float number(PyObject* o) {
   return static_cast<float>(x);
 }
 
-const Handle& handle(PyObject* o) {
-  void* p = PyCapsule_GetPointer(o, kCapsule);
+template <typename H>
+const H& handle_of(PyObject* o) {
+  void* p = PyCapsule_GetPointer(o, H::kCapsule);
   if (!p) throw PythonError();
-  return *static_cast<Handle*>(p);
+  return *static_cast<H*>(p);
 }
+const Handle& handle(PyObject* o) { return handle_of<Handle>(o); }
 
 // Runs ``body`` on ``n`` arguments, of which there must be ``want``; it returns a
 // Python object, and its exceptions become Python's.
@@ -174,7 +185,9 @@ PyObject* call(Py_ssize_t n, Py_ssize_t want, F body) {
 
 bool given(PyObject* o) { return o != Py_None; }
 
-// handle(dims address, pages, page_indptr, page_values, length_info, workspace)
+// handle(dims address, pages, page_indptr, page_values, length_info, workspace),
+// latent_handle(the same)
+template <typename H>
 PyObject* make_handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
     const void* dims = PyLong_AsVoidPtr(a[0]);
@@ -186,12 +199,13 @@ PyObject* make_handle(PyObject*, PyObject* const* a, Py_ssize_t n) {
       t.push_back(THPVariable_Unpack(a[i]));
     }
     auto ints = [&](int i) { return static_cast<int32_t*>(t[i].data_ptr()); };
-    std::unique_ptr<Handle> h(new Handle{
-        *static_cast<const ta_cache_dims*>(dims), t[0].data_ptr(), ints(1), ints(2), ints(3),
-        t[4].data_ptr(), static_cast<size_t>(t[4].nbytes()), static_cast<int>(t[0].get_device()),
-        t[0].scalar_type(), t, {}});
-    PyObject* c = PyCapsule_New(h.get(), kCapsule, [](PyObject* o) {
-      delete static_cast<Handle*>(PyCapsule_GetPointer(o, kCapsule));
+    std::unique_ptr<H> h(new H{
+        {t[0].data_ptr(), ints(1), ints(2), ints(3), t[4].data_ptr(),
+         static_cast<size_t>(t[4].nbytes()), static_cast<int>(t[0].get_device()),
+         t[0].scalar_type(), t, {}},
+        *static_cast<const typename H::Dims*>(dims)});
+    PyObject* c = PyCapsule_New(h.get(), H::kCapsule, [](PyObject* o) {
+      delete static_cast<H*>(PyCapsule_GetPointer(o, H::kCapsule));
     });
     if (c) h.release();
     return c;
@@ -239,9 +253,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // compact(handle, mn_indptr, accept_indptr, accept_nodes, new_page_indptr,
 //         new_page_values, new_length_info, freed_pages, num_freed, stream)
+template <typename H, auto F>
 PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 10, [&] {
-    const Handle& h = handle(a[0]);
+    const H& h = handle_of<H>(a[0]);
     const int64_t b = h.dims.batch_size, nnz = h.dims.nnz_pages;
     const int64_t accepted = length("accept_nodes", a[3], 1);
     if (accepted > INT32_MAX) throw std::invalid_argument("too many accepted nodes");
@@ -253,22 +268,105 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* lengths = ints(h, "new_length_info", a[6], b);
     int32_t* freed = ints(h, "freed_pages", a[7], nnz);
     int32_t* num_freed = ints(h, "num_freed", a[8], 1);
-    return (long)tree_attn_compact_paged(h.pages, h.indptr, h.values, h.length, mn, accept, nodes,
-                                         (int32_t)accepted, indptr, values, lengths, freed, num_freed,
-                                         &h.dims, h.workspace, h.workspace_bytes, stream_of(h, a[9]));
+    return (long)F(h.pages, h.indptr, h.values, h.length, mn, accept, nodes, (int32_t)accepted, indptr,
+                   values, lengths, freed, num_freed, &h.dims, h.workspace, h.workspace_bytes,
+                   stream_of(h, a[9]));
   });
 }
 
 // copy_pages(handle, src_pages, dst_pages, stream)
+template <typename H, auto F>
 PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 4, [&] {
-    const Handle& h = handle(a[0]);
+    const H& h = handle_of<H>(a[0]);
     const int64_t pairs = length("src_pages", a[1], 1);
     if (pairs > INT32_MAX) throw std::invalid_argument("too many pages");
     const int32_t* src = ints(h, "src_pages", a[1], pairs);
     const int32_t* dst = ints(h, "dst_pages", a[2], pairs);
-    return (long)tree_attn_copy_pages(h.pages, src, dst, (int32_t)pairs, &h.dims, h.workspace,
-                                      h.workspace_bytes, stream_of(h, a[3]));
+    return (long)F(h.pages, src, dst, (int32_t)pairs, &h.dims, h.workspace, h.workspace_bytes,
+                   stream_of(h, a[3]));
+  });
+}
+
+// A [tokens, width] argument whose rows may be apart.
+const void* token_rows(const Base& h, const char* name, PyObject* o, int64_t n, int64_t width,
+                       int64_t* stride) {
+  const at::Tensor& t = tensor(h, name, o, h.dtype, {n, width});
+  if (t.stride(1) != 1)
+    throw std::invalid_argument(std::string("the elements of one token must be contiguous in ") + name);
+  *stride = n > 1 ? t.stride(0) : width;
+  return t.data_ptr();
+}
+
+// A [tokens, heads, width] argument whose tokens and heads may be apart.
+void* head_rows(const Base& h, const char* name, PyObject* o, int64_t n, int64_t heads, int64_t width,
+                int64_t* token, int64_t* head) {
+  const at::Tensor& t = tensor(h, name, o, h.dtype, {n, heads, width});
+  if (t.stride(2) != 1)
+    throw std::invalid_argument(std::string("the elements of one head must be contiguous in ") + name);
+  *head = heads > 1 ? t.stride(1) : width;
+  *token = n > 1 ? t.stride(0) : (heads - 1) * *head + width;
+  return t.data_ptr();
+}
+
+// latent_append(handle, latent, k_rope, q_rope, append_indptr, positions, rope
+//               address, weight, norm_eps, q_out, rows_out, stream)
+PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 12, [&] {
+    const Latent& h = handle_of<Latent>(a[0]);
+    const int64_t tokens = length("latent", a[1], 2), heads = h.dims.h_q, rd = h.dims.rope_dim;
+    const int64_t width = h.dims.rank + rd;
+    int64_t ls, ks, qt = 0, qh = 0, ot = 0, oh = 0;
+    const void* latent = token_rows(h, "latent", a[1], tokens, h.dims.rank, &ls);
+    const void* k = token_rows(h, "k_rope", a[2], tokens, rd, &ks);
+    if (tokens > INT32_MAX) throw std::invalid_argument("too many tokens");
+    const void* q = given(a[3]) ? head_rows(h, "q_rope", a[3], tokens, heads, rd, &qt, &qh) : nullptr;
+    const int32_t* indptr = ints(h, "append_indptr", a[4], h.dims.batch_size + 1);
+    const int32_t* positions = given(a[5]) ? ints(h, "positions", a[5], tokens) : nullptr;
+    const ta_rope* rope = given(a[6]) ? static_cast<const ta_rope*>(PyLong_AsVoidPtr(a[6])) : nullptr;
+    if (PyErr_Occurred()) throw PythonError();
+    const void* w = given(a[7]) ? address(h, "weight", a[7], h.dtype, {h.dims.rank}) : nullptr;
+    const float eps = number(a[8]);
+    void* q_out = given(a[9]) ? head_rows(h, "q_out", a[9], tokens, heads, rd, &ot, &oh) : nullptr;
+    void* rows_out = given(a[10]) ? address(h, "rows_out", a[10], h.dtype, {tokens, width}) : nullptr;
+    return (long)tree_attn_append_latent(latent, ls, k, ks, q, qt, qh, (int32_t)tokens, indptr,
+                                         positions, w, eps, rope, h.pages, h.indptr, h.values,
+                                         h.length, q_out, ot, oh, rows_out, &h.dims, h.workspace,
+                                         h.workspace_bytes, stream_of(h, a[11]));
+  });
+}
+
+// latent_decode(handle, q, sm_scale, out, lse, stream)
+PyObject* latent_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 6, [&] {
+    const Latent& h = handle_of<Latent>(a[0]);
+    const int64_t b = h.dims.batch_size, hq = h.dims.h_q, rank = h.dims.rank;
+    const void* q = address(h, "q", a[1], h.dtype, {b, hq, rank + h.dims.rope_dim});
+    const float sm_scale = number(a[2]);
+    void* out = address(h, "out", a[3], h.dtype, {b, hq, rank});
+    float* lse = address<float>(h, "lse", a[4], at::kFloat, {b, hq});
+    return (long)tree_attn_decode_latent(q, h.pages, h.indptr, h.values, h.length, out, lse, sm_scale,
+                                         &h.dims, h.workspace, h.workspace_bytes, stream_of(h, a[5]));
+  });
+}
+
+// latent_tree(handle, q, q_indptr, mn_indptr, tree_order, sm_scale, out, lse, stream)
+PyObject* latent_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 9, [&] {
+    const Latent& h = handle_of<Latent>(a[0]);
+    const int64_t rows = length("q", a[1], 3), nodes = length("tree_order", a[4], 2);
+    const int64_t b = h.dims.batch_size, hq = h.dims.h_q, rank = h.dims.rank;
+    if (rows > INT32_MAX || nodes > INT32_MAX) throw std::invalid_argument("too many rows");
+    const void* q = address(h, "q", a[1], h.dtype, {rows, hq, rank + h.dims.rope_dim});
+    const int32_t* q_indptr = ints(h, "q_indptr", a[2], b + 1);
+    const int32_t* mn = ints(h, "mn_indptr", a[3], b + 1);
+    const int32_t* order = address<int32_t>(h, "tree_order", a[4], at::kInt, {nodes, 2});
+    const float sm_scale = number(a[5]);
+    void* out = address(h, "out", a[6], h.dtype, {rows, hq, rank});
+    float* lse = address<float>(h, "lse", a[7], at::kFloat, {rows, hq});
+    return (long)tree_attn_latent(q, q_indptr, (int32_t)rows, h.pages, h.indptr, h.values, h.length, mn,
+                                  order, (int32_t)nodes, out, lse, sm_scale, &h.dims, h.workspace,
+                                  h.workspace_bytes, stream_of(h, a[8]));
   });
 }
 
@@ -292,10 +390,20 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<make_handle>("handle"), method<append>("append"),
-                           method<decode>("decode"),      method<compact>("compact"),
-                           method<copy_pages>("copy_pages"), method<zero_now>("zero_now"),
-                           {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {
+    method<make_handle<Handle>>("handle"),
+    method<append>("append"),
+    method<decode>("decode"),
+    method<compact<Handle, tree_attn_compact_paged>>("compact"),
+    method<copy_pages<Handle, tree_attn_copy_pages>>("copy_pages"),
+    method<make_handle<Latent>>("latent_handle"),
+    method<latent_append>("latent_append"),
+    method<latent_decode>("latent_decode"),
+    method<latent_tree>("latent_tree"),
+    method<compact<Latent, tree_attn_compact_latent>>("latent_compact"),
+    method<copy_pages<Latent, tree_attn_copy_pages_latent>>("latent_copy_pages"),
+    method<zero_now>("zero_now"),
+    {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -398,13 +398,13 @@ __global__ void __launch_bounds__(kCompactThreads, 4) compact_kernel(const Compa
 
   // the moves: every node checked before the first row moves
   const int64_t head_vecs = (int64_t)kPageSize * p.row_vecs;   // one head's plane of a page
-  const int cols = 2 * p.h_kv * p.row_vecs;
+  const int cols = p.planes * p.row_vecs;
   const int col = blockIdx.y * kCompactThreads + tid;
   const int64_t col_off = (int64_t)(col / p.row_vecs) * head_vecs + col % p.row_vecs;
   auto row_offset = [&](int row) -> long long {
     const int page = tb.page_values[me.p0 + row / kPageSize];
     if (page < 0 || page >= tb.num_pages) return -1;
-    return (long long)page * 2 * p.h_kv * head_vecs + (long long)(row % kPageSize) * p.row_vecs;
+    return (long long)page * p.planes * head_vecs + (long long)(row % kPageSize) * p.row_vecs;
   };
   auto stage = [&](int j) {      // move j into slot tid; whether it is valid
     if (node <= prev || node >= tree) return false;
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kCopyThreads) mark_pages_kernel(const CopyPara
 // Measured, marked / not, us: 300 pages of 64 KB 9.0 / 7.3, 1,000 26.1 / 24.3,
 // 4,096 84.9 / 94.0 (6.3 TB/s; a contiguous copy of as much takes torch 86),
 // 16,000 310 / 381; of 8 KB, 1,500 pages 8.1 / 6.5, 16,000 45.5 / 88.
-template <bool MARKED>
+// RAGGED: pages that are not whole lines (a latent cache's), whose last line is short.
+template <bool MARKED, bool RAGGED>
 __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyParams p) {
   __shared__ uint4 s_ring[kCopyDepth][kCopyThreads];
   __shared__ unsigned int s_filter[kCopyFilter / 32];
@@ -552,7 +553,8 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
   const int64_t hi = lo + per + (blockIdx.x < extra);
   if (lo >= hi) return;
   const int64_t first = lo / p.page_lines, last = (hi - 1) / p.page_lines;
-  const int64_t page_vecs = (int64_t)p.page_lines * kCopyThreads;
+  const int64_t page_vecs = RAGGED ? p.page_vecs : (int64_t)p.page_lines * kCopyThreads;
+  auto in_page = [&](int line) { return !RAGGED || line * kCopyThreads + tid < p.page_vecs; };
   for (int64_t base = first; base <= last; base += kCopyPairs) {
     const int m = (int)min((int64_t)kCopyPairs, last - base + 1);
     __syncthreads();
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
     CopyAt get{line0 / p.page_lines, line0 % p.page_lines}, put = get;
     auto fetch = [&](int l) {
       if (l < lines) {
-        if (!s_skip[get.k]) {
+        if (!s_skip[get.k] && in_page(get.line)) {
           const uint4* from = p.pages + s_src[get.k] * page_vecs + get.line * kCopyThreads + tid;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            smem_u32(&s_ring[l % kCopyDepth][tid])),
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(kCopyThreads, 5) copy_pages_kernel(const CopyP
     __syncthreads();
     for (int l = 0; l < lines; ++l) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kCopyDepth - 1) : "memory");
-      if (!s_skip[put.k])
+      if (!s_skip[put.k] && in_page(put.line))
         __stcs(p.pages + s_dst[put.k] * page_vecs + put.line * kCopyThreads + tid,
                s_ring[l % kCopyDepth][tid]);
       put.next(p.page_lines);
@@ -646,19 +648,21 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, bool bf16, int gr
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  const int cols = 2 * p.h_kv * p.row_vecs;
+  const int cols = p.planes * p.row_vecs;
   const dim3 g(p.tab.batch, (cols + kCompactThreads - 1) / kCompactThreads);
   return launch_pdl(compact_kernel, g, dim3(kCompactThreads), 0, stream, p);
 }
 
-cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream) {
+namespace {
+template <bool RAGGED>
+cudaError_t launch_copy_as(const CopyParams& p, int nsm, cudaStream_t stream) {
   const int64_t lines = (int64_t)p.n * p.page_lines;
   const dim3 threads(kCopyThreads);
   // Marking costs two more launches, about 2 us; searching the list costs every
   // CTA 1 us per 1,000 pairs and long equal shares a tenth of a large copy.
   if (lines < kCopyMarkedLines && p.n < kCopyMarkedPairs) {
     const int64_t grid = (lines + 1) / 2 < 5 * nsm ? (lines + 1) / 2 : 5 * nsm;
-    return launch_pdl(copy_pages_kernel<false>, dim3((unsigned)grid), threads, 0, stream, p);
+    return launch_pdl(copy_pages_kernel<false, RAGGED>, dim3((unsigned)grid), threads, 0, stream, p);
   }
   const int64_t blocks = ((int64_t)p.n + kCopyThreads - 1) / kCopyThreads;
   const dim3 marking((unsigned)(blocks < 4 * nsm ? blocks : 4 * nsm));
@@ -666,9 +670,15 @@ cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream)
   if (e != cudaSuccess) return e;
   int64_t grid = (lines + 15) / 16;
   if (grid > INT32_MAX) grid = INT32_MAX;
-  e = launch_pdl(copy_pages_kernel<true>, dim3((unsigned)grid), threads, 0, stream, p);
+  e = launch_pdl(copy_pages_kernel<true, RAGGED>, dim3((unsigned)grid), threads, 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(mark_pages_kernel<true>, marking, threads, 0, stream, p);
+}
+}  // namespace
+
+cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream) {
+  return p.page_vecs == p.page_lines * kCopyThreads ? launch_copy_as<false>(p, nsm, stream)
+                                                    : launch_copy_as<true>(p, nsm, stream);
 }
 
 }  // namespace ta

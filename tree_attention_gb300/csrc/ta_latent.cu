@@ -1,0 +1,329 @@
+// ta_latent.cu -- latent attention over a paged latent cache: appending tokens,
+// and absorbed attention of one token per sequence and of draft trees.
+//
+// The cache is [num_pages, 16, rank + rope_dim]: row j of a sequence is its
+// token's latent c_j and, behind it, the rotary key k_j that all heads share.
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "ta_device.cuh"
+#include "ta_launch.h"
+
+namespace ta {
+namespace {
+
+__device__ __forceinline__ void report_bad_tables(unsigned int* error) {
+  atomicOr(error, DEVERR_BAD_INDPTR);
+}
+
+// The largest b in [0, batch) with indptr[b] <= t, by one warp: 32 probes a
+// round.  Any contents end the search inside the range.
+__device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, int t, int lane) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33;
+    const int at = lo + (lane + 1) * step;
+    const bool le = at < hi && indptr[at] <= t;
+    lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 128;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& u, float2 (&x)[4]) {
+  x[0] = unpack2<BF16>(u.x);
+  x[1] = unpack2<BF16>(u.y);
+  x[2] = unpack2<BF16>(u.z);
+  x[3] = unpack2<BF16>(u.w);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(pack2<BF16>(x[0].x, x[0].y), pack2<BF16>(x[1].x, x[1].y),
+                    pack2<BF16>(x[2].x, x[2].y), pack2<BF16>(x[3].x, x[3].y));
+}
+
+// The two 16-byte vectors i and i + half_vecs of a rotary row of 16 half_vecs
+// elements, turned by (cos, sin) pairs cs: with halves as layout, element e of
+// the first is paired with element e of the second; interleaved, neighbours are.
+template <bool BF16, int LAYOUT>
+__device__ __forceinline__ void turn(uint4& u0, uint4& u1, const float2* cs, int i, int half_vecs) {
+  float2 a[4], b[4];
+  unpack8<BF16>(u0, a);
+  unpack8<BF16>(u1, b);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = a[k], y = b[k];
+    if (LAYOUT == 1) {
+      const float2 c0 = cs[8 * i + 2 * k], c1 = cs[8 * i + 2 * k + 1];
+      a[k] = make_float2(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+      b[k] = make_float2(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+    } else {
+      const float2 c0 = cs[4 * i + k], c1 = cs[4 * (i + half_vecs) + k];
+      a[k] = make_float2(x.x * c0.x - x.y * c0.y, x.y * c0.x + x.x * c0.y);
+      b[k] = make_float2(y.x * c1.x - y.y * c1.y, y.y * c1.x + y.x * c1.y);
+    }
+  }
+  u0 = pack8<BF16>(a);
+  u1 = pack8<BF16>(b);
+}
+
+// One CTA per token.  Its first warp looks up the token's cache row and moves
+// the latent and the rotary key, all of them the heads' rotary queries.
+template <bool BF16, int LAYOUT>
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendParams p) {
+  __shared__ float2 s_cs[32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = blockIdx.x;
+  const int half_vecs = p.rope_dim / 16, width = p.rank + p.rope_dim;
+  if (LAYOUT != 0 && tid < p.rope_dim / 2) {
+    // the fraction of a turn, exact modulo 1, then one rounding to float32
+    const uint64_t ph = (uint64_t)(int64_t)p.positions[t] * p.turns[tid];
+    float sn, cs;
+    sincospif((float)(int64_t)ph * 0x1p-63f, &sn, &cs);
+    s_cs[tid] = make_float2(cs * p.magnitude, sn * p.magnitude);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
+    const int a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
+    const int p0 = p.tab.page_indptr[b], p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
+    int64_t slot = -1;                     // element offset of its row; -1: none
+    if (a0 >= 0 && t >= a0 && t < a1 && a1 <= p.total_new && p0 >= 0 && p1 > p0 &&
+        p1 <= p.tab.nnz_pages && last >= 1 && last <= kPageSize) {
+      const int kv = (p1 - p0 - 1) * kPageSize + last, row = kv - (a1 - t);
+      if (kv >= a1 - a0) {
+        const int page = p.tab.page_values[p0 + row / kPageSize];
+        if (page >= 0 && page < p.tab.num_pages)
+          slot = ((int64_t)page * kPageSize + row % kPageSize) * width;
+      }
+    }
+    if (slot < 0 && lane == 0) report_bad_tables(p.error);
+    uint16_t* rows = p.rows_out ? p.rows_out + (int64_t)t * width : nullptr;
+    const int vecs = p.rank / 8;           // 32 or 64
+    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.latent_stride);
+    uint4 u[2];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u[i] = lane + 32 * i < vecs ? src[lane + 32 * i] : make_uint4(0, 0, 0, 0);
+      float2 x[4];
+      unpack8<BF16>(u[i], x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum += x[k].x * x[k].x + x[k].y * x[k].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = rsqrtf(sum / (float)p.rank + p.eps);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int v = lane + 32 * i;
+      if (v >= vecs) continue;
+      if (p.weight) {                      // without a norm the latent keeps its bits
+        float2 x[4], w[4];
+        unpack8<BF16>(u[i], x);
+        unpack8<BF16>(reinterpret_cast<const uint4*>(p.weight)[v], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = make_float2(x[k].x * inv * w[k].x, x[k].y * inv * w[k].y);
+        u[i] = pack8<BF16>(x);
+      }
+      if (slot >= 0) reinterpret_cast<uint4*>(p.pages + slot)[v] = u[i];
+      if (rows) reinterpret_cast<uint4*>(rows)[v] = u[i];
+    }
+    if (lane < half_vecs) {
+      const uint4* k = reinterpret_cast<const uint4*>(p.k_rope + t * p.k_rope_stride);
+      uint4 u0 = k[lane], u1 = k[lane + half_vecs];
+      if (LAYOUT != 0) turn<BF16, LAYOUT>(u0, u1, s_cs, lane, half_vecs);
+      if (slot >= 0) {
+        uint4* to = reinterpret_cast<uint4*>(p.pages + slot + p.rank);
+        to[lane] = u0;
+        to[lane + half_vecs] = u1;
+      }
+      if (rows) {
+        uint4* to = reinterpret_cast<uint4*>(rows + p.rank);
+        to[lane] = u0;
+        to[lane + half_vecs] = u1;
+      }
+    }
+  }
+  if (p.q_rope == nullptr) return;
+  for (int e = tid; e < p.h * half_vecs; e += kAppendThreads) {
+    const int h = e / half_vecs, i = e % half_vecs;
+    const uint4* q = reinterpret_cast<const uint4*>(p.q_rope + t * p.q_token_stride + h * p.q_head_stride);
+    uint4 u0 = q[i], u1 = q[i + half_vecs];
+    if (LAYOUT != 0) turn<BF16, LAYOUT>(u0, u1, s_cs, i, half_vecs);
+    uint4* to = reinterpret_cast<uint4*>(p.q_out + t * p.qo_token_stride + h * p.qo_head_stride);
+    to[i] = u0;
+    to[i + half_vecs] = u1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// absorbed attention
+// ---------------------------------------------------------------------------
+
+// What the tables say of one sequence: its kv rows, tree nodes and q rows.
+struct LatentSeq {
+  int p0, kv, m0, tree, q0, qo;
+  bool good;
+};
+__device__ __forceinline__ LatentSeq latent_seq(const LatentParams& p, int b) {
+  LatentSeq s;
+  const int p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
+  s.p0 = p.tab.page_indptr[b];
+  s.good = s.p0 >= 0 && p1 >= s.p0 && p1 <= p.tab.nnz_pages &&
+           (p1 == s.p0 || (last >= 1 && last <= kPageSize)) && (b > 0 || s.p0 == 0);
+  s.kv = s.good && p1 > s.p0 ? (p1 - s.p0 - 1) * kPageSize + last : 0;
+  s.m0 = s.tree = 0;
+  s.q0 = b;
+  s.qo = 1;
+  if (p.q_indptr) {
+    const int q1 = p.q_indptr[b + 1], m1 = p.mn_indptr[b + 1];
+    s.q0 = p.q_indptr[b];
+    s.m0 = p.mn_indptr[b];
+    s.qo = q1 - s.q0;
+    s.tree = m1 - s.m0;
+    s.good = s.good && s.q0 >= 0 && s.m0 >= 0 && q1 >= s.q0 && m1 >= s.m0 && s.qo <= s.tree &&
+             s.tree <= s.kv && (b > 0 || (s.q0 == 0 && s.m0 == 0)) &&
+             (b < p.tab.batch - 1 || (q1 == p.total_q && m1 == p.total_tree));
+  }
+  return s;
+}
+
+// One q row and head by one warp, row by row: a lane holds 8 elements of every
+// 256 of the row's latent, and lanes below rope_dim / 8 of its rotary key.
+template <bool BF16>
+__device__ void attend_row(const LatentParams& p, const LatentSeq& s, int r, int h, int lane) {
+  const int width = p.rank + p.rope_dim, parts = p.rank / 256;
+  const int64_t row = (int64_t)(s.q0 + r) * p.h + h;
+  float2 q[3][4], o[2][4];
+  const uint4* qp = reinterpret_cast<const uint4*>(p.q + row * width);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const bool mine = i < 2 ? i < parts : lane < p.rope_dim / 8;
+    unpack8<BF16>(mine ? qp[i < 2 ? lane + 32 * i : p.rank / 8 + lane] : zero, q[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[i][k] = make_float2(0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+  const int start = s.kv - s.tree;
+  const int2* order = reinterpret_cast<const int2*>(p.tree_order) + s.m0;
+  const int enter = s.tree ? order[s.tree - s.qo + r].x : 0;
+  for (int j = 0; j < s.kv; ++j) {
+    if (j >= start) {
+      const int2 iv = order[j - start];
+      if (iv.x > enter || enter >= iv.y) continue;
+    }
+    const int page = p.tab.page_values[s.p0 + j / kPageSize];
+    const bool in = page >= 0 && page < p.tab.num_pages;
+    const uint4* kp =
+        reinterpret_cast<const uint4*>(p.pages + ((int64_t)page * kPageSize + j % kPageSize) * width);
+    float2 x[3][4];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const bool mine = in && (i < 2 ? i < parts : lane < p.rope_dim / 8);
+      unpack8<BF16>(mine ? kp[i < 2 ? lane + 32 * i : p.rank / 8 + lane] : zero, x[i]);
+    }
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc = ffma2(q[i][k], x[i][k], acc);
+    float sc = acc.x + acc.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, d);
+    sc *= p.scale_log2;
+    if (sc == -INFINITY) continue;
+    if (sc > m) {
+      const float f = ex2_approx(m - sc);
+      m = sc;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] = make_float2(o[i][k].x * f, o[i][k].y * f);
+    }
+    const float w = ex2_approx(sc - m);
+    l += w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = ffma2(make_float2(w, w), x[i][k], o[i][k]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint4* out = reinterpret_cast<uint4*>(p.out + row * p.rank);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= parts) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[i][k] = make_float2(o[i][k].x * inv, o[i][k].y * inv);
+    out[lane + 32 * i] = pack8<BF16>(o[i]);
+  }
+  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + log2f(l);
+}
+
+constexpr int kRowThreads = 128;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kRowThreads) latent_rows_kernel(const LatentParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31;
+  bool bad = false;
+  for (int b = tid; b < p.tab.batch; b += kRowThreads) bad |= !latent_seq(p, b).good;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) report_bad_tables(p.error);
+    return;
+  }
+  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (tid >> 5);
+  if (i >= (int64_t)p.total_q * p.h) return;
+  const int row = (int)(i / p.h), h = (int)(i % p.h);
+  const int b = p.q_indptr ? find_sequence(p.q_indptr, p.tab.batch, row, lane) : row;
+  const LatentSeq s = latent_seq(p, b);
+  attend_row<BF16>(p, s, row - s.q0, h, lane);
+}
+
+}  // namespace
+
+LatentWorkspace latent_workspace(int num_pages, int nsm) {
+  (void)nsm;
+  LatentWorkspace w{};
+  w.off_parts = 256;
+  w.off_marks = w.off_parts;
+  w.total = w.off_marks + round_up((int64_t)num_pages * 4, 256);
+  return w;
+}
+
+cudaError_t launch_latent_append(const LatentAppendParams& p, bool bf16, cudaStream_t stream) {
+  auto kern = [&](auto a, auto b, auto c) {
+    return p.rope_layout == 1 ? a : p.rope_layout == 2 ? b : c;
+  };
+  return launch_pdl(bf16 ? kern(latent_append_kernel<true, 1>, latent_append_kernel<true, 2>,
+                                latent_append_kernel<true, 0>)
+                         : kern(latent_append_kernel<false, 1>, latent_append_kernel<false, 2>,
+                                latent_append_kernel<false, 0>),
+                    dim3(p.total_new), dim3(kAppendThreads), 0, stream, p);
+}
+
+cudaError_t launch_latent(const LatentParams& p, bool bf16, int nsm, cudaStream_t stream) {
+  (void)nsm;
+  const int64_t rows = (int64_t)p.total_q * p.h;
+  const int64_t grid = ceil_div(rows, kRowThreads / 32);
+  return launch_pdl(bf16 ? latent_rows_kernel<true> : latent_rows_kernel<false>,
+                    dim3((unsigned)grid), dim3(kRowThreads), 0, stream, p);
+}
+
+}  // namespace ta

@@ -1,6 +1,6 @@
 // ta_launch.h -- internal interface between the C-ABI host code (ta_api.cu)
 // and the kernel translation units (ta_plan.cu, ta_attn.cu, ta_merge.cu,
-// ta_cache.cu, ta_decode.cu).
+// ta_cache.cu, ta_decode.cu, ta_latent.cu, ta_expanded.cu).
 #pragma once
 
 #include <cuda.h>
@@ -194,7 +194,8 @@ struct CompactParams {
   const int32_t* accept_nodes;
   int32_t *new_indptr, *new_values, *new_length, *freed, *num_freed;
   unsigned int* error;
-  int total_accept, h_kv, row_vecs;       // row_vecs: 16-byte vectors per head row
+  int total_accept;
+  int planes, row_vecs;                   // of 16 rows each per page, 16-byte vectors per row
 };
 
 struct CopyParams {
@@ -202,8 +203,61 @@ struct CopyParams {
   const int32_t *src, *dst;
   unsigned int* error;
   int n, num_pages;
-  int page_lines;                         // 4 KB lines per page
+  int page_lines;                         // 4 KB lines per page, the last one maybe short
+  int page_vecs;                          // 16-byte vectors per page
   unsigned int* marks;                    // [num_pages], zero between calls
+};
+
+// A latent cache [num_pages, 16, rank + rope_dim] (ta_latent.cu).
+struct LatentAppendParams {
+  const uint16_t *latent, *k_rope, *q_rope;   // q_rope null: no queries
+  int64_t latent_stride, k_rope_stride, q_token_stride, q_head_stride;
+  const int32_t* append_indptr;
+  const int32_t* positions;
+  const uint16_t* weight;                 // null: no norm
+  uint16_t* pages;
+  uint16_t* q_out;
+  int64_t qo_token_stride, qo_head_stride;
+  uint16_t* rows_out;                     // null: not wanted
+  PageTable tab;
+  unsigned int* error;
+  int total_new, h, rank, rope_dim;
+  float eps;
+  int rope_layout;                        // 0: no rotation
+  float magnitude;
+  uint64_t turns[32];
+};
+
+struct LatentParams {
+  const uint16_t* q;
+  const uint16_t* pages;
+  uint16_t* out;
+  float* lse;
+  PageTable tab;
+  // trees; null (and total_q = batch) for one token per sequence
+  const int32_t *q_indptr, *mn_indptr, *tree_order;
+  int total_q, total_tree;
+  unsigned int* error;
+  int h, rank, rope_dim;
+  float scale_log2;                       // sm_scale * log2(e)
+};
+
+// Workspace of the latent calls: header | parts | marks.  The parts have the
+// same place and room whatever the dims.
+struct LatentWorkspace {
+  int64_t off_parts, off_marks, total;
+};
+LatentWorkspace latent_workspace(int num_pages, int nsm);
+
+struct ExpandedParams {
+  const uint16_t *q, *k, *k_rope, *v;
+  int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;   // token and head strides, elements
+  const int32_t *q_indptr, *kv_indptr;
+  uint16_t* out;
+  float* lse;
+  unsigned int* error;
+  int batch, total_q, total_kv, h, rope_dim;
+  float scale_log2;
 };
 
 // Plan kernel: sequence/tile enumeration, tile classification and LPT
@@ -244,6 +298,14 @@ cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int ns
 
 // Accepted tree nodes moved down, new page table, freed pages.
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+// The same three for a latent cache (one token per sequence and trees).
+cudaError_t launch_latent_append(const LatentAppendParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_latent(const LatentParams& p, bool bf16, int nsm, cudaStream_t stream);
+
+// Causal attention with keys and values per head and a shared rotary key.
+cudaError_t launch_expanded(const ExpandedParams& p, int head_dim, bool bf16, int nsm,
+                            cudaStream_t stream);
 
 // pages[dst[i]] = pages[src[i]].
 cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream);
