@@ -499,8 +499,9 @@ ta_status tree_attn_append_latent(const void* latent, int64_t latent_stride, con
  * rows gets out = 0 and lse = -inf).  A page index outside the pool reads zeros,
  * slots past a sequence's length are never used, a row whose score is -inf
  * counts as if it were not there, one whose score is NaN or +inf makes its head's
- * out NaN.  Weights are rounded to dtype before they meet the values (their sum
- * is of the rounded ones), all else is float32.  The result does not depend on timing.
+ * out NaN.  Weights are rounded to dtype before they meet the values (and out is
+ * divided by the sum of the rounded ones), all else is float32.  The result does
+ * not depend on timing.
  * Inconsistent page tables are reported by tree_attn_device_status and nothing
  * is computed.  q, pages and out 16-byte aligned.  Asynchronous on stream. */
 ta_status tree_attn_decode_latent(const void* q, const void* pages, const int32_t* page_indptr,
@@ -572,8 +573,8 @@ size_t tree_attn_expanded_workspace_size(const ta_expanded_dims* dims);
  * Every *_token_stride and *_head_stride in elements, multiples of 8, at least a
  * row, so that k and v may be views of one projection of the latents.  What a
  * q row does not see has no part in its result, whatever it holds.  Weights are
- * rounded to dtype before they meet the values (their sum is of the rounded
- * ones), all else is float32.  A row whose score is -inf counts as if it were not
+ * rounded to dtype before they meet the values (and out is divided by the sum of
+ * the rounded ones), all else is float32.  A row whose score is -inf counts as if it were not
  * there; one of NaN or +inf makes the result NaN.  Inconsistent indptr arrays are
  * reported by tree_attn_device_status and nothing is computed.  Pointers 16-byte
  * aligned.  Asynchronous on stream. */

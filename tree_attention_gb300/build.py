@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(PKG, "libtreeattn.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
 BINDING_STAMP = os.path.join(BUILD_DIR, "binding.txt")
 SOURCES = ["ta_api.cu", "ta_plan.cu", "ta_attn.cu", "ta_merge.cu", "ta_cache.cu", "ta_decode.cu",
-           "ta_latent.cu", "ta_expanded.cu"]
+           "ta_latent.cu", "ta_absorbed.cu", "ta_expanded.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -177,6 +177,30 @@ bool make_pages_map(CUtensorMap* m, const void* base, ta_dtype dt, int num_pages
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map of 16-bit elements with 128-byte swizzle: sizes of ``n`` dimensions,
+// the fastest first, strides (elements) of all but the first, box sizes.  Elements
+// outside read as zeros.
+template <int N>
+bool make_tiled_map(CUtensorMap* m, const void* base, ta_dtype dt, const int64_t (&size)[N],
+                    const int64_t (&stride)[N - 1], const int (&box)[N]) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[N], gstride[N - 1];
+  cuuint32_t gbox[N], estride[N];
+  for (int i = 0; i < N; ++i) {
+    gdim[i] = (cuuint64_t)size[i];
+    gbox[i] = (cuuint32_t)box[i];
+    estride[i] = 1u;
+    if (i) gstride[i - 1] = (cuuint64_t)stride[i - 1] * 2;
+  }
+  const CUtensorMapDataType t =
+      dt == TA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUresult r = fn(m, t, N, const_cast<void*>(base), gdim, gstride, gbox, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1192,8 +1216,25 @@ ta_status latent_attention(const void* q, const int32_t* q_indptr, int32_t total
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_failure();
-  return cuda_status(ta::launch_latent(p, dims->dtype == TA_BF16, nsm,
-                                       static_cast<cudaStream_t>(stream)));
+  const ta::LatentWorkspace layout = ta::latent_workspace(dims->num_pages, nsm);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.merge = reinterpret_cast<ta::LatentMerge*>(ws + layout.off_merge);
+  p.parts = reinterpret_cast<float*>(ws + layout.off_parts);
+  p.timeout_ns = wait_limit_ns();
+  p.debug_stall = g_stall;
+  const int64_t w = dims->rank + dims->rope_dim, page = w * ta::kPageSize;
+  const int64_t rows = (int64_t)total_q * dims->h_q, pool = dims->num_pages;
+  const int half = dims->rank / 128;
+  ta::AbsorbedMaps maps;
+  const int64_t chunked[4] = {64, ta::kPageSize, dims->rank / 64, pool};
+  if (!make_tiled_map<3>(&maps.q, q, dims->dtype, {w, rows, 1}, {w, w}, {64, 64, 1}) ||
+      !make_tiled_map<4>(&maps.k, pages, dims->dtype, chunked, {w, 64, page}, {64, 8, half, 1}) ||
+      !make_tiled_map<4>(&maps.v, pages, dims->dtype, chunked, {w, 64, page},
+                         {64, ta::kPageSize, half, 1}) ||
+      !make_tiled_map<3>(&maps.rot, pages, dims->dtype, {w, ta::kPageSize, pool}, {w, page}, {64, 8, 1}))
+    return cuda_failure();
+  return cuda_status(ta::launch_absorbed(p, maps, dims->dtype == TA_BF16, nsm,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

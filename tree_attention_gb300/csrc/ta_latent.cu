@@ -1,15 +1,12 @@
-// ta_latent.cu -- latent attention over a paged latent cache: appending tokens,
-// and absorbed attention of one token per sequence and of draft trees.
+// ta_latent.cu -- appending tokens to a paged latent cache.
 //
 // The cache is [num_pages, 16, rank + rope_dim]: row j of a sequence is its
 // token's latent c_j and, behind it, the rotary key k_j that all heads share.
 #include <cuda_runtime.h>
 
-#include <cfloat>
 #include <cstdint>
 
-#include "ta_device.cuh"
-#include "ta_launch.h"
+#include "ta_latent.cuh"
 
 namespace ta {
 namespace {
@@ -36,19 +33,6 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& u, float2 (&x)[4]) {
-  x[0] = unpack2<BF16>(u.x);
-  x[1] = unpack2<BF16>(u.y);
-  x[2] = unpack2<BF16>(u.z);
-  x[3] = unpack2<BF16>(u.w);
-}
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
-  return make_uint4(pack2<BF16>(x[0].x, x[0].y), pack2<BF16>(x[1].x, x[1].y),
-                    pack2<BF16>(x[2].x, x[2].y), pack2<BF16>(x[3].x, x[3].y));
-}
 
 // The two 16-byte vectors i and i + half_vecs of a rotary row of 16 half_vecs
 // elements, turned by (cos, sin) pairs cs: with halves as layout, element e of
@@ -168,144 +152,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
   }
 }
 
-// ---------------------------------------------------------------------------
-// absorbed attention
-// ---------------------------------------------------------------------------
-
-// What the tables say of one sequence: its kv rows, tree nodes and q rows.
-struct LatentSeq {
-  int p0, kv, m0, tree, q0, qo;
-  bool good;
-};
-__device__ __forceinline__ LatentSeq latent_seq(const LatentParams& p, int b) {
-  LatentSeq s;
-  const int p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
-  s.p0 = p.tab.page_indptr[b];
-  s.good = s.p0 >= 0 && p1 >= s.p0 && p1 <= p.tab.nnz_pages &&
-           (p1 == s.p0 || (last >= 1 && last <= kPageSize)) && (b > 0 || s.p0 == 0);
-  s.kv = s.good && p1 > s.p0 ? (p1 - s.p0 - 1) * kPageSize + last : 0;
-  s.m0 = s.tree = 0;
-  s.q0 = b;
-  s.qo = 1;
-  if (p.q_indptr) {
-    const int q1 = p.q_indptr[b + 1], m1 = p.mn_indptr[b + 1];
-    s.q0 = p.q_indptr[b];
-    s.m0 = p.mn_indptr[b];
-    s.qo = q1 - s.q0;
-    s.tree = m1 - s.m0;
-    s.good = s.good && s.q0 >= 0 && s.m0 >= 0 && q1 >= s.q0 && m1 >= s.m0 && s.qo <= s.tree &&
-             s.tree <= s.kv && (b > 0 || (s.q0 == 0 && s.m0 == 0)) &&
-             (b < p.tab.batch - 1 || (q1 == p.total_q && m1 == p.total_tree));
-  }
-  return s;
-}
-
-// One q row and head by one warp, row by row: a lane holds 8 elements of every
-// 256 of the row's latent, and lanes below rope_dim / 8 of its rotary key.
-template <bool BF16>
-__device__ void attend_row(const LatentParams& p, const LatentSeq& s, int r, int h, int lane) {
-  const int width = p.rank + p.rope_dim, parts = p.rank / 256;
-  const int64_t row = (int64_t)(s.q0 + r) * p.h + h;
-  float2 q[3][4], o[2][4];
-  const uint4* qp = reinterpret_cast<const uint4*>(p.q + row * width);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const bool mine = i < 2 ? i < parts : lane < p.rope_dim / 8;
-    unpack8<BF16>(mine ? qp[i < 2 ? lane + 32 * i : p.rank / 8 + lane] : zero, q[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[i][k] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  const int start = s.kv - s.tree;
-  const int2* order = reinterpret_cast<const int2*>(p.tree_order) + s.m0;
-  const int enter = s.tree ? order[s.tree - s.qo + r].x : 0;
-  for (int j = 0; j < s.kv; ++j) {
-    if (j >= start) {
-      const int2 iv = order[j - start];
-      if (iv.x > enter || enter >= iv.y) continue;
-    }
-    const int page = p.tab.page_values[s.p0 + j / kPageSize];
-    const bool in = page >= 0 && page < p.tab.num_pages;
-    const uint4* kp =
-        reinterpret_cast<const uint4*>(p.pages + ((int64_t)page * kPageSize + j % kPageSize) * width);
-    float2 x[3][4];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const bool mine = in && (i < 2 ? i < parts : lane < p.rope_dim / 8);
-      unpack8<BF16>(mine ? kp[i < 2 ? lane + 32 * i : p.rank / 8 + lane] : zero, x[i]);
-    }
-    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc = ffma2(q[i][k], x[i][k], acc);
-    float sc = acc.x + acc.y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sc += __shfl_xor_sync(0xffffffffu, sc, d);
-    sc *= p.scale_log2;
-    if (sc == -INFINITY) continue;
-    if (sc > m) {
-      const float f = ex2_approx(m - sc);
-      m = sc;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][k] = make_float2(o[i][k].x * f, o[i][k].y * f);
-    }
-    const float w = ex2_approx(sc - m);
-    l += w;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = ffma2(make_float2(w, w), x[i][k], o[i][k]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint4* out = reinterpret_cast<uint4*>(p.out + row * p.rank);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i >= parts) continue;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[i][k] = make_float2(o[i][k].x * inv, o[i][k].y * inv);
-    out[lane + 32 * i] = pack8<BF16>(o[i]);
-  }
-  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + log2f(l);
-}
-
-constexpr int kRowThreads = 128;
-
-template <bool BF16>
-__global__ void __launch_bounds__(kRowThreads) latent_rows_kernel(const LatentParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31;
-  bool bad = false;
-  for (int b = tid; b < p.tab.batch; b += kRowThreads) bad |= !latent_seq(p, b).good;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) report_bad_tables(p.error);
-    return;
-  }
-  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (tid >> 5);
-  if (i >= (int64_t)p.total_q * p.h) return;
-  const int row = (int)(i / p.h), h = (int)(i % p.h);
-  const int b = p.q_indptr ? find_sequence(p.q_indptr, p.tab.batch, row, lane) : row;
-  const LatentSeq s = latent_seq(p, b);
-  attend_row<BF16>(p, s, row - s.q0, h, lane);
-}
-
 }  // namespace
-
-LatentWorkspace latent_workspace(int num_pages, int nsm) {
-  (void)nsm;
-  LatentWorkspace w{};
-  w.off_parts = 256;
-  w.off_marks = w.off_parts;
-  w.total = w.off_marks + round_up((int64_t)num_pages * 4, 256);
-  return w;
-}
 
 cudaError_t launch_latent_append(const LatentAppendParams& p, bool bf16, cudaStream_t stream) {
   auto kern = [&](auto a, auto b, auto c) {
@@ -316,14 +163,6 @@ cudaError_t launch_latent_append(const LatentAppendParams& p, bool bf16, cudaStr
                          : kern(latent_append_kernel<false, 1>, latent_append_kernel<false, 2>,
                                 latent_append_kernel<false, 0>),
                     dim3(p.total_new), dim3(kAppendThreads), 0, stream, p);
-}
-
-cudaError_t launch_latent(const LatentParams& p, bool bf16, int nsm, cudaStream_t stream) {
-  (void)nsm;
-  const int64_t rows = (int64_t)p.total_q * p.h;
-  const int64_t grid = ceil_div(rows, kRowThreads / 32);
-  return launch_pdl(bf16 ? latent_rows_kernel<true> : latent_rows_kernel<false>,
-                    dim3((unsigned)grid), dim3(kRowThreads), 0, stream, p);
 }
 
 }  // namespace ta

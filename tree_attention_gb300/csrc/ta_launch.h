@@ -1,6 +1,7 @@
 // ta_launch.h -- internal interface between the C-ABI host code (ta_api.cu)
 // and the kernel translation units (ta_plan.cu, ta_attn.cu, ta_merge.cu,
-// ta_cache.cu, ta_decode.cu, ta_latent.cu, ta_expanded.cu).
+// ta_cache.cu, ta_decode.cu, ta_latent.cu, ta_absorbed.cu,
+// ta_expanded.cu).
 #pragma once
 
 #include <cuda.h>
@@ -208,7 +209,7 @@ struct CopyParams {
   unsigned int* marks;                    // [num_pages], zero between calls
 };
 
-// A latent cache [num_pages, 16, rank + rope_dim] (ta_latent.cu).
+// A latent cache [num_pages, 16, rank + rope_dim] (ta_latent.cu, ta_absorbed.cu).
 struct LatentAppendParams {
   const uint16_t *latent, *k_rope, *q_rope;   // q_rope null: no queries
   int64_t latent_stride, k_rope_stride, q_token_stride, q_head_stride;
@@ -240,12 +241,32 @@ struct LatentParams {
   unsigned int* error;
   int h, rank, rope_dim;
   float scale_log2;                       // sm_scale * log2(e)
+  struct LatentMerge* merge;              // [pairs of SMs]
+  float* parts;                           // [pairs][2] states, see ta_absorbed.cu
+  unsigned long long timeout_ns;
+  int debug_stall;                        // as in AttnParams
 };
 
-// Workspace of the latent calls: header | parts | marks.  The parts have the
-// same place and room whatever the dims.
+// The item of 128 packed rows that begins in one pair's range of tiles and ends
+// in another's: packed rows row0 .. row0 + nrows - 1 (of its sequence b: m_row
+// on), in ``parts`` parts; 0: there is none.
+struct LatentMerge {
+  int b, row0, m_row, nrows, parts, pad[3];
+};
+
+// Tensor maps of absorbed attention, all with 128-byte swizzle: q [rows * h, W] (box
+// {64, 64 rows}); of the pages [num_pages, 16, W] the latent as chunks of 64
+// elements, [num_pages, rank / 64, 16, 64], for keys (box {64, 8 rows, rank / 128
+// chunks, a page}) and values ({64, 16, rank / 128, 1}), and the whole rows, for the
+// rotary key ({64, 8, 1}; elements past a row's end read as zeros).
+struct AbsorbedMaps {
+  CUtensorMap q, k, v, rot;
+};
+
+// Workspace of the latent calls: header | merge records | parts | marks.  All but
+// the marks have the same place and room whatever the dims.
 struct LatentWorkspace {
-  int64_t off_parts, off_marks, total;
+  int64_t off_merge, off_parts, off_marks, total;
 };
 LatentWorkspace latent_workspace(int num_pages, int nsm);
 
@@ -299,9 +320,11 @@ cudaError_t launch_decode(const DecodeParams& p, int head_dim, bool bf16, int ns
 // Accepted tree nodes moved down, new page table, freed pages.
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
-// The same three for a latent cache (one token per sequence and trees).
+// Appends tokens to a latent cache; attention over it of one token per sequence
+// or of trees.
 cudaError_t launch_latent_append(const LatentAppendParams& p, bool bf16, cudaStream_t stream);
-cudaError_t launch_latent(const LatentParams& p, bool bf16, int nsm, cudaStream_t stream);
+cudaError_t launch_absorbed(const LatentParams& p, const AbsorbedMaps& maps, bool bf16, int nsm,
+                            cudaStream_t stream);
 
 // Causal attention with keys and values per head and a shared rotary key.
 cudaError_t launch_expanded(const ExpandedParams& p, int head_dim, bool bf16, int nsm,
