@@ -57,8 +57,13 @@ __device__ __forceinline__ uint32_t in_first_cta(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
+// Arrives on a barrier of the pair's first CTA, releasing to this CTA only: what
+// the arrivals here announce is this CTA's own shared memory, behind a proxy fence,
+// and tensor memory, which this SM's own units read.  (A release to the cluster
+// waits for all that its thread has under way, 1,000 to 4,000 cycles a time: with it
+// a tile took 6,500 cycles, whoever executed it.)
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -93,6 +98,17 @@ __device__ __forceinline__ void tma_load_pair_4d(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return (sw128_desc(addr, lbo) & ~((uint64_t)0x3FFF << 32)) | ((uint64_t)(sbo >> 4) << 32);
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+// Called within ``if (elect_one())``: in code that the compiler knows to be one
+// lane's by other means it moves the descriptors from the lane's registers to the
+// warp's before every product, 83 cycles a product instead of 40 to 65.
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
@@ -385,7 +401,7 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
 // The products: QK(t + 1) goes before PV(t), so that the softmax of one tile
 // runs beside the products of another.
 template <int RANK, bool BF16>
-__device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem) {
+__device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem, int lane) {
   using C = Cfg<RANK>;
   Misc& m = *cx.m;
   constexpr uint32_t idesc_qk = umma_idesc_f16(BF16, 128, 128, false);
@@ -398,73 +414,87 @@ __device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem) {
   uint32_t n = 0, it = 0, qt = 0;   // pieces, tiles whose PV, whose QK was issued
   const int rot_steps = p.rope_dim / 16;
   bool ok = true, issued = false;
-  if (p.debug_stall) ok = cx.wait(&m.stall, 0);
+  if (p.debug_stall) ok = cx.wait_warp(&m.stall, 0);
   auto qk = [&]() -> bool {
     const int b = qt & 1;
-    if (!cx.wait(&m.s_empty[b], ((qt >> 1) & 1) ^ 1)) return false;
+    if (!cx.wait_warp(&m.s_empty[b], ((qt >> 1) & 1) ^ 1)) return false;
     const uint32_t d = tmem + C::kTmemS + 64 * b;
     issued = true;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      if (!cx.wait(&m.k_full[g], qt & 1)) return false;
+      if (!cx.wait_warp(&m.k_full[g], qt & 1)) return false;
       tc_fence_after();
-      const uint64_t a = dq + (g * C::kHalf * kChunkBytes >> 4), x = dk + (g * C::kPages * C::kKBox >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int c = 0; c < C::kHalf; ++c)
+        for (int c = 0; c < C::kHalf; ++c)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_pair(d, a + ((c * kChunkBytes + k * 32) >> 4), x + ((c * 1024 + k * 32) >> 4), idesc_qk,
-                    g + c + k > 0 ? 1u : 0u);
-      commit_pair(&m.k_empty[g]);
+          for (int k = 0; k < 4; ++k)
+            umma_pair(d, dq + (((g * C::kHalf + c) * kChunkBytes + k * 32) >> 4),
+                      dk + ((g * C::kPages * C::kKBox + c * 1024 + k * 32) >> 4), idesc_qk,
+                      g + c + k > 0 ? 1u : 0u);
+        commit_pair(&m.k_empty[g]);
+      }
+      __syncwarp();
     }
-    if (!cx.wait(&m.k_full[2], qt & 1)) return false;
+    if (!cx.wait_warp(&m.k_full[2], qt & 1)) return false;
     tc_fence_after();
-#pragma unroll 1
-    for (int k = 0; k < rot_steps; ++k)
-      umma_pair(d, dq + ((2 * C::kHalf * kChunkBytes + k * 32) >> 4), dr + (k * 32 >> 4), idesc_qk, 1u);
-    commit_pair(&m.k_empty[2]);
-    commit_pair(&m.s_full[b]);
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < rot_steps)
+          umma_pair(d, dq + ((2 * C::kHalf * kChunkBytes + k * 32) >> 4), dr + (k * 32 >> 4), idesc_qk, 1u);
+      commit_pair(&m.k_empty[2]);
+      commit_pair(&m.s_full[b]);
+    }
+    __syncwarp();
     ++qt;
     return true;
   };
   for (; ok; ++n) {
     const int slot = n % kPieces;
-    if (!(ok = cx.wait(&m.piece_full[slot], (n / kPieces) & 1))) break;
+    if (!(ok = cx.wait_warp(&m.piece_full[slot], (n / kPieces) & 1))) break;
     const int t0 = m.piece[slot].t0, t1 = m.piece[slot].t1, kv = m.piece[slot].kv;
-    mbar_arrive(&m.piece_empty[slot]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.piece_empty[slot]);
     if (t0 == t1) break;
-    if (!(ok = cx.wait(&m.q_full, n & 1))) break;
+    if (!(ok = cx.wait_warp(&m.q_full, n & 1))) break;
     if (!(ok = qk())) break;
-    if (t1 - t0 == 1) commit_pair(&m.q_empty);
+    if (t1 - t0 == 1 && elect_one()) commit_pair(&m.q_empty);
+    __syncwarp();
     for (int t = t0; t < t1; ++t, ++it) {
       if (t + 1 < t1) {
         if (!(ok = qk())) break;
-        if (t + 2 == t1) commit_pair(&m.q_empty);
+        if (t + 2 == t1 && elect_one()) commit_pair(&m.q_empty);
+        __syncwarp();
       }
-      if (t == t0 && !(ok = cx.wait(&m.o_empty, (n & 1) ^ 1))) break;
-      if (!(ok = cx.wait(&m.p_full, it & 1))) break;
+      if (t == t0 && !(ok = cx.wait_warp(&m.o_empty, (n & 1) ^ 1))) break;
+      if (!(ok = cx.wait_warp(&m.p_full, it & 1))) break;
       const int steps = min(C::kPages, (kv - t * kTile + kPageSize - 1) / kPageSize);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        if (!(ok = cx.wait(&m.v_ready[g], it & 1))) break;
+        if (!(ok = cx.wait_warp(&m.v_ready[g], it & 1))) break;
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = g * (C::kPages / 2); k < (g + 1) * (C::kPages / 2); ++k)
-          if (k < steps)
+          for (int k = g * (C::kPages / 2); k < (g + 1) * (C::kPages / 2); ++k)
+            if (k < steps)
 #pragma unroll
-            for (int j = 0; j < C::kHalf / 2; ++j)
-              umma_pair(tmem + C::kTmemO + 128 * j,
-                        dp + ((uint32_t)((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
-                        dv + ((uint32_t)(k * C::kVBox + j * 2 * kPageSize * 128) >> 4), idesc_pv,
-                        t > t0 || k > 0 ? 1u : 0u);
-        commit_pair(&m.v_empty[g]);
+              for (int j = 0; j < C::kHalf / 2; ++j)
+                umma_pair(tmem + C::kTmemO + 128 * j,
+                          dp + (((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
+                          dv + ((k * C::kVBox + j * 2 * kPageSize * 128) >> 4), idesc_pv,
+                          k > 0 ? 1u : (uint32_t)(t > t0));
+          commit_pair(&m.v_empty[g]);
+          if (g == 1) commit_pair(&m.pv_done);
+        }
+        __syncwarp();
       }
       if (!ok) break;
-      commit_pair(&m.pv_done);
     }
   }
   if (!ok && issued) {
-    commit_pair(&m.drain);
+    if (elect_one()) commit_pair(&m.drain);
+    __syncwarp();
     const uint64_t t0 = globaltimer_ns();
     while (!try_wait_cluster(&m.drain, 0) && globaltimer_ns() - t0 < 10000000ull) {}
   }
@@ -505,7 +535,6 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
   const int part = half * 2 + wg;                // of the row's four threads
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const uint32_t o_at = tmem + lanes + C::kTmemO + wg * C::kCols;
-  const uint32_t p_full = in_first_cta(&m.p_full), o_empty = in_first_cta(&m.o_empty);
   uint8_t* p_row = cx.smem + C::kOffP + wg * kChunkBytes + rr * 128;
   uint32_t n = 0, it = 0, turn = 0;
   // the four threads of a row give a number each and get all four combined (an
@@ -612,7 +641,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
         return;   // no warp is a phase of p_full ahead
       }
       __syncwarp();
-      if (lane == 0) arrive_remote(p_full);
+      if (lane == 0) arrive_remote(in_first_cta(&m.p_full));
     }
     // the piece's result
     if (!cx.wait_warp(&m.pv_done, (it - 1) & 1)) return;
@@ -675,7 +704,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) arrive_remote(o_empty);
+    if (lane == 0) arrive_remote(in_first_cta(&m.o_empty));
   }
 }
 
@@ -689,7 +718,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t cta = cta_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
-    const uint32_t readers = cta == 0 ? 11 : 10;
     mbar_init(&m.q_full, 1);
     mbar_init(&m.q_empty, 1);
     for (int i = 0; i < 3; ++i) {
@@ -708,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&m.o_empty, 16);
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&m.piece_full[i], 1);
-      mbar_init(&m.piece_empty[i], readers);
+      mbar_init(&m.piece_empty[i], cta == 0 ? 11 : 10);   // its readers
     }
     for (int i = 0; i < 4; ++i) mbar_init(&m.shared_rows[i >> 1][i & 1], 4);
     mbar_init(&m.stall, 1);
@@ -797,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       run_v_producer<RANK>(cx, p, maps, cta, lane);
     else if (warp == 10) {
-      if (cta == 0 && lane == 0) run_mma<RANK, BF16>(cx, p, m.tmem);
+      if (cta == 0) run_mma<RANK, BF16>(cx, p, m.tmem, lane);
     } else if (lane == 0)
       run_planner(cx, p, split, pair, cta == 0);
   }
