@@ -37,6 +37,7 @@ constexpr int kTile = 128;                 // kv rows, packed rows
 constexpr int kChunkBytes = 64 * 128;      // 64 rows of 64 elements
 constexpr int kThreads = 384;
 constexpr int kPieces = 4;                 // records ahead
+constexpr int kAhead = 2;                  // tiles
 constexpr int kSlotFloats = kTile * (512 + 3);   // O, reference, sums (see run_softmax)
 
 // ---------------------------------------------------------------------------
@@ -93,6 +94,13 @@ __device__ __forceinline__ void tma_load_pair_4d(uint32_t dst, const CUtensorMap
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
+}
+// The same into L2 only.
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
 }
 // sw128_desc with any distance between groups of 8 rows
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -363,10 +371,18 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
     __syncwarp();
     if (lane == 0) mbar_arrive(&m.piece_empty[slot]);
     if (x.t0 == x.t1) return;
-    int next = page_of(p, x, x.t0, lane);
+    int next = page_of(p, x, x.t0, lane), after = x.t0 + 1 < x.t1 ? page_of(p, x, x.t0 + 1, lane) : 0;
     for (int t = x.t0; t < x.t1; ++t, ++it) {
       const int page = next;
-      if (t + 1 < x.t1) next = page_of(p, x, t + 1, lane);
+      next = after;
+      // K has room for one tile, so the memory's latency would be in every tile's way:
+      // this CTA's half of the tile after the next goes into L2 ahead of it
+      if (t + kAhead < x.t1) {
+        after = page_of(p, x, t + kAhead, lane);
+        if (lane < C::kPages && after < p.tab.num_pages)
+          tma_prefetch_l2_4d(&maps.v, 0, 0, (int)cta * C::kHalf, after);
+        __syncwarp();
+      }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (!cx.wait_warp(&m.v_empty[g], (it & 1) ^ 1)) return;
@@ -847,97 +863,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 256;
-constexpr int kMergeVecs = 8;      // of 4 columns, per CTA
+constexpr int kMergeThreads = 256;   // 32 packed rows by 8 warps
+constexpr int kMaxPairs = 128;
 
-// CTA (pair, y): the item that begins in this pair's range and ends in another's,
-// 32 columns.  A thread has a row and a share of the parts; shares are added up
-// in order, so results do not depend on timing.
+// One unit of work: 32 rows by 32 V columns of an item, V vectors of 4 columns and B
+// of its parts in flight per thread.
+template <int RANK, bool BF16, int V, int B>
+__device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMerge& r, int pair,
+                                           int row0, int slice, uint2 (*s_out)[8 * V + 1]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = row0 + lane;
+  const bool valid = row < r.nrows;
+  const int at = min(row, r.nrows - 1);
+  float top = -FLT_MAX, l = 0.f, lr = 0.f;
+  float4 o[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < r.parts; k0 += B) {
+    float4 v[B][V];
+    float pm[B], pl[B], pr[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      pm[k] = -FLT_MAX;
+      pl[k] = pr[k] = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < r.parts) {
+        const float* st = p.parts + (int64_t)(2 * (pair + k0 + k) + (k0 + k == 0)) * kSlotFloats;
+        pm[k] = __ldcg(st + kTile * 512 + at);
+        pl[k] = __ldcg(st + kTile * 513 + at);
+        pr[k] = __ldcg(st + kTile * 514 + at);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          v[k][j] = __ldcg(reinterpret_cast<const float4*>(st) + ((slice * 8 + warp) * V + j) * kTile + at);
+      }
+    }
+    float to = top;
+#pragma unroll
+    for (int k = 0; k < B; ++k) to = fmaxf(to, pm[k]);
+    const float f = ex2_approx(top - to);
+    top = to;
+    l *= f;
+    lr *= f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = make_float4(o[j].x * f, o[j].y * f, o[j].z * f, o[j].w * f);
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const float w = ex2_approx(pm[k] - top);
+      l += w * pl[k];
+      lr += w * pr[k];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        o[j].x += w * v[k][j].x;
+        o[j].y += w * v[k][j].y;
+        o[j].z += w * v[k][j].z;
+        o[j].w += w * v[k][j].w;
+      }
+    }
+  }
+  const float inv = lr == 0.f ? 0.f : 1.f / lr;
+  float odd = 0.f;
+  __syncthreads();                             // s_out is read from the unit before
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    odd += (o[j].x + o[j].y) * 0.f + (o[j].z + o[j].w) * 0.f;
+    s_out[lane][warp * V + j] =
+        make_uint2(pack2<BF16>(o[j].x * inv, o[j].y * inv), pack2<BF16>(o[j].z * inv, o[j].w * inv));
+  }
+  const int64_t first = (int64_t)r.row0 + row0;
+  if (warp == 0 && slice == 0 && valid) p.lse[first + lane] = l == 0.f ? -INFINITY : top + log2f(l);
+  __syncthreads();
+  // 64 V contiguous bytes of every row
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = tid + j * kMergeThreads, orow = i / (8 * V), c = i % (8 * V);
+    if (row0 + orow < r.nrows)
+      *reinterpret_cast<uint2*>(p.out + (first + orow) * RANK + (slice * 8 * V + c) * 4) = s_out[orow][c];
+  }
+  // a value that is not finite, though the weights are: it may be one that does not count
+  const unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
+  if (__syncthreads_or(again != 0)) {
+    for (int i = 0; i < 32; ++i) {
+      if (!(again >> i & 1)) continue;
+      const int x = r.m_row + row0 + i, e0 = ((slice * 8 + warp) * V * 4) & ~7;
+      latent_row_exact<BF16>(p, r.b, x / p.h, x % p.h, e0, e0 + (V > 1 ? 4 * V : 8));
+    }
+  }
+}
+
+// Joins the parts of the items that several pairs share, in their order.  All items'
+// units are shared out over one resident wave of CTAs: large units where there are
+// enough of them (each costs its loads' latency once), small ones where not.
 template <int RANK, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) absorbed_merge_kernel(const LatentParams p) {
-  __shared__ float s_o[kMergeThreads][4 * kMergeVecs + 1];
-  __shared__ float2 s_l[kMergeThreads];
+__global__ void __launch_bounds__(kMergeThreads) absorbed_merge_kernel(const LatentParams p, int pairs) {
+  __shared__ int s_at[kMaxPairs + 1];          // groups of 32 rows before each item
+  __shared__ LatentMerge s_rec[kMaxPairs];
+  __shared__ uint2 s_out[32][33];
   pdl_wait();
   pdl_trigger();
-  const int pair = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const LatentMerge r = p.merge[pair];
-  if (r.parts == 0) return;
-  // rows to a power of two, so that a warp's threads have rows next to one another
-  int rows = 16;
-  while (rows < r.nrows) rows *= 2;
-  const int share = kMergeThreads / rows, row = tid % rows, k0 = tid / rows;
-  const bool valid = row < r.nrows;
-  auto part = [&](int k) { return p.parts + (int64_t)(2 * (pair + k) + (k == 0)) * kSlotFloats; };
-  float top = -FLT_MAX;
-  if (valid)
-    for (int k = 0; k < r.parts; ++k) top = fmaxf(top, __ldcg(part(k) + kTile * 512 + row));
-  float l = 0.f, lr = 0.f, o[4 * kMergeVecs];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < pairs) s_rec[tid] = p.merge[tid];
+  __syncthreads();
+  if (tid < 32) {
+    int sum = 0;
+    for (int base = 0; base < pairs; base += 32) {
+      const int i = base + lane;
+      const int n = i < pairs && s_rec[i].parts > 0 ? (s_rec[i].nrows + 31) / 32 : 0;
+      int up = n;
 #pragma unroll
-  for (int i = 0; i < 4 * kMergeVecs; ++i) o[i] = 0.f;
-  if (valid) {
-    for (int k = k0; k < r.parts; k += share) {
-      const float* st = part(k);
-      const float4* y = reinterpret_cast<const float4*>(st) + blockIdx.y * kMergeVecs * kTile + row;
-      const float w = ex2_approx(__ldcg(st + kTile * 512 + row) - top);
-      float4 v[kMergeVecs];
-#pragma unroll
-      for (int i = 0; i < kMergeVecs; ++i) v[i] = __ldcg(y + i * kTile);
-      l += w * __ldcg(st + kTile * 513 + row);
-      lr += w * __ldcg(st + kTile * 514 + row);
-#pragma unroll
-      for (int i = 0; i < kMergeVecs; ++i) {
-        o[4 * i] += w * v[i].x;
-        o[4 * i + 1] += w * v[i].y;
-        o[4 * i + 2] += w * v[i].z;
-        o[4 * i + 3] += w * v[i].w;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up += y;
       }
+      if (i < pairs) s_at[i] = sum + up - n;
+      sum += __shfl_sync(0xffffffffu, up, 31);
     }
+    if (lane == 0) s_at[pairs] = sum;
   }
-  if (share > 1) {
-#pragma unroll
-    for (int i = 0; i < 4 * kMergeVecs; ++i) s_o[tid][i] = o[i];
-    s_l[tid] = make_float2(l, lr);
-    __syncthreads();
-    if (k0 == 0) {
-      for (int k = 1; k < share; ++k) {
-        const int from = k * rows + row;
-        l += s_l[from].x;
-        lr += s_l[from].y;
-#pragma unroll
-        for (int i = 0; i < 4 * kMergeVecs; ++i) o[i] += s_o[from][i];
-      }
-    }
-  }
-  if (tid - lane >= rows) return;   // whole warps
-  const bool mine = valid && k0 == 0;
-  const int64_t at = (int64_t)r.row0 + row;
-  const float inv = lr == 0.f ? 0.f : 1.f / lr;
-  uint4* out = reinterpret_cast<uint4*>(p.out + at * RANK + blockIdx.y * kMergeVecs * 4);
-  float odd = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4 * kMergeVecs; ++i) {
-    odd += o[i] * 0.f;
-    o[i] *= inv;
-  }
-  if (mine) {
-#pragma unroll
-    for (int i = 0; i < kMergeVecs / 2; ++i)
-      out[i] = make_uint4(pack2<BF16>(o[8 * i], o[8 * i + 1]), pack2<BF16>(o[8 * i + 2], o[8 * i + 3]),
-                          pack2<BF16>(o[8 * i + 4], o[8 * i + 5]), pack2<BF16>(o[8 * i + 6], o[8 * i + 7]));
-    if (blockIdx.y == 0) p.lse[at] = l == 0.f ? -INFINITY : top + log2f(l);
-  }
-  unsigned again = __ballot_sync(0xffffffffu, mine && odd != 0.f && l < INFINITY);
-  while (again) {
-    const int i = __ffs(again) - 1;
-    again &= again - 1;
-    const int x = r.m_row + tid - lane + i, e0 = blockIdx.y * kMergeVecs * 4;
-    __syncwarp();
-    latent_row_exact<BF16>(p, r.b, x / p.h, x % p.h, e0, e0 + 4 * kMergeVecs);
+  __syncthreads();
+  const int groups = s_at[pairs];
+  const bool large = groups * (RANK / 128) * 2 >= (int)gridDim.x;
+  const int slices = large ? RANK / 128 : RANK / 32;
+  for (int u = blockIdx.x; u < groups * slices; u += gridDim.x) {
+    // the last item that begins at or before u's group (those without any begin where
+    // the next does)
+    const int g = u / slices;
+    int pair = 0;
+    for (int step = kMaxPairs / 2; step > 0; step >>= 1)
+      if (pair + step < pairs && s_at[pair + step] <= g) pair += step;
+    const int row0 = (g - s_at[pair]) * 32;
+    if (large)
+      merge_unit<RANK, BF16, 4, 4>(p, s_rec[pair], pair, row0, u % slices, s_out);
+    else
+      merge_unit<RANK, BF16, 1, 8>(p, s_rec[pair], pair, row0, u % slices,
+                                   reinterpret_cast<uint2(*)[9]>(s_out));
   }
 }
 
 template <int RANK, bool BF16>
-cudaError_t launch(const LatentParams& p, const AbsorbedMaps& maps, int pairs, cudaStream_t stream) {
+cudaError_t launch(const LatentParams& p, const AbsorbedMaps& maps, int pairs, int nsm,
+                   cudaStream_t stream) {
   using C = Cfg<RANK>;
   constexpr int smem = C::kOffMisc + (int)sizeof(Misc);
   static_assert(smem <= 232448, "shared memory of an SM");
@@ -947,11 +1011,13 @@ cudaError_t launch(const LatentParams& p, const AbsorbedMaps& maps, int pairs, c
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), smem, stream, maps, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(absorbed_merge_kernel<RANK, BF16>, dim3(pairs, RANK / (4 * kMergeVecs)),
-                    dim3(kMergeThreads), 0, stream, p);
+  // a table of no more pages than a tile's has no item of two tiles
+  if (p.tab.nnz_pages <= kTile / kPageSize) return cudaSuccess;
+  return launch_pdl(absorbed_merge_kernel<RANK, BF16>, dim3(4 * nsm), dim3(kMergeThreads), 0, stream,
+                    p, pairs);
 }
 
-int max_pairs(int nsm) { return nsm >= 2 ? nsm / 2 : 1; }
+int max_pairs(int nsm) { return nsm < 4 ? 1 : nsm / 2 < kMaxPairs ? nsm / 2 : kMaxPairs; }
 
 }  // namespace
 
@@ -973,10 +1039,10 @@ cudaError_t launch_absorbed(const LatentParams& p, const AbsorbedMaps& maps, boo
   int pairs = max_pairs(nsm);
   if (kv_tiles * row_tiles < pairs) pairs = (int)(kv_tiles * row_tiles);
   if (p.rank == 512)
-    return bf16 ? launch<512, true>(p, maps, pairs, stream)
-                : launch<512, false>(p, maps, pairs, stream);
-  return bf16 ? launch<256, true>(p, maps, pairs, stream)
-              : launch<256, false>(p, maps, pairs, stream);
+    return bf16 ? launch<512, true>(p, maps, pairs, nsm, stream)
+                : launch<512, false>(p, maps, pairs, nsm, stream);
+  return bf16 ? launch<256, true>(p, maps, pairs, nsm, stream)
+              : launch<256, false>(p, maps, pairs, nsm, stream);
 }
 
 }  // namespace ta
