@@ -573,8 +573,7 @@ size_t tree_attn_expanded_workspace_size(const ta_expanded_dims* dims);
  * Every *_token_stride and *_head_stride in elements, multiples of 8, at least a
  * row, so that k and v may be views of one projection of the latents.  What a
  * q row does not see has no part in its result, whatever it holds.  Weights are
- * rounded to dtype before they meet the values (and out is divided by the sum of
- * the rounded ones), all else is float32.  A row whose score is -inf counts as if it were not
+ * rounded to dtype before they meet the values, all else is float32.  A row whose score is -inf counts as if it were not
  * there; one of NaN or +inf makes the result NaN.  Inconsistent indptr arrays are
  * reported by tree_attn_device_status and nothing is computed.  Pointers 16-byte
  * aligned.  Asynchronous on stream. */

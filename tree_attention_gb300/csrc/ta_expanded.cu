@@ -1,7 +1,25 @@
 // ta_expanded.cu -- causal attention in the expanded form of latent attention:
 // keys and values per head, and a rotary key that the heads share.
+//
+//   s = log2(e) sm_scale (q[:d] . k + q[d:] . k_rope),  out = sum 2^(s - lse) v,
+//   lse = log2 sum 2^s,  over the kv rows up to the q row's own
+//
+// 2 (2 d + rope_dim) operations per pair of q row and kv row: bound by the tensor
+// cores for prompts of some hundred rows, by the memory below.
+//
+// * A unit of work is 256 q rows of one sequence and head, two tiles of 128 (A and
+//   B) that read the same kv tiles of 128 rows.  A CTA per SM takes every
+//   gridDim.x-th unit, the last rows of a sequence (the most kv tiles) first.
+// * The products alternate: PV_A(t-1) QK_A(t) PV_B(t-1) QK_B(t), so that one
+//   tile's softmax runs beside the other tile's products.  P lies over its own S in
+//   tensor memory, and products of one thread execute in order.
+// * Keys (three chunks of 64 elements, the last the rotary one) and values (two
+//   halves of 64 rows) pass through one ring of eight 16 KB slots, so that a tile's
+//   values arrive where the tile before had its keys.
+// * One softmax thread per q row.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 
@@ -11,18 +29,72 @@
 namespace ta {
 namespace {
 
-constexpr int kRowThreads = 128;
+constexpr int kThreads = 384;
+constexpr int kTile = 128;
+constexpr int kSlots = 8;
+constexpr int kSlotBytes = 16384;
+constexpr int kItems = 4;            // records ahead
 
-__device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, int t, int lane) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 32) / 33;
-    const int at = lo + (lane + 1) * step;
-    const bool le = at < hi && indptr[at] <= t;
-    lo += __popc(__ballot_sync(0xffffffffu, le)) * step;
-    hi = min(hi, lo + step);
+struct Item {
+  int b, head, q0, nq;     // q rows q0 .. q0 + nq - 1 of the batch
+  int first;               // the kv row of the sequence that q0 is
+  int kv0, kv;             // the sequence's rows
+  int na, nb;              // kv tiles of tiles A and B; na 0: no more items
+};
+
+struct Misc {
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t v_short[2], v_clean[2];   // a sequence's last tile, which is cleaned before use
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], item_full[kItems], item_empty[kItems];
+  uint64_t stall, drain;
+  Item item[kItems];
+  uint32_t tmem;
+  int abort;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kC = D / 64;                 // chunks of a head's part
+  static constexpr int kQTile = (kC + 1) * kSlotBytes;
+  static constexpr int kOffQ = 0, kOffRing = 2 * kQTile;
+  static constexpr int kOffMisc = kOffRing + kSlots * kSlotBytes;
+  static constexpr int kPerTile = kC + 1 + 2;       // slots a kv tile takes: K, rotary K, V, V
+  static constexpr int kTmemS = 0, kTmemO = 256;    // of tile A; B 128 columns on
+};
+
+struct Ctx {
+  uint8_t* smem;
+  Misc* m;
+  unsigned int* error;
+  uint64_t limit_ns;
+  __device__ __forceinline__ bool expired(uint64_t t0) const {
+    if (*(volatile int*)&m->abort) return true;
+    if (globaltimer_ns() - t0 <= limit_ns) return false;
+    atomicOr(error, DEVERR_TIMEOUT);
+    *(volatile int*)&m->abort = 1;
+    return true;
   }
-  return lo;
+  // by a whole warp, with one answer for all lanes; at most limit_ns, or until
+  // another warp gave up
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_long(bar, parity);
+  }
+  __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) const {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t spins = 1;; ++spins) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      if ((spins & 63u) == 0 && __any_sync(0xffffffffu, expired(t0))) return false;
+    }
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ bool good_sequence(const ExpandedParams& p, int b) {
@@ -32,11 +104,13 @@ __device__ __forceinline__ bool good_sequence(const ExpandedParams& p, int b) {
          (b < p.batch - 1 || (q1 == p.total_q && k1 == p.total_kv));
 }
 
-// One q row and head by one warp, kv row by kv row; a lane holds D / 32
-// elements of a head's part and 2 of the rotary part (lanes below rope_dim / 2).
+// One q row and head by one warp, kv row by kv row; a lane holds D / 32 elements
+// of a head's part and 2 of the rotary part (lanes below rope_dim / 2).  For rows in
+// which the matrix products met a value that is not finite in a row not seen.
 template <int D, bool BF16>
-__device__ void attend_row(const ExpandedParams& p, int b, int row, int h, int lane) {
+__device__ __noinline__ void row_exact(const ExpandedParams& p, int b, int row, int h) {
   constexpr int E = D / 64;
+  const int lane = threadIdx.x & 31;
   const int k0 = p.kv_indptr[b];
   const int n = p.kv_indptr[b + 1] - k0 - (p.q_indptr[b + 1] - row) + 1;   // rows it sees
   const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q + row * p.q_ts + h * p.q_hs);
@@ -48,6 +122,7 @@ __device__ void attend_row(const ExpandedParams& p, int b, int row, int h, int l
     o[i] = make_float2(0.f, 0.f);
   }
   float m = -INFINITY, l = 0.f;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const int64_t at = k0 + j;
     const uint32_t* kp = reinterpret_cast<const uint32_t*>(p.k + at * p.k_ts + h * p.k_hs);
@@ -75,40 +150,517 @@ __device__ void attend_row(const ExpandedParams& p, int b, int row, int h, int l
     for (int i = 0; i < E; ++i) o[i] = ffma2(make_float2(w, w), unpack2<BF16>(vp[lane + 32 * i]), o[i]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = (int64_t)row * p.h + h;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * D);
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((int64_t)row * p.h + h) * D);
 #pragma unroll
   for (int i = 0; i < E; ++i) out[lane + 32 * i] = pack2<BF16>(o[i].x * inv, o[i].y * inv);
-  if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+}
+
+// ---------------------------------------------------------------------------
+// roles
+// ---------------------------------------------------------------------------
+
+// Every gridDim.x-th unit, counted sequence by sequence, in one from the last 256
+// rows on, head by head; 32 sequences at a time.
+__device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) {
+  Misc& m = *cx.m;
+  long long u = blockIdx.x, base = 0;
+  int b0 = -32, q0 = 0, qo = 0, k0 = 0, kv = 0;
+  long long before = 0, units = 0, total = 0;
+  for (uint32_t n = 0;; ++n) {
+    while (u >= base + total && b0 + 32 < p.batch) {
+      base += total;
+      b0 += 32;
+      const int b = b0 + lane;
+      units = 0;
+      if (b < p.batch) {
+        q0 = p.q_indptr[b];
+        qo = p.q_indptr[b + 1] - q0;
+        k0 = p.kv_indptr[b];
+        kv = p.kv_indptr[b + 1] - k0;
+        units = (long long)((qo + 2 * kTile - 1) / (2 * kTile)) * p.h;
+      }
+      long long up = units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up += y;
+      }
+      before = up - units;
+      total = __shfl_sync(0xffffffffu, up, 31);
+    }
+    Item x{};
+    if (u < base + total) {
+      const long long in = u - base - before;
+      const int src = __ffs(__ballot_sync(0xffffffffu, in >= 0 && in < units)) - 1;
+      if (lane == src) {
+        const int pairs = (qo + 2 * kTile - 1) / (2 * kTile);
+        const int r0 = (pairs - 1 - (int)(in / p.h)) * 2 * kTile;
+        x.b = b0 + lane;
+        x.head = (int)(in % p.h);
+        x.q0 = q0 + r0;
+        x.nq = min(2 * kTile, qo - r0);
+        x.first = kv - qo + r0;
+        x.kv0 = k0;
+        x.kv = kv;
+        x.na = (x.first + min(kTile, x.nq) + kTile - 1) / kTile;
+        x.nb = x.nq > kTile ? (x.first + x.nq + kTile - 1) / kTile : 0;
+      }
+      const int slot = n % kItems;
+      if (!cx.wait(&m.item_empty[slot], ((n / kItems) & 1) ^ 1)) return;
+      if (lane == src) {
+        m.item[slot] = x;
+        mbar_arrive(&m.item_full[slot]);
+      }
+      __syncwarp();
+      u += gridDim.x;
+    } else {
+      const int slot = n % kItems;
+      if (!cx.wait(&m.item_empty[slot], ((n / kItems) & 1) ^ 1)) return;
+      if (lane == 0) {
+        m.item[slot] = x;
+        mbar_arrive(&m.item_full[slot]);
+      }
+      return;
+    }
+  }
+}
+
+// The next record, for a whole warp.
+__device__ __forceinline__ bool next_item(const Ctx& cx, uint32_t n, int lane, Item& x) {
+  const int slot = n % kItems;
+  if (!cx.wait(&cx.m->item_full[slot], (n / kItems) & 1)) return false;
+  x = cx.m->item[slot];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&cx.m->item_empty[slot]);
+  return x.na > 0;
+}
+
+template <int D>
+__device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) {
+  using C = Cfg<D>;
+  Misc& m = *cx.m;
+  uint32_t it = 0, chunk = 0, units[2] = {0, 0};
+  Item x;
+  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
+    auto load_q = [&](int tile) {
+      if (!cx.wait(&m.q_empty[tile], (units[tile] & 1) ^ 1)) return false;
+      ++units[tile];
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&m.q_full[tile], C::kQTile);
+        for (int c = 0; c <= C::kC; ++c)
+          tma_load_3d(cx.smem + C::kOffQ + tile * C::kQTile + c * kSlotBytes, &maps.q, &m.q_full[tile],
+                      64 * c, x.head, x.q0 + tile * kTile);
+      }
+      __syncwarp();
+      return true;
+    };
+    // the ring slot of this producer's next chunk, once what it held is used up
+    auto slot = [&]() -> uint8_t* {
+      if (chunk >= kSlots) {
+        const uint32_t old = chunk - kSlots, t = old / C::kPerTile;
+        uint64_t* bar = old % C::kPerTile <= C::kC ? &m.k_empty[t & 1] : &m.v_empty[t & 1];
+        if (!cx.wait(bar, (t >> 1) & 1)) return nullptr;
+      }
+      return cx.smem + C::kOffRing + (chunk++ % kSlots) * kSlotBytes;
+    };
+    if (!load_q(0)) return;
+    const int tiles = max(x.na, x.nb);
+    for (int t = 0; t < tiles; ++t, ++it) {
+      const int row = x.kv0 + t * kTile, s = it & 1;
+      uint64_t* v_bar = x.kv < (t + 1) * kTile ? &m.v_short[s] : &m.v_full[s];
+      for (int c = 0; c <= C::kC; ++c) {
+        uint8_t* to = slot();
+        if (!to) return;
+        if (elect_one()) {
+          if (c == 0) mbar_arrive_expect_tx(&m.k_full[s], C::kQTile);
+          if (c < C::kC)
+            tma_load_3d(to, &maps.k, &m.k_full[s], 64 * c, x.head, row);
+          else
+            tma_load_3d(to, &maps.rot, &m.k_full[s], 0, row, 0);
+        }
+        __syncwarp();
+      }
+      if (t == 0 && x.nb > 0 && !load_q(1)) return;
+      for (int half = 0; half < 2; ++half) {
+        uint8_t* to = slot();
+        if (!to) return;
+        if (elect_one()) {
+          if (half == 0) mbar_arrive_expect_tx(v_bar, kTile * D * 2);
+          for (int c = 0; c < C::kC; ++c)
+            tma_load_3d(to + c * 8192, &maps.v, v_bar, 64 * c, x.head, row + 64 * half);
+        }
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// Zeroes the value rows of a sequence's last tile that are not its own: what does
+// not count must not reach the products as NaN.
+template <int D>
+__device__ void run_cleaner(const Ctx& cx, int lane) {
+  using C = Cfg<D>;
+  Misc& m = *cx.m;
+  uint32_t it = 0, count[2] = {0, 0};
+  Item x;
+  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
+    const int tiles = max(x.na, x.nb);
+    it += tiles;
+    const int valid = x.kv - (tiles - 1) * kTile;
+    if (valid >= kTile) continue;
+    const uint32_t t = it - 1;
+    if (!cx.wait(&m.v_short[t & 1], count[t & 1]++ & 1)) return;
+    for (int i = lane; i < (kTile - valid) * C::kC * 8; i += 32) {
+      const int row = valid + i / (C::kC * 8), c = i / 8 % C::kC;
+      const uint32_t chunk = t * C::kPerTile + C::kC + 1 + row / 64;
+      *reinterpret_cast<uint4*>(cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes + c * 8192 +
+                                row % 64 * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.v_clean[t & 1]);
+  }
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kRowThreads) expanded_rows_kernel(const ExpandedParams p) {
+__device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int lane) {
+  using C = Cfg<D>;
+  Misc& m = *cx.m;
+  constexpr uint32_t idesc_qk = umma_idesc_f16(BF16, kTile, kTile, false);
+  constexpr uint32_t idesc_pv = umma_idesc_f16(BF16, kTile, D, true);
+  const uint64_t dq = sw128_desc(smem_u32(cx.smem + C::kOffQ), 0);
+  const uint64_t dring = sw128_desc(smem_u32(cx.smem + C::kOffRing), 0);
+  const uint64_t dv = sw128_desc(smem_u32(cx.smem + C::kOffRing), 8192);
+  const int rot_steps = p.rope_dim / 16;
+  uint32_t it = 0, units[2] = {0, 0}, pv[2] = {0, 0};
+  uint32_t cleaned[2] = {0, 0}, full[2] = {0, 0};   // of v_clean, v_full
+  bool ok = true, issued = false;
+  if (p.debug_stall) ok = cx.wait(&m.stall, 0);
+  Item x;
+  for (uint32_t n = 0; ok && next_item(cx, n, lane, x); ++n) {
+    const int tiles = max(x.na, x.nb);
+    const int count[2] = {x.na, x.nb};
+    uint32_t k_seen = ~0u, v_seen = ~0u;       // the tile last waited for
+    auto qk = [&](int w, int t) -> bool {
+      const uint32_t g = it + t;
+      if (t == 0 && !cx.wait(&m.q_full[w], units[w] & 1)) return false;
+      if (k_seen != g) {
+        if (!cx.wait(&m.k_full[g & 1], (g >> 1) & 1)) return false;
+        k_seen = g;
+      }
+      tc_fence_after();
+      issued = true;
+      const uint32_t d = tmem + C::kTmemS + 128 * w;
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c <= C::kC; ++c) {
+          const uint64_t a = dq + ((w * C::kQTile + c * kSlotBytes) >> 4);
+          const uint64_t k = dring + (((g * C::kPerTile + c) % kSlots * kSlotBytes) >> 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c < C::kC || i < rot_steps) umma_f16(d, a + 2 * i, k + 2 * i, idesc_qk, c + i > 0 ? 1u : 0u);
+        }
+        umma_commit(&m.s_full[w]);
+        if (t == count[w] - 1) umma_commit(&m.q_empty[w]);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto do_pv = [&](int w, int t) -> bool {
+      const uint32_t g = it + t;
+      if (!cx.wait(&m.p_full[w], pv[w] & 1)) return false;
+      ++pv[w];
+      if (v_seen != g) {
+        // the sequence's last, short tile is cleaned first
+        const bool is_short = x.kv < (t + 1) * kTile;
+        uint32_t& uses = is_short ? cleaned[g & 1] : full[g & 1];
+        if (!cx.wait(is_short ? &m.v_clean[g & 1] : &m.v_full[g & 1], uses & 1)) return false;
+        ++uses;
+        v_seen = g;
+      }
+      if (t == 0) {
+        if (!cx.wait(&m.o_free[w], (units[w] & 1) ^ 1)) return false;
+        ++units[w];
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + C::kTmemO + 128 * w, a = tmem + C::kTmemS + 128 * w;
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) {
+          const uint64_t v = dv + (((g * C::kPerTile + C::kC + 1 + (i >> 2)) % kSlots * kSlotBytes +
+                                    (i & 3) * 2048) >> 4);
+          umma_f16_tmem_a(d, a + 8 * i, v, idesc_pv, i > 0 ? 1u : (uint32_t)(t > 0));
+        }
+        if (t == count[w] - 1) umma_commit(&m.o_full[w]);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int t = 0; ok && t <= tiles; ++t) {
+      if (t > 0 && t - 1 < x.na) ok = do_pv(0, t - 1);
+      if (ok && t < x.na) ok = qk(0, t);
+      if (ok && t > 0 && t - 1 < x.nb) ok = do_pv(1, t - 1);
+      if (ok && t > 0) {
+        if (elect_one()) umma_commit(&m.v_empty[(it + t - 1) & 1]);
+        __syncwarp();
+      }
+      if (ok && t < x.nb) ok = qk(1, t);
+      if (ok && t < tiles) {
+        if (elect_one()) umma_commit(&m.k_empty[(it + t) & 1]);
+        __syncwarp();
+      }
+    }
+    it += tiles;
+  }
+  if (*(volatile int*)&m.abort && issued) {
+    if (elect_one()) umma_commit(&m.drain);
+    __syncwarp();
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&m.drain, 0) && globaltimer_ns() - t0 < 10000000ull) {}
+  }
+}
+
+// Where a moved reference puts the largest weight, and how far one may exceed it:
+// fp16 weights are held 2^7 higher than bf16 ones, as what lies 2^-24 below a weight
+// of one is the type's end.
+template <bool BF16>
+struct Ref {
+  static constexpr float kTop = BF16 ? 8.f : 15.f, kPut = BF16 ? 0.f : 7.f;
+};
+
+template <int D>
+__device__ __noinline__ void rescale(uint32_t o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float v[32];
+    tmem_ld32(o + c, v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+    tmem_st32(o + c, v);
+  }
+  tmem_wait_st();
+}
+
+template <int D, bool BF16>
+__device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int warp, int lane) {
+  using C = Cfg<D>;
+  Misc& m = *cx.m;
+  const int w = warp >> 2;                       // tile A or B
+  const int rr = (warp & 3) * 32 + lane;         // the tile's row
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_at = tmem + lanes + C::kTmemS + 128 * w, o_at = tmem + lanes + C::kTmemO + 128 * w;
+  uint32_t done = 0, units = 0;
+  Item x;
+  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
+    const int tiles = w ? x.nb : x.na;
+    if (tiles == 0) continue;
+    const int row = w * kTile + rr;              // of the unit's
+    const int see = x.first + row;               // the last kv row it sees
+    const int low = x.first + w * kTile + (warp & 3) * 32;   // the warp's first row's
+    float ref = -FLT_MAX, l = 0.f;
+    for (int t = 0; t < tiles; ++t, ++done) {
+      if (!cx.wait(&m.s_full[w], done & 1)) return;
+      tc_fence_after();
+      // The scores are read twice, 32 at a time, for their maximum and for the
+      // weights (128 registers for all of them do not go with the rest); a chunk is
+      // on its way while the one before is worked on.
+      float s[2][32];
+      const int lim = see - t * kTile;
+      const bool masked = t * kTile + kTile - 1 > low;
+      float top[2] = {-INFINITY, -INFINITY};
+      tmem_ld32(s_at, s[0]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_wait_ld(s[c & 1]);
+        tmem_ld32(s_at + 32 * ((c + 1) & 3), s[(c + 1) & 1]);
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            top[j & 1] = fmaxf(top[j & 1], 32 * c + j <= lim ? s[c & 1][j] * p.scale_log2 : -INFINITY);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], s[c & 1][j] * p.scale_log2);
+        }
+      }
+      const float most = fmaxf(top[0], top[1]);
+      const bool move = most - ref > Ref<BF16>::kTop;
+      if (__any_sync(0xffffffffu, move)) {
+        float f = 1.f;
+        if (move) {
+          const float to = most - Ref<BF16>::kPut;
+          f = ex2_approx(ref - to);
+          ref = to;
+          l *= f;
+        }
+        // the product before has been waited for with these scores: O is at rest
+        if (t > 0) {
+          tmem_wait_ld(s[0]);                  // no load may be under way into registers a call saves
+          rescale<D>(o_at, f);
+        }
+      }
+      float2 sum = make_float2(0.f, 0.f);
+      const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        tmem_wait_ld(s[c & 1]);
+        if (c < 3) tmem_ld32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+        uint32_t w16[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float2 e = ffma2(make_float2(s[c & 1][2 * j], s[c & 1][2 * j + 1]), scale, shift);
+          if (masked) {
+            e.x = 32 * c + 2 * j <= lim ? e.x : -INFINITY;
+            e.y = 32 * c + 2 * j + 1 <= lim ? e.y : -INFINITY;
+          }
+          e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+          sum = fadd2(sum, e);
+          w16[j] = pack2<BF16>(e.x, e.y);
+        }
+        // over scores that have been read: columns 16 c on are of chunk c / 2
+        tmem_st16(s_at + 16 * c, w16);
+      }
+      l += sum.x + sum.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.p_full[w]);
+    }
+    if (!cx.wait(&m.o_full[w], units & 1)) return;
+    ++units;
+    tc_fence_after();
+    const bool valid = row < x.nq;
+    const int64_t at = (int64_t)(x.q0 + row) * p.h + x.head;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint4* out = reinterpret_cast<uint4*>(p.out + at * D);
+    float odd = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float v[32];
+      tmem_ld32(o_at + c, v);
+      tmem_wait_ld(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          odd += v[8 * i + 2 * k] * 0.f + v[8 * i + 2 * k + 1] * 0.f;
+          y[k] = pack2<BF16>(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+        }
+        if (valid) out[c / 8 + i] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.o_free[w]);
+    if (valid) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
+    // a value that is not finite, though the weights are: it may be one not seen
+    unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
+    while (again) {
+      const int i = __ffs(again) - 1;
+      again &= again - 1;
+      __syncwarp();
+      row_exact<D, BF16>(p, x.b, x.q0 + w * kTile + (warp & 3) * 32 + i, x.head);
+    }
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    expanded_kernel(const __grid_constant__ ExpandedMaps maps, const ExpandedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc& m = *reinterpret_cast<Misc*>(smem + C::kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.q_full[i], 1);
+      mbar_init(&m.q_empty[i], 1);
+      mbar_init(&m.k_full[i], 1);
+      mbar_init(&m.k_empty[i], 1);
+      mbar_init(&m.v_full[i], 1);
+      mbar_init(&m.v_empty[i], 1);
+      mbar_init(&m.v_short[i], 1);
+      mbar_init(&m.v_clean[i], 1);
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.p_full[i], 4);
+      mbar_init(&m.o_full[i], 1);
+      mbar_init(&m.o_free[i], 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&m.item_full[i], 1);
+      mbar_init(&m.item_empty[i], 11);   // 8 softmax warps, producer, products, cleaner
+    }
+    mbar_init(&m.stall, 1);
+    mbar_init(&m.drain, 1);
+    m.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.q);
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.rot);
+      tma_prefetch_desc(&maps.v);
+    }
+    tmem_alloc(&m.tmem, 512);
+  }
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
-  for (int b = tid; b < p.batch; b += kRowThreads) bad |= !good_sequence(p, b);
-  if (__syncthreads_or(bad)) {
+  for (int b = tid; b < p.batch; b += kThreads) bad |= !good_sequence(p, b);
+  tc_fence_before();
+  const bool stop = __syncthreads_or(bad);
+  tc_fence_after();
+  const Ctx cx{smem, &m, p.error, p.timeout_ns};
+  if (stop) {
     if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
-    return;
+  } else if (warp < 8) {
+    run_softmax<D, BF16>(cx, p, m.tmem, warp, lane);
+  } else {
+    if (warp == 8)
+      run_producer<D>(cx, maps, lane);
+    else if (warp == 9)
+      run_mma<D, BF16>(cx, p, m.tmem, lane);
+    else if (warp == 10)
+      run_cleaner<D>(cx, lane);
+    else
+      run_scheduler(cx, p, lane);
   }
-  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (tid >> 5);
-  if (i >= (int64_t)p.total_q * p.h) return;
-  const int row = (int)(i / p.h);
-  attend_row<D, BF16>(p, find_sequence(p.q_indptr, p.batch, row, lane), row, (int)(i % p.h), lane);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // after a wait ran out copies may still be on their way into shared memory
+  if (m.abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(m.tmem, 512);
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const ExpandedParams& p, const ExpandedMaps& maps, int grid, cudaStream_t stream) {
+  constexpr int smem = Cfg<D>::kOffMisc + (int)sizeof(Misc);
+  static_assert(smem <= 232448, "shared memory of an SM");
+  const auto kern = expanded_kernel<D, BF16>;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared((const void*)kern, smem, allowed);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, maps, p);
 }
 
 }  // namespace
 
-cudaError_t launch_expanded(const ExpandedParams& p, int head_dim, bool bf16, int nsm,
-                            cudaStream_t stream) {
-  (void)nsm;
-  const int64_t grid = ceil_div((int64_t)p.total_q * p.h, kRowThreads / 32);
-  const auto kern = head_dim == 128
-                        ? (bf16 ? expanded_rows_kernel<128, true> : expanded_rows_kernel<128, false>)
-                        : (bf16 ? expanded_rows_kernel<64, true> : expanded_rows_kernel<64, false>);
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(kRowThreads), 0, stream, p);
+cudaError_t launch_expanded(const ExpandedParams& p, const ExpandedMaps& maps, int head_dim, bool bf16,
+                            int nsm, cudaStream_t stream) {
+  const int64_t most = (ceil_div(p.total_q, 2 * kTile) + p.batch) * p.h;   // units there can be
+  const int grid = (int)(most < nsm ? most : nsm);
+  if (head_dim == 128)
+    return bf16 ? launch<128, true>(p, maps, grid, stream) : launch<128, false>(p, maps, grid, stream);
+  return bf16 ? launch<64, true>(p, maps, grid, stream) : launch<64, false>(p, maps, grid, stream);
 }
 
 }  // namespace ta

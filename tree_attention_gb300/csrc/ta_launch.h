@@ -279,6 +279,15 @@ struct ExpandedParams {
   unsigned int* error;
   int batch, total_q, total_kv, h, rope_dim;
   float scale_log2;
+  unsigned long long timeout_ns;
+  int debug_stall;                        // as in AttnParams
+};
+
+// Tensor maps of the expanded form, all with 128-byte swizzle: q [total_q, h, d +
+// rope_dim] (box {64, 1 head, 128 rows}), k (the same) and v ({64, 1, 64}) [total_kv,
+// h, d], k_rope [total_kv, rope_dim] ({64, 128}).  Elements outside read as zeros.
+struct ExpandedMaps {
+  CUtensorMap q, k, v, rot;
 };
 
 // Plan kernel: sequence/tile enumeration, tile classification and LPT
@@ -327,8 +336,8 @@ cudaError_t launch_absorbed(const LatentParams& p, const AbsorbedMaps& maps, boo
                             cudaStream_t stream);
 
 // Causal attention with keys and values per head and a shared rotary key.
-cudaError_t launch_expanded(const ExpandedParams& p, int head_dim, bool bf16, int nsm,
-                            cudaStream_t stream);
+cudaError_t launch_expanded(const ExpandedParams& p, const ExpandedMaps& maps, int head_dim, bool bf16,
+                            int nsm, cudaStream_t stream);
 
 // pages[dst[i]] = pages[src[i]].
 cudaError_t launch_copy_pages(const CopyParams& p, int nsm, cudaStream_t stream);
