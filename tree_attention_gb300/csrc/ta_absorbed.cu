@@ -175,7 +175,8 @@ struct Misc {
   float exchange[2][4][64];
   Piece piece[kPieces];
   long long scan[12];
-  long long first_unit;
+  long long first_unit;              // of the range's first sequence
+  LatentSeq first;
   int first_seq;
   uint32_t tmem;
   int abort;
@@ -250,8 +251,8 @@ __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& s
   long long base = m.first_unit;
   LatentMerge merge{};
   uint32_t n = 0;
-  LatentSeq s{};
-  bool loaded = false;
+  LatentSeq s = m.first;
+  bool loaded = true;
   while (true) {
     Piece x{};
     if (u < u_end) {
@@ -376,11 +377,14 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
       const int page = next;
       next = after;
       // K has room for one tile, so the memory's latency would be in every tile's way:
-      // this CTA's half of the tile after the next goes into L2 ahead of it
+      // this CTA's half of the latents and of the rotary keys of the tile after the next
+      // go into L2 ahead of it
       if (t + kAhead < x.t1) {
         after = page_of(p, x, t + kAhead, lane);
-        if (lane < C::kPages && after < p.tab.num_pages)
+        if (lane < C::kPages && after < p.tab.num_pages) {
           tma_prefetch_l2_4d(&maps.v, 0, 0, (int)cta * C::kHalf, after);
+          tma_prefetch_l2_3d(&maps.rot, RANK, 8 * (int)cta, after);
+        }
         __syncwarp();
       }
 #pragma unroll
@@ -774,16 +778,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
   // this thread's sequences: checked, and their tiles counted
   const int each = (p.tab.batch + kThreads - 1) / kThreads;
   const int b_lo = min(p.tab.batch, tid * each), b_hi = min(p.tab.batch, b_lo + each);
   long long mine = 0;
-  bool bad = false;
+  bool bad = false, empty = false;
+  LatentSeq s{};
   for (int b = b_lo; b < b_hi; ++b) {
-    const LatentSeq s = latent_seq(p, b);
+    s = latent_seq(p, b);
     bad |= !s.good;
+    empty |= s.kv == 0;
     if (s.good) mine += (long long)tiles_of(s) * items_of(s, p.h);
   }
   long long sum = mine;
@@ -807,31 +817,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const long long u = split.start(pair);
     if (u >= before && u < before + mine) {
       int b = b_lo;
-      for (; b < b_hi; ++b) {
-        const LatentSeq s = latent_seq(p, b);
+      for (; each > 1 && b < b_hi; ++b) {
+        s = latent_seq(p, b);
         const long long k = (long long)tiles_of(s) * items_of(s, p.h);
         if (u < before + k) break;
         before += k;
       }
       m.first_seq = b;
+      m.first = s;
       m.first_unit = before;
-    }
-    if (!p.q_indptr) {   // sequences without rows
-      for (int b = blockIdx.x; b < p.tab.batch; b += gridDim.x) {
-        if (p.tab.page_indptr[b] != p.tab.page_indptr[b + 1]) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.h * RANK);
-        for (int i = tid; i < p.h * (RANK / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-        if (tid < p.h) p.lse[(int64_t)b * p.h + tid] = -INFINITY;
-      }
     }
   } else if (tid == 0) {
     atomicOr(p.error, DEVERR_BAD_INDPTR);
     if (cta == 0) p.merge[pair] = LatentMerge{};
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // both CTAs' barriers exist
-  tc_fence_after();
+  // one-token attention of sequences without rows
+  if (__syncthreads_or(empty) && !stop && !p.q_indptr) {
+    for (int b = blockIdx.x; b < p.tab.batch; b += gridDim.x) {
+      if (p.tab.page_indptr[b] != p.tab.page_indptr[b + 1]) continue;
+      uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.h * RANK);
+      for (int i = tid; i < p.h * (RANK / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+      if (tid < p.h) p.lse[(int64_t)b * p.h + tid] = -INFINITY;
+    }
+  }
   const Ctx cx{smem, &m, p.error, p.timeout_ns};
   if (!stop) {
     if (warp < 8)
