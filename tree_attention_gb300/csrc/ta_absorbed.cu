@@ -674,13 +674,15 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       if (x.slot < 0) {
         const int64_t at = (int64_t)x.row0 + row;
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
-        uint4* out = reinterpret_cast<uint4*>(p.out + at * RANK + col0);
+        const int four = lane & ~3;              // the rows whose vectors this lane stores
+        uint16_t* out = p.out + (at - lane + four) * RANK + col0 + (lane & 3) * 8;
         float odd = 0.f;
 #pragma unroll 1
         for (int c = 0; c < C::kCols; c += 32) {
           float v[32];
           tmem_ld32(o_at + c, v);
           tmem_wait_ld(v);
+          uint4 y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
@@ -689,8 +691,12 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
               odd += v[8 * i + 2 * k] * 0.f + v[8 * i + 2 * k + 1] * 0.f;
               w[k] = pack2<BF16>(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
             }
-            if (valid) out[c / 8 + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            y[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          transpose4(y, lane);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row - lane + four + j < x.nrows) *reinterpret_cast<uint4*>(out + j * RANK + c) = y[j];
         }
         if (valid && part == 0) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
         // a value that is not finite, though the weights are: it may be one that does not count

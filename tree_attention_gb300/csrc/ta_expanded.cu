@@ -532,13 +532,16 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     const bool valid = row < x.nq;
     const int64_t at = (int64_t)(x.q0 + row) * p.h + x.head;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint4* out = reinterpret_cast<uint4*>(p.out + at * D);
+    const int four = lane & ~3;                  // the rows whose vectors this lane stores
+    const int64_t step = (int64_t)p.h * D;       // from row to row
+    uint16_t* out = p.out + (at + (four - lane) * (int64_t)p.h) * D + (lane & 3) * 8;
     float odd = 0.f;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float v[32];
       tmem_ld32(o_at + c, v);
       tmem_wait_ld(v);
+      uint4 z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t y[4];
@@ -547,8 +550,12 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
           odd += v[8 * i + 2 * k] * 0.f + v[8 * i + 2 * k + 1] * 0.f;
           y[k] = pack2<BF16>(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
         }
-        if (valid) out[c / 8 + i] = make_uint4(y[0], y[1], y[2], y[3]);
+        z[i] = make_uint4(y[0], y[1], y[2], y[3]);
       }
+      transpose4(z, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (row - lane + four + j < x.nq) *reinterpret_cast<uint4*>(out + j * step + c) = z[j];
     }
     tc_fence_before();
     __syncwarp();
