@@ -8,8 +8,10 @@
 // cores for prompts of some hundred rows, by the memory below.
 //
 // * A unit of work is 256 q rows of one sequence and head, two tiles of 128 (A and
-//   B) that read the same kv tiles of 128 rows.  A CTA per SM takes every
-//   gridDim.x-th unit, the last rows of a sequence (the most kv tiles) first.
+//   B) that read the same kv tiles of 128 rows; where a sequence's last rows are 128
+//   at most, they are A of one head and B of the next, which read kv tiles of their
+//   own in turn.  A CTA per SM takes every gridDim.x-th unit, the last rows of a
+//   sequence (the most kv tiles) first.
 // * The products alternate: PV_A(t-1) QK_A(t) PV_B(t-1) QK_B(t), so that one
 //   tile's softmax runs beside the other tile's products.  P lies over its own S in
 //   tensor memory, and products of one thread execute in order.
@@ -22,6 +24,7 @@
 #include <atomic>
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "ta_device.cuh"
 #include "ta_launch.h"
@@ -40,6 +43,11 @@ struct Item {
   int first;               // the kv row of the sequence that q0 is
   int kv0, kv;             // the sequence's rows
   int na, nb;              // kv tiles of tiles A and B; na 0: no more items
+  int heads;               // 1: B is the next 128 rows, 2: B is the same rows of head + 1
+  // kv tiles loaded, and the place of the s-th of them in its sequence
+  __device__ __forceinline__ int loads() const { return heads == 2 ? 2 * na : max(na, nb); }
+  __device__ __forceinline__ int tile(int s) const { return heads == 2 ? s >> 1 : s; }
+  __device__ __forceinline__ bool is_short(int s) const { return kv < (tile(s) + 1) * kTile; }
 };
 
 struct Misc {
@@ -159,6 +167,12 @@ __device__ __noinline__ void row_exact(const ExpandedParams& p, int b, int row, 
 // roles
 // ---------------------------------------------------------------------------
 
+// Units of the last 256 q rows of a sequence with qo > 0 of them.
+__device__ __forceinline__ int last_units(int qo, int h) {
+  const int rows = (qo - 1) % (2 * kTile) + 1;
+  return rows <= kTile ? (h + 1) / 2 : h;
+}
+
 // Every gridDim.x-th unit, counted sequence by sequence, in one from the last 256
 // rows on, head by head; 32 sequences at a time.
 __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) {
@@ -177,7 +191,8 @@ __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) 
         qo = p.q_indptr[b + 1] - q0;
         k0 = p.kv_indptr[b];
         kv = p.kv_indptr[b + 1] - k0;
-        units = (long long)((qo + 2 * kTile - 1) / (2 * kTile)) * p.h;
+        const int pairs = (qo + 2 * kTile - 1) / (2 * kTile);
+        if (pairs) units = (long long)(pairs - 1) * p.h + last_units(qo, p.h);
       }
       long long up = units;
 #pragma unroll
@@ -193,10 +208,11 @@ __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) 
       const long long in = u - base - before;
       const int src = __ffs(__ballot_sync(0xffffffffu, in >= 0 && in < units)) - 1;
       if (lane == src) {
-        const int pairs = (qo + 2 * kTile - 1) / (2 * kTile);
-        const int r0 = (pairs - 1 - (int)(in / p.h)) * 2 * kTile;
+        const int pairs = (qo + 2 * kTile - 1) / (2 * kTile), last = last_units(qo, p.h);
+        const int r0 = (in < last ? pairs - 1 : pairs - 2 - (int)((in - last) / p.h)) * 2 * kTile;
+        x.heads = in < last && last < p.h ? 2 : 1;
         x.b = b0 + lane;
-        x.head = (int)(in % p.h);
+        x.head = in < last ? (int)in * x.heads : (int)((in - last) % p.h);
         x.q0 = q0 + r0;
         x.nq = min(2 * kTile, qo - r0);
         x.first = kv - qo + r0;
@@ -204,6 +220,12 @@ __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) 
         x.kv = kv;
         x.na = (x.first + min(kTile, x.nq) + kTile - 1) / kTile;
         x.nb = x.nq > kTile ? (x.first + x.nq + kTile - 1) / kTile : 0;
+        if (x.heads == 2) {
+          if (x.head + 1 < p.h)
+            x.nb = x.na;
+          else
+            x.heads = 1;
+        }
       }
       const int slot = n % kItems;
       if (!cx.wait(&m.item_empty[slot], ((n / kItems) & 1) ^ 1)) return;
@@ -249,7 +271,7 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
         mbar_arrive_expect_tx(&m.q_full[tile], C::kQTile);
         for (int c = 0; c <= C::kC; ++c)
           tma_load_3d(cx.smem + C::kOffQ + tile * C::kQTile + c * kSlotBytes, &maps.q, &m.q_full[tile],
-                      64 * c, x.head, x.q0 + tile * kTile);
+                      64 * c, x.head + tile * (x.heads - 1), x.q0 + tile * (2 - x.heads) * kTile);
       }
       __syncwarp();
       return true;
@@ -264,17 +286,17 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
       return cx.smem + C::kOffRing + (chunk++ % kSlots) * kSlotBytes;
     };
     if (!load_q(0)) return;
-    const int tiles = max(x.na, x.nb);
-    for (int t = 0; t < tiles; ++t, ++it) {
-      const int row = x.kv0 + t * kTile, s = it & 1;
-      uint64_t* v_bar = x.kv < (t + 1) * kTile ? &m.v_short[s] : &m.v_full[s];
+    const int loads = x.loads();
+    for (int t = 0; t < loads; ++t, ++it) {
+      const int row = x.kv0 + x.tile(t) * kTile, s = it & 1, head = x.head + (t & (x.heads - 1));
+      uint64_t* v_bar = x.is_short(t) ? &m.v_short[s] : &m.v_full[s];
       for (int c = 0; c <= C::kC; ++c) {
         uint8_t* to = slot();
         if (!to) return;
         if (elect_one()) {
           if (c == 0) mbar_arrive_expect_tx(&m.k_full[s], C::kQTile);
           if (c < C::kC)
-            tma_load_3d(to, &maps.k, &m.k_full[s], 64 * c, x.head, row);
+            tma_load_3d(to, &maps.k, &m.k_full[s], 64 * c, head, row);
           else
             tma_load_3d(to, &maps.rot, &m.k_full[s], 0, row, 0);
         }
@@ -287,7 +309,7 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
         if (elect_one()) {
           if (half == 0) mbar_arrive_expect_tx(v_bar, kTile * D * 2);
           for (int c = 0; c < C::kC; ++c)
-            tma_load_3d(to + c * 8192, &maps.v, v_bar, 64 * c, x.head, row + 64 * half);
+            tma_load_3d(to + c * 8192, &maps.v, v_bar, 64 * c, head, row + 64 * half);
         }
         __syncwarp();
       }
@@ -304,21 +326,21 @@ __device__ void run_cleaner(const Ctx& cx, int lane) {
   uint32_t it = 0, count[2] = {0, 0};
   Item x;
   for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
-    const int tiles = max(x.na, x.nb);
-    it += tiles;
-    const int valid = x.kv - (tiles - 1) * kTile;
+    const int loads = x.loads(), valid = x.kv - x.tile(loads - 1) * kTile;
+    it += loads;
     if (valid >= kTile) continue;
-    const uint32_t t = it - 1;
-    if (!cx.wait(&m.v_short[t & 1], count[t & 1]++ & 1)) return;
-    for (int i = lane; i < (kTile - valid) * C::kC * 8; i += 32) {
-      const int row = valid + i / (C::kC * 8), c = i / 8 % C::kC;
-      const uint32_t chunk = t * C::kPerTile + C::kC + 1 + row / 64;
-      *reinterpret_cast<uint4*>(cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes + c * 8192 +
-                                row % 64 * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    for (uint32_t t = it - x.heads; t < it; ++t) {
+      if (!cx.wait(&m.v_short[t & 1], count[t & 1]++ & 1)) return;
+      for (int i = lane; i < (kTile - valid) * C::kC * 8; i += 32) {
+        const int row = valid + i / (C::kC * 8), c = i / 8 % C::kC;
+        const uint32_t chunk = t * C::kPerTile + C::kC + 1 + row / 64;
+        *reinterpret_cast<uint4*>(cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes + c * 8192 +
+                                  row % 64 * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.v_clean[t & 1]);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&m.v_clean[t & 1]);
   }
 }
 
@@ -334,83 +356,104 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
   const int rot_steps = p.rope_dim / 16;
   uint32_t it = 0, units[2] = {0, 0}, pv[2] = {0, 0};
   uint32_t cleaned[2] = {0, 0}, full[2] = {0, 0};   // of v_clean, v_full
+  uint32_t k_seen = ~0u, v_seen = ~0u;              // the load last waited for
   bool ok = true, issued = false;
   if (p.debug_stall) ok = cx.wait(&m.stall, 0);
   Item x;
-  for (uint32_t n = 0; ok && next_item(cx, n, lane, x); ++n) {
-    const int tiles = max(x.na, x.nb);
-    const int count[2] = {x.na, x.nb};
-    uint32_t k_seen = ~0u, v_seen = ~0u;       // the tile last waited for
-    auto qk = [&](int w, int t) -> bool {
-      const uint32_t g = it + t;
-      if (t == 0 && !cx.wait(&m.q_full[w], units[w] & 1)) return false;
-      if (k_seen != g) {
-        if (!cx.wait(&m.k_full[g & 1], (g >> 1) & 1)) return false;
-        k_seen = g;
-      }
-      tc_fence_after();
-      issued = true;
-      const uint32_t d = tmem + C::kTmemS + 128 * w;
-      if (elect_one()) {
-#pragma unroll
-        for (int c = 0; c <= C::kC; ++c) {
-          const uint64_t a = dq + ((w * C::kQTile + c * kSlotBytes) >> 4);
-          const uint64_t k = dring + (((g * C::kPerTile + c) % kSlots * kSlotBytes) >> 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c < C::kC || i < rot_steps) umma_f16(d, a + 2 * i, k + 2 * i, idesc_qk, c + i > 0 ? 1u : 0u);
-        }
-        umma_commit(&m.s_full[w]);
-        if (t == count[w] - 1) umma_commit(&m.q_empty[w]);
-      }
-      __syncwarp();
-      return true;
-    };
-    auto do_pv = [&](int w, int t) -> bool {
-      const uint32_t g = it + t;
-      if (!cx.wait(&m.p_full[w], pv[w] & 1)) return false;
-      ++pv[w];
-      if (v_seen != g) {
-        // the sequence's last, short tile is cleaned first
-        const bool is_short = x.kv < (t + 1) * kTile;
-        uint32_t& uses = is_short ? cleaned[g & 1] : full[g & 1];
-        if (!cx.wait(is_short ? &m.v_clean[g & 1] : &m.v_full[g & 1], uses & 1)) return false;
-        ++uses;
-        v_seen = g;
-      }
-      if (t == 0) {
-        if (!cx.wait(&m.o_free[w], (units[w] & 1) ^ 1)) return false;
-        ++units[w];
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + C::kTmemO + 128 * w, a = tmem + C::kTmemS + 128 * w;
-      if (elect_one()) {
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i) {
-          const uint64_t v = dv + (((g * C::kPerTile + C::kC + 1 + (i >> 2)) % kSlots * kSlotBytes +
-                                    (i & 3) * 2048) >> 4);
-          umma_f16_tmem_a(d, a + 8 * i, v, idesc_pv, i > 0 ? 1u : (uint32_t)(t > 0));
-        }
-        if (t == count[w] - 1) umma_commit(&m.o_full[w]);
-      }
-      __syncwarp();
-      return true;
-    };
-    for (int t = 0; ok && t <= tiles; ++t) {
-      if (t > 0 && t - 1 < x.na) ok = do_pv(0, t - 1);
-      if (ok && t < x.na) ok = qk(0, t);
-      if (ok && t > 0 && t - 1 < x.nb) ok = do_pv(1, t - 1);
-      if (ok && t > 0) {
-        if (elect_one()) umma_commit(&m.v_empty[(it + t - 1) & 1]);
-        __syncwarp();
-      }
-      if (ok && t < x.nb) ok = qk(1, t);
-      if (ok && t < tiles) {
-        if (elect_one()) umma_commit(&m.k_empty[(it + t) & 1]);
-        __syncwarp();
-      }
+  using A = std::integral_constant<int, 0>;
+  using B = std::integral_constant<int, 1>;
+  // S of tile w and load s, of its kv tiles the first or the last; both in line, with
+  // w known, as descriptors that are not the warp's constants cost 40 cycles a product
+  auto qk = [&](auto wc, int s, bool first, bool last) __attribute__((always_inline)) -> bool {
+    constexpr int w = decltype(wc)::value;
+    const uint32_t g = it + s;
+    if (first && !cx.wait(&m.q_full[w], units[w] & 1)) return false;
+    if (k_seen != g) {
+      if (!cx.wait(&m.k_full[g & 1], (g >> 1) & 1)) return false;
+      k_seen = g;
     }
-    it += tiles;
+    tc_fence_after();
+    issued = true;
+    uint64_t k[C::kC + 1];
+#pragma unroll
+    for (int c = 0; c <= C::kC; ++c) k[c] = dring + (((g * C::kPerTile + c) % kSlots * kSlotBytes) >> 4);
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < C::kC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          umma_f16(tmem + C::kTmemS + 128 * w, dq + ((w * C::kQTile + c * kSlotBytes + 32 * i) >> 4),
+                   k[c] + 2 * i, idesc_qk, c + i > 0 ? 1u : 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < rot_steps)
+          umma_f16(tmem + C::kTmemS + 128 * w, dq + ((w * C::kQTile + C::kC * kSlotBytes + 32 * i) >> 4),
+                   k[C::kC] + 2 * i, idesc_qk, 1u);
+      umma_commit(&m.s_full[w]);
+      if (last) umma_commit(&m.q_empty[w]);
+    }
+    __syncwarp();
+    return true;
+  };
+  auto do_pv = [&](auto wc, int s, bool first, bool last) __attribute__((always_inline)) -> bool {
+    constexpr int w = decltype(wc)::value;
+    const uint32_t g = it + s;
+    if (!cx.wait(&m.p_full[w], pv[w] & 1)) return false;
+    ++pv[w];
+    if (v_seen != g) {
+      // the sequence's last, short tile is cleaned first
+      const bool is_short = x.is_short(s);
+      const uint32_t uses = is_short ? cleaned[g & 1]++ : full[g & 1]++;
+      if (!cx.wait(is_short ? &m.v_clean[g & 1] : &m.v_full[g & 1], uses & 1)) return false;
+      v_seen = g;
+    }
+    if (first) {
+      if (!cx.wait(&m.o_free[w], (units[w] & 1) ^ 1)) return false;
+      ++units[w];
+    }
+    tc_fence_after();
+    uint64_t v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[i] = dv + (((g * C::kPerTile + C::kC + 1 + i) % kSlots * kSlotBytes) >> 4);
+    if (elect_one()) {
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        umma_f16_tmem_a(tmem + C::kTmemO + 128 * w, tmem + C::kTmemS + 128 * w + 8 * i,
+                        v[i >> 2] + ((i & 3) * 2048 >> 4), idesc_pv, i > 0 ? 1u : (uint32_t)!first);
+      if (last) umma_commit(&m.o_full[w]);
+    }
+    __syncwarp();
+    return true;
+  };
+  auto release = [&](uint64_t* bars, int s) {
+    if (elect_one()) umma_commit(&bars[(it + s) & 1]);
+    __syncwarp();
+  };
+  for (uint32_t n = 0; ok && next_item(cx, n, lane, x); ++n) {
+    const int loads = x.loads(), step = x.heads, na = x.na, nb = x.nb;
+    // kv tile t is load t of both tiles, or load 2 t of A and 2 t + 1 of B
+    for (int t = 0; ok; ++t) {
+      const int sa = t * step, sb = sa + step - 1;
+      if (t > 0 && t - 1 < na) {
+        if (!(ok = do_pv(A{}, sa - step, t == 1, t == na))) break;
+        if (step == 2 || t - 1 >= nb) release(m.v_empty, sa - step);
+      }
+      if (t < na) {
+        if (!(ok = qk(A{}, sa, t == 0, t == na - 1))) break;
+        if (step == 2 || t >= nb) release(m.k_empty, sa);
+      }
+      if (t > 0 && t - 1 < nb) {
+        if (!(ok = do_pv(B{}, sb - step, t == 1, t == nb))) break;
+        release(m.v_empty, sb - step);
+      }
+      if (t < nb) {
+        if (!(ok = qk(B{}, sb, t == 0, t == nb - 1))) break;
+        release(m.k_empty, sb);
+      }
+      if (t >= na && t >= nb) break;
+    }
+    it += loads;
   }
   if (*(volatile int*)&m.abort && issued) {
     if (elect_one()) umma_commit(&m.drain);
@@ -455,9 +498,10 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
   for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
     const int tiles = w ? x.nb : x.na;
     if (tiles == 0) continue;
-    const int row = w * kTile + rr;              // of the unit's
+    const int row = w * (2 - x.heads) * kTile + rr;          // of the unit's
+    const int head = x.head + w * (x.heads - 1);
     const int see = x.first + row;               // the last kv row it sees
-    const int low = x.first + w * kTile + (warp & 3) * 32;   // the warp's first row's
+    const int low = see - lane;                  // the warp's first row's
     float ref = -FLT_MAX, l = 0.f;
     for (int t = 0; t < tiles; ++t, ++done) {
       if (!cx.wait(&m.s_full[w], done & 1)) return;
@@ -530,7 +574,7 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     ++units;
     tc_fence_after();
     const bool valid = row < x.nq;
-    const int64_t at = (int64_t)(x.q0 + row) * p.h + x.head;
+    const int64_t at = (int64_t)(x.q0 + row) * p.h + head;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int four = lane & ~3;                  // the rows whose vectors this lane stores
     const int64_t step = (int64_t)p.h * D;       // from row to row
@@ -567,7 +611,7 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
       const int i = __ffs(again) - 1;
       again &= again - 1;
       __syncwarp();
-      row_exact<D, BF16>(p, x.b, x.q0 + w * kTile + (warp & 3) * 32 + i, x.head);
+      row_exact<D, BF16>(p, x.b, x.q0 + row - lane + i, head);
     }
   }
 }
