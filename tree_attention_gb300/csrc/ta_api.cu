@@ -1455,13 +1455,13 @@ ta_status tree_attn_expanded(const void* q, int64_t q_token_stride, int64_t q_he
   ta::ExpandedMaps maps;
   const int64_t h = dims->heads, nq = dims->total_q, nk = dims->total_kv, rd = dims->rope_dim;
   if (!make_tiled_map<3>(&maps.q, q, dims->dtype, {dq, h, nq}, {q_head_stride, q_token_stride},
-                         {64, 1, 128}) ||
+                         {64, 1, 64}) ||
       !make_tiled_map<3>(&maps.k, k, dims->dtype, {dk, h, nk}, {k_head_stride, k_token_stride},
-                         {64, 1, 128}) ||
+                         {64, 1, 64}) ||
       !make_tiled_map<3>(&maps.v, v, dims->dtype, {dk, h, nk}, {v_head_stride, v_token_stride},
                          {64, 1, 64}) ||
       !make_tiled_map<3>(&maps.rot, k_rope, dims->dtype, {rd, nk, 1}, {k_rope_stride, k_rope_stride},
-                         {64, 128, 1}))
+                         {64, 64, 1}))
     return cuda_failure();
   return cuda_status(ta::launch_expanded(p, maps, dims->head_dim, dims->dtype == TA_BF16, nsm,
                                          static_cast<cudaStream_t>(stream)));

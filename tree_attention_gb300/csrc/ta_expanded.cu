@@ -48,6 +48,9 @@ struct Item {
   __device__ __forceinline__ int loads() const { return heads == 2 ? 2 * na : max(na, nb); }
   __device__ __forceinline__ int tile(int s) const { return heads == 2 ? s >> 1 : s; }
   __device__ __forceinline__ bool is_short(int s) const { return kv < (tile(s) + 1) * kTile; }
+  // rows of the s-th, and of Q tile w
+  __device__ __forceinline__ int rows(int s) const { return min(kTile, kv - tile(s) * kTile); }
+  __device__ __forceinline__ int q_rows(int w) const { return min(kTile, nq - w * (2 - heads) * kTile); }
 };
 
 struct Misc {
@@ -268,10 +271,14 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
       if (!cx.wait(&m.q_empty[tile], (units[tile] & 1) ^ 1)) return false;
       ++units[tile];
       if (elect_one()) {
-        mbar_arrive_expect_tx(&m.q_full[tile], C::kQTile);
+        // 64 rows at a time, those that there are
+        const int boxes = x.q_rows(tile) > 64 ? 2 : 1;
+        mbar_arrive_expect_tx(&m.q_full[tile], boxes * C::kQTile / 2);
         for (int c = 0; c <= C::kC; ++c)
-          tma_load_3d(cx.smem + C::kOffQ + tile * C::kQTile + c * kSlotBytes, &maps.q, &m.q_full[tile],
-                      64 * c, x.head + tile * (x.heads - 1), x.q0 + tile * (2 - x.heads) * kTile);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(cx.smem + C::kOffQ + tile * C::kQTile + c * kSlotBytes + i * 8192, &maps.q,
+                        &m.q_full[tile], 64 * c, x.head + tile * (x.heads - 1),
+                        x.q0 + tile * (2 - x.heads) * kTile + 64 * i);
       }
       __syncwarp();
       return true;
@@ -290,15 +297,17 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
     for (int t = 0; t < loads; ++t, ++it) {
       const int row = x.kv0 + x.tile(t) * kTile, s = it & 1, head = x.head + (t & (x.heads - 1));
       uint64_t* v_bar = x.is_short(t) ? &m.v_short[s] : &m.v_full[s];
+      const int boxes = x.rows(t) > 64 ? 2 : 1;
       for (int c = 0; c <= C::kC; ++c) {
         uint8_t* to = slot();
         if (!to) return;
         if (elect_one()) {
-          if (c == 0) mbar_arrive_expect_tx(&m.k_full[s], C::kQTile);
-          if (c < C::kC)
-            tma_load_3d(to, &maps.k, &m.k_full[s], 64 * c, head, row);
-          else
-            tma_load_3d(to, &maps.rot, &m.k_full[s], 0, row, 0);
+          if (c == 0) mbar_arrive_expect_tx(&m.k_full[s], boxes * C::kQTile / 2);
+          for (int i = 0; i < boxes; ++i)
+            if (c < C::kC)
+              tma_load_3d(to + i * 8192, &maps.k, &m.k_full[s], 64 * c, head, row + 64 * i);
+            else
+              tma_load_3d(to + i * 8192, &maps.rot, &m.k_full[s], 0, row + 64 * i, 0);
         }
         __syncwarp();
       }
@@ -307,8 +316,8 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
         uint8_t* to = slot();
         if (!to) return;
         if (elect_one()) {
-          if (half == 0) mbar_arrive_expect_tx(v_bar, kTile * D * 2);
-          for (int c = 0; c < C::kC; ++c)
+          if (half == 0) mbar_arrive_expect_tx(v_bar, boxes * kTile * D);
+          for (int c = 0; c < C::kC && half < boxes; ++c)
             tma_load_3d(to + c * 8192, &maps.v, v_bar, 64 * c, head, row + 64 * half);
         }
         __syncwarp();
@@ -317,8 +326,8 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
   }
 }
 
-// Zeroes the value rows of a sequence's last tile that are not its own: what does
-// not count must not reach the products as NaN.
+// Zeroes the value rows behind a sequence's last, up to the 16 of a product: what
+// does not count must not reach the products as NaN.
 template <int D>
 __device__ void run_cleaner(const Ctx& cx, int lane) {
   using C = Cfg<D>;
@@ -331,7 +340,7 @@ __device__ void run_cleaner(const Ctx& cx, int lane) {
     if (valid >= kTile) continue;
     for (uint32_t t = it - x.heads; t < it; ++t) {
       if (!cx.wait(&m.v_short[t & 1], count[t & 1]++ & 1)) return;
-      for (int i = lane; i < (kTile - valid) * C::kC * 8; i += 32) {
+      for (int i = lane; i < (-valid & 15) * C::kC * 8; i += 32) {
         const int row = valid + i / (C::kC * 8), c = i / 8 % C::kC;
         const uint32_t chunk = t * C::kPerTile + C::kC + 1 + row / 64;
         *reinterpret_cast<uint4*>(cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes + c * 8192 +
@@ -416,10 +425,11 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       v[i] = dv + (((g * C::kPerTile + C::kC + 1 + i) % kSlots * kSlotBytes) >> 4);
+    const int steps = (x.rows(s) + 15) / 16;
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < kTile / 16; ++i)
-        umma_f16_tmem_a(tmem + C::kTmemO + 128 * w, tmem + C::kTmemS + 128 * w + 8 * i,
+        if (i < steps) umma_f16_tmem_a(tmem + C::kTmemO + 128 * w, tmem + C::kTmemS + 128 * w + 8 * i,
                         v[i >> 2] + ((i & 3) * 2048 >> 4), idesc_pv, i > 0 ? 1u : (uint32_t)!first);
       if (last) umma_commit(&m.o_full[w]);
     }
@@ -502,34 +512,23 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     const int head = x.head + w * (x.heads - 1);
     const int see = x.first + row;               // the last kv row it sees
     const int low = see - lane;                  // the warp's first row's
+    const bool work = row - lane < x.nq;
     float ref = -FLT_MAX, l = 0.f;
     for (int t = 0; t < tiles; ++t, ++done) {
       if (!cx.wait(&m.s_full[w], done & 1)) return;
+      if (!work) {                               // no row of the warp is the sequence's
+        if (lane == 0) mbar_arrive(&m.p_full[w]);
+        continue;
+      }
       tc_fence_after();
       // The scores are read twice, 32 at a time, for their maximum and for the
-      // weights (128 registers for all of them do not go with the rest); a chunk is
-      // on its way while the one before is worked on.
+      // weights (128 registers for all of them do not go with the rest).
       float s[2][32];
-      const int lim = see - t * kTile;
-      const bool masked = t * kTile + kTile - 1 > low;
-      float top[2] = {-INFINITY, -INFINITY};
-      tmem_ld32(s_at, s[0]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_wait_ld(s[c & 1]);
-        tmem_ld32(s_at + 32 * ((c + 1) & 3), s[(c + 1) & 1]);
-        if (masked) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            top[j & 1] = fmaxf(top[j & 1], 32 * c + j <= lim ? s[c & 1][j] * p.scale_log2 : -INFINITY);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], s[c & 1][j] * p.scale_log2);
-        }
-      }
-      const float most = fmaxf(top[0], top[1]);
-      const bool move = most - ref > Ref<BF16>::kTop;
-      if (__any_sync(0xffffffffu, move)) {
+      const int lim = see - t * kTile, lim0 = low - t * kTile;
+      float2 sum = make_float2(0.f, 0.f);
+      auto refer = [&](float most) {             // moves the reference where it has to be
+        const bool move = most - ref > Ref<BF16>::kTop;
+        if (!__any_sync(0xffffffffu, move)) return;
         float f = 1.f;
         if (move) {
           const float to = most - Ref<BF16>::kPut;
@@ -538,31 +537,74 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
           l *= f;
         }
         // the product before has been waited for with these scores: O is at rest
-        if (t > 0) {
-          tmem_wait_ld(s[0]);                  // no load may be under way into registers a call saves
-          rescale<D>(o_at, f);
+        if (t > 0) rescale<D>(o_at, f);
+      };
+      float top[2] = {-INFINITY, -INFINITY};
+      tmem_ld32(s_at, s[0]);
+      if (lim0 >= kTile - 1) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c & 1]);
+          if (c < 3) tmem_ld32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], s[c & 1][j] * p.scale_log2);
         }
-      }
-      float2 sum = make_float2(0.f, 0.f);
-      const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
+        refer(fmaxf(top[0], top[1]));
+        tmem_ld32(s_at, s[0]);
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_wait_ld(s[c & 1]);
-        if (c < 3) tmem_ld32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
-        uint32_t w16[16];
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c & 1]);
+          if (c < 3) tmem_ld32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+          uint32_t w16[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float2 e = ffma2(make_float2(s[c & 1][2 * j], s[c & 1][2 * j + 1]), scale, shift);
-          if (masked) {
-            e.x = 32 * c + 2 * j <= lim ? e.x : -INFINITY;
-            e.y = 32 * c + 2 * j + 1 <= lim ? e.y : -INFINITY;
+          for (int j = 0; j < 16; ++j) {
+            float2 e = ffma2(make_float2(s[c & 1][2 * j], s[c & 1][2 * j + 1]), scale, shift);
+            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            sum = fadd2(sum, e);
+            w16[j] = pack2<BF16>(e.x, e.y);
           }
-          e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-          sum = fadd2(sum, e);
-          w16[j] = pack2<BF16>(e.x, e.y);
+          // over scores that have been read: columns 16 c on are of chunk c / 2
+          tmem_st16(s_at + 16 * c, w16);
         }
-        // over scores that have been read: columns 16 c on are of chunk c / 2
-        tmem_st16(s_at + 16 * c, w16);
+      } else {
+        // The diagonal: chunks that none of the warp's rows sees are left out.
+        const int last = min(3, (lim0 + 31) / 32);
+#pragma unroll 1
+        for (int c = 0; c <= last; ++c) {
+          tmem_wait_ld(s[0]);
+          if (32 * c + 31 > lim0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              top[j & 1] = fmaxf(top[j & 1], 32 * c + j <= lim ? s[0][j] * p.scale_log2 : -INFINITY);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], s[0][j] * p.scale_log2);
+          }
+          tmem_ld32(s_at + (c < last ? 32 * (c + 1) : 0), s[0]);
+        }
+        tmem_wait_ld(s[0]);
+        refer(fmaxf(top[0], top[1]));
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w16[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w16[j] = 0;
+          if (c <= last) {
+            tmem_ld32(s_at + 32 * c, s[0]);
+            tmem_wait_ld(s[0]);
+            const int left = lim - 32 * c;       // the last column that counts, if below 31
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float2 e = ffma2(make_float2(s[0][2 * j], s[0][2 * j + 1]), scale, shift);
+              e = make_float2(2 * j <= left ? ex2_approx(e.x) : 0.f, 2 * j < left ? ex2_approx(e.y) : 0.f);
+              sum = fadd2(sum, e);
+              w16[j] = pack2<BF16>(e.x, e.y);
+            }
+          }
+          tmem_st16(s_at + 16 * c, w16);
+        }
       }
       l += sum.x + sum.y;
       tmem_wait_st();
@@ -572,6 +614,10 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     }
     if (!cx.wait(&m.o_full[w], units & 1)) return;
     ++units;
+    if (!work) {
+      if (lane == 0) mbar_arrive(&m.o_free[w]);
+      continue;
+    }
     tc_fence_after();
     const bool valid = row < x.nq;
     const int64_t at = (int64_t)(x.q0 + row) * p.h + head;

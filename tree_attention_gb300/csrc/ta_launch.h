@@ -283,9 +283,9 @@ struct ExpandedParams {
   int debug_stall;                        // as in AttnParams
 };
 
-// Tensor maps of the expanded form, all with 128-byte swizzle: q [total_q, h, d +
-// rope_dim] (box {64, 1 head, 128 rows}), k (the same) and v ({64, 1, 64}) [total_kv,
-// h, d], k_rope [total_kv, rope_dim] ({64, 128}).  Elements outside read as zeros.
+// Tensor maps of the expanded form, all with 128-byte swizzle and boxes of 64
+// elements of 64 rows: q [total_q, h, d + rope_dim], k and v [total_kv, h, d], k_rope
+// [total_kv, rope_dim].  Elements outside read as zeros.
 struct ExpandedMaps {
   CUtensorMap q, k, v, rot;
 };
