@@ -32,7 +32,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* indptr, int batch, i
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 160;
 
 // The two 16-byte vectors i and i + half_vecs of a rotary row of 16 half_vecs
 // elements, turned by (cos, sin) pairs cs: with halves as layout, element e of
@@ -59,8 +59,9 @@ __device__ __forceinline__ void turn(uint4& u0, uint4& u1, const float2* cs, int
   u1 = pack8<BF16>(b);
 }
 
-// One CTA per token.  Its first warp looks up the token's cache row and moves
-// the latent and the rotary key, all of them the heads' rotary queries.
+// One CTA per token.  Its last warp looks up the token's cache row and moves the
+// latent and the rotary key, the others the heads' rotary queries, whose loads go
+// out before the angles are known.
 template <bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendParams p) {
   __shared__ float2 s_cs[32];
@@ -69,15 +70,27 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x;
   const int half_vecs = p.rope_dim / 16, width = p.rank + p.rope_dim;
-  if (LAYOUT != 0 && tid < p.rope_dim / 2) {
+  auto angles = [&](int j) {
     // the fraction of a turn, exact modulo 1, then one rounding to float32
-    const uint64_t ph = (uint64_t)(int64_t)p.positions[t] * p.turns[tid];
+    const uint64_t ph = (uint64_t)(int64_t)p.positions[t] * p.turns[j];
     float sn, cs;
     sincospif((float)(int64_t)ph * 0x1p-63f, &sn, &cs);
-    s_cs[tid] = make_float2(cs * p.magnitude, sn * p.magnitude);
-  }
-  __syncthreads();
-  if (warp == 0) {
+    s_cs[j] = make_float2(cs * p.magnitude, sn * p.magnitude);
+  };
+  if (warp == kAppendThreads / 32 - 1) {
+    const int vecs = p.rank / 8;           // 32 or 64
+    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.latent_stride);
+    const uint4* k = reinterpret_cast<const uint4*>(p.k_rope + t * p.k_rope_stride);
+    uint4 u[2], k0, k1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      u[i] = lane + 32 * i < vecs ? src[lane + 32 * i] : make_uint4(0, 0, 0, 0);
+    if (lane < half_vecs) {
+      k0 = k[lane];
+      k1 = k[lane + half_vecs];
+    }
+    if (LAYOUT != 0 && lane < p.rope_dim / 2) angles(lane);
+    __syncthreads();
     const int b = find_sequence(p.append_indptr, p.tab.batch, t, lane);
     const int a0 = p.append_indptr[b], a1 = p.append_indptr[b + 1];
     const int p0 = p.tab.page_indptr[b], p1 = p.tab.page_indptr[b + 1], last = p.tab.length_info[b];
@@ -93,17 +106,13 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
     }
     if (slot < 0 && lane == 0) report_bad_tables(p.error);
     uint16_t* rows = p.rows_out ? p.rows_out + (int64_t)t * width : nullptr;
-    const int vecs = p.rank / 8;           // 32 or 64
-    const uint4* src = reinterpret_cast<const uint4*>(p.latent + t * p.latent_stride);
-    uint4 u[2];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      u[i] = lane + 32 * i < vecs ? src[lane + 32 * i] : make_uint4(0, 0, 0, 0);
       float2 x[4];
       unpack8<BF16>(u[i], x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum += x[k].x * x[k].x + x[k].y * x[k].y;
+      for (int j = 0; j < 4; ++j) sum += x[j].x * x[j].x + x[j].y * x[j].y;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -117,38 +126,52 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
         unpack8<BF16>(u[i], x);
         unpack8<BF16>(reinterpret_cast<const uint4*>(p.weight)[v], w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[k] = make_float2(x[k].x * inv * w[k].x, x[k].y * inv * w[k].y);
+        for (int j = 0; j < 4; ++j)
+          x[j] = make_float2(x[j].x * inv * w[j].x, x[j].y * inv * w[j].y);
         u[i] = pack8<BF16>(x);
       }
       if (slot >= 0) reinterpret_cast<uint4*>(p.pages + slot)[v] = u[i];
       if (rows) reinterpret_cast<uint4*>(rows)[v] = u[i];
     }
     if (lane < half_vecs) {
-      const uint4* k = reinterpret_cast<const uint4*>(p.k_rope + t * p.k_rope_stride);
-      uint4 u0 = k[lane], u1 = k[lane + half_vecs];
-      if (LAYOUT != 0) turn<BF16, LAYOUT>(u0, u1, s_cs, lane, half_vecs);
+      if (LAYOUT != 0) turn<BF16, LAYOUT>(k0, k1, s_cs, lane, half_vecs);
       if (slot >= 0) {
         uint4* to = reinterpret_cast<uint4*>(p.pages + slot + p.rank);
-        to[lane] = u0;
-        to[lane + half_vecs] = u1;
+        to[lane] = k0;
+        to[lane + half_vecs] = k1;
       }
       if (rows) {
         uint4* to = reinterpret_cast<uint4*>(rows + p.rank);
-        to[lane] = u0;
-        to[lane + half_vecs] = u1;
+        to[lane] = k0;
+        to[lane + half_vecs] = k1;
       }
     }
+    return;
   }
-  if (p.q_rope == nullptr) return;
-  for (int e = tid; e < p.h * half_vecs; e += kAppendThreads) {
-    const int h = e / half_vecs, i = e % half_vecs;
-    const uint4* q = reinterpret_cast<const uint4*>(p.q_rope + t * p.q_token_stride + h * p.q_head_stride);
-    uint4 u0 = q[i], u1 = q[i + half_vecs];
-    if (LAYOUT != 0) turn<BF16, LAYOUT>(u0, u1, s_cs, i, half_vecs);
-    uint4* to = reinterpret_cast<uint4*>(p.q_out + t * p.qo_token_stride + h * p.qo_head_stride);
-    to[i] = u0;
-    to[i + half_vecs] = u1;
+  const int items = p.q_rope != nullptr ? p.h * half_vecs : 0;
+  constexpr int kBatch = 4, kStep = kAppendThreads - 32;   // 128 heads of 64 elements at most
+  uint4 u0[kBatch], u1[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int e = tid + j * kStep;
+    if (e < items) {
+      const uint4* q = reinterpret_cast<const uint4*>(p.q_rope + t * p.q_token_stride +
+                                                      (e / half_vecs) * p.q_head_stride);
+      u0[j] = q[e % half_vecs];
+      u1[j] = q[e % half_vecs + half_vecs];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int e = tid + j * kStep;
+    if (e < items) {
+      if (LAYOUT != 0) turn<BF16, LAYOUT>(u0[j], u1[j], s_cs, e % half_vecs, half_vecs);
+      uint4* to = reinterpret_cast<uint4*>(p.q_out + t * p.qo_token_stride +
+                                           (e / half_vecs) * p.qo_head_stride);
+      to[e % half_vecs] = u0[j];
+      to[e % half_vecs + half_vecs] = u1[j];
+    }
   }
 }
 
