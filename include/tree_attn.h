@@ -502,8 +502,9 @@ ta_status tree_attn_append_latent(const void* latent, int64_t latent_stride, con
  * out NaN.  Weights are rounded to dtype before they meet the values (and out is
  * divided by the sum of the rounded ones), all else is float32.  The result does
  * not depend on timing.
- * Inconsistent page tables are reported by tree_attn_device_status and nothing
- * is computed.  q, pages and out 16-byte aligned.  Asynchronous on stream. */
+ * Inconsistent page tables (or 2^31 pairs of 128 heads of q rows and 128 kv rows and
+ * more) are reported by tree_attn_device_status and nothing is computed.  q, pages
+ * and out 16-byte aligned.  Asynchronous on stream. */
 ta_status tree_attn_decode_latent(const void* q, const void* pages, const int32_t* page_indptr,
                                   const int32_t* page_values, const int32_t* length_info,
                                   void* out, float* lse, float sm_scale,

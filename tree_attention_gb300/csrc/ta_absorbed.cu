@@ -175,9 +175,8 @@ struct Misc {
   float exchange[2][4][64];
   Piece piece[kPieces];
   long long scan[12];
-  long long first_unit;              // of the range's first sequence
-  LatentSeq first;
-  int first_seq;
+  LatentSeq first;                   // the range's first sequence, its first tile
+  int first_seq, first_unit;
   uint32_t tmem;
   int abort;
 };
@@ -220,14 +219,13 @@ struct Ctx {
   }
 };
 
-// Pair i's tiles of U: from here on.
+// Pair i's tiles, of fewer than 2^31: from here on.
 struct Split {
-  long long per;
-  int extra;
-  __host__ __device__ long long start(int i) const { return i * per + (i < extra ? i : extra); }
-  __device__ int pair_of(long long u) const {
-    const long long wide = extra * (per + 1);
-    return (int)(u < wide ? u / (per + 1) : extra + (u - wide) / per);
+  int per, extra;
+  __device__ int start(int i) const { return i * per + (i < extra ? i : extra); }
+  __device__ int pair_of(int u) const {
+    const int wide = extra * (per + 1);
+    return u < wide ? u / (per + 1) : extra + (u - wide) / per;
   }
 };
 
@@ -245,10 +243,9 @@ __device__ __forceinline__ int items_of(const LatentSeq& s, int h) {
 __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& split, int pair,
                             bool leader) {
   Misc& m = *cx.m;
-  long long u = split.start(pair);
-  const long long u_end = split.start(pair + 1);
-  int b = m.first_seq;
-  long long base = m.first_unit;
+  int u = split.start(pair);
+  const int u_end = split.start(pair + 1);
+  int b = m.first_seq, base = m.first_unit;
   LatentMerge merge{};
   uint32_t n = 0;
   LatentSeq s = m.first;
@@ -261,14 +258,14 @@ __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& s
         loaded = true;
       }
       const int kt = tiles_of(s), items = items_of(s, p.h);
-      const long long off = u - base;
-      if (off >= (long long)kt * items) {
-        base += (long long)kt * items;
+      const int off = u - base;
+      if (off >= kt * items) {
+        base += kt * items;
         ++b;
         loaded = false;
         continue;
       }
-      const int item = (int)(off / kt);
+      const int item = off / kt;
       x.b = b;
       x.p0 = s.p0;
       x.kv = s.kv;
@@ -278,11 +275,11 @@ __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& s
       x.m_row = item * kTile;
       x.row0 = s.q0 * p.h + x.m_row;
       x.nrows = min(kTile, s.qo * p.h - x.m_row);
-      x.t0 = (int)(off - (long long)item * kt);
-      x.t1 = (int)min((long long)kt, x.t0 + (u_end - u));
+      x.t0 = off - item * kt;
+      x.t1 = min(kt, x.t0 + (u_end - u));
       x.slot = x.t0 == 0 && x.t1 == kt ? -1 : x.t0 == 0;
       if (x.slot == 1) {
-        const long long last = base + (long long)(item + 1) * kt - 1;
+        const int last = base + (item + 1) * kt - 1;
         merge.b = b;
         merge.row0 = x.row0;
         merge.m_row = x.m_row;
@@ -365,6 +362,13 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
   Misc& m = *cx.m;
   uint8_t* sv = cx.smem + C::kOffV;
   uint32_t n = 0, it = 0;
+  auto prefetch = [&](int page) {
+    if (lane < C::kPages && page < p.tab.num_pages) {
+      tma_prefetch_l2_4d(&maps.v, 0, 0, (int)cta * C::kHalf, page);
+      tma_prefetch_l2_3d(&maps.rot, RANK, 8 * (int)cta, page);
+    }
+    __syncwarp();
+  };
   for (;; ++n) {
     const int slot = n % kPieces;
     if (!cx.wait_warp(&m.piece_full[slot], (n / kPieces) & 1)) return;
@@ -373,6 +377,7 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
     if (lane == 0) mbar_arrive(&m.piece_empty[slot]);
     if (x.t0 == x.t1) return;
     int next = page_of(p, x, x.t0, lane), after = x.t0 + 1 < x.t1 ? page_of(p, x, x.t0 + 1, lane) : 0;
+    if (x.t0 + 1 < x.t1) prefetch(after);
     for (int t = x.t0; t < x.t1; ++t, ++it) {
       const int page = next;
       next = after;
@@ -381,11 +386,7 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
       // go into L2 ahead of it
       if (t + kAhead < x.t1) {
         after = page_of(p, x, t + kAhead, lane);
-        if (lane < C::kPages && after < p.tab.num_pages) {
-          tma_prefetch_l2_4d(&maps.v, 0, 0, (int)cta * C::kHalf, after);
-          tma_prefetch_l2_3d(&maps.rot, RANK, 8 * (int)cta, after);
-        }
-        __syncwarp();
+        prefetch(after);
       }
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -809,31 +810,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane >= d) sum += y;
   }
   if (lane == 31) m.scan[warp] = sum;
-  const bool stop = __syncthreads_or(bad);
-  Split split{0, 0};
-  if (!stop) {
-    long long before = sum - mine, total = 0;
+  bool stop = __syncthreads_or(bad);
+  long long before = sum - mine, total = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += m.scan[i];
-      total += m.scan[i];
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += m.scan[i];
+    total += m.scan[i];
+  }
+  stop |= total > INT32_MAX;
+  const Split split{(int)total / pairs, (int)total % pairs};
+  const int u = split.start(pair);
+  if (!stop && u >= before && u < before + mine) {
+    int b = b_lo;
+    for (; each > 1 && b < b_hi; ++b) {
+      s = latent_seq(p, b);
+      const int k = tiles_of(s) * items_of(s, p.h);
+      if (u < before + k) break;
+      before += k;
     }
-    split.per = total / pairs;
-    split.extra = (int)(total % pairs);
-    const long long u = split.start(pair);
-    if (u >= before && u < before + mine) {
-      int b = b_lo;
-      for (; each > 1 && b < b_hi; ++b) {
-        s = latent_seq(p, b);
-        const long long k = (long long)tiles_of(s) * items_of(s, p.h);
-        if (u < before + k) break;
-        before += k;
-      }
-      m.first_seq = b;
-      m.first = s;
-      m.first_unit = before;
-    }
-  } else if (tid == 0) {
+    m.first_seq = b;
+    m.first = s;
+    m.first_unit = (int)before;
+  }
+  if (stop && tid == 0) {
     atomicOr(p.error, DEVERR_BAD_INDPTR);
     if (cta == 0) p.merge[pair] = LatentMerge{};
   }
