@@ -790,3 +790,130 @@ def test_one_workspace_for_several_caches():
     check_absorbed(a, qa, *oa, 0.07)
     check_absorbed(b, qb, *ob, 0.07)
     assert shared.device_status() == ta.TA_OK
+
+
+# --------------------------------------------------------------------------
+# the ends of what is allowed
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("sm", [0.0, -0.07])
+def test_scales_of_zero_and_below(sm):
+    s = Setup([700, 3, 130], 20, 512, 64, seed=12)
+    q = s.randn(3, 20, s.w)
+    out, lse = s.cache.decode(q, sm)
+    check_absorbed(s, q, out, lse, sm)
+    e = Expanded([70, 300], [90, 300], 3, 128, 64, "bf16", seed=13)
+    out, lse = e.run(sm)
+    assert ta.device_status(e.ws) == ta.TA_OK
+    e.check(out, lse, sm)
+
+
+def test_expanded_rows_head_by_head():
+    """Queries, keys and values laid out with the heads outside the tokens."""
+    e = Expanded([70, 130], [200, 130], 5, 128, 48, "fp16", seed=14)
+    far = lambda x: x.transpose(0, 1).contiguous().transpose(0, 1)
+    want = [t.clone() for t in e.run(0.07)]
+    got = e.run(0.07, q=far(e.q), k=far(e.k), v=far(e.v), out=torch.zeros_like(e.out),
+                lse=torch.zeros_like(e.lse))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    e.check(*want, 0.07)
+
+
+def test_expanded_repeats_and_captures():
+    """A captured call replayed, and another beside it on the same workspace."""
+    e = Expanded([200, 3, 900], [200, 50, 1500], 4, 128, 64, "bf16", seed=15)
+    want = [t.clone() for t in e.run(0.07)]
+    e.check(*want, 0.07)
+    out, lse = torch.zeros_like(e.out), torch.zeros_like(e.lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        e.run(0.07, out=out, lse=lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        g.replay()
+        with torch.cuda.stream(side):
+            o2, l2 = e.run(0.07, out=torch.empty_like(out), lse=torch.empty_like(lse))
+    torch.cuda.synchronize()
+    for o, x in ((out, want[0]), (o2, want[0]), (lse, want[1]), (l2, want[1])):
+        assert torch.equal(o, x)
+    assert ta.device_status(e.ws) == ta.TA_OK
+
+
+def test_expanded_largest_batch():
+    rng = np.random.default_rng(16)
+    kv = rng.integers(0, 6, 16384)
+    new = np.minimum(rng.integers(0, 4, 16384), kv)
+    e = Expanded([int(x) for x in new], [int(x) for x in kv], 2, 64, 16, "bf16", seed=16)
+    out, lse = e.run(0.1)
+    assert ta.device_status(e.ws) == ta.TA_OK
+    e.check(out, lse, 0.1)
+    with pytest.raises(ta.TreeAttnError):
+        e.run(0.1, q_indptr=i32(np.zeros(16386)), kv_indptr=i32(np.zeros(16386)))
+
+
+def test_expanded_long_prompt():
+    e = Expanded([12000], [20000], 2, 128, 64, "bf16", seed=17)
+    out, lse = e.run(0.07)
+    assert ta.device_status(e.ws) == ta.TA_OK
+    e.check(out, lse, 0.07)
+
+
+def test_tree_and_append_of_the_largest_batch():
+    """16,384 sequences of 1 to 40 rows, each ending in a tree of one node."""
+    rng = np.random.default_rng(18)
+    kv = rng.integers(1, 41, 16384)
+    n = -(-kv // 16)
+    s = Setup([1], 3, 256, 16, seed=18)
+    s.kv, s.indptr, s.values = kv, indptr(n), np.arange(n.sum())
+    s.last, s.pool = kv - (n - 1) * 16, s.randn(int(n.sum()), 16, s.w)
+    s.cache = s.handle()
+    one, q = i32(np.arange(16385)), s.randn(16384, 3, s.w)
+    x = s.randn(16384, s.w)
+    s.cache.append(x[:, :256], x[:, 256:], one)
+    pid = torch.from_numpy(s.indptr[1:] - 1).cuda()
+    assert torch.equal(s.pool[pid, torch.from_numpy(s.last - 1).cuda()], x)
+    out, lse = s.cache.tree_attn(q, one, one, i32([[0, 1]] * 16384), 0.1)
+    assert s.cache.device_status() == ta.TA_OK
+    check_absorbed(s, q, out, lse, 0.1)
+
+
+def test_streams_given_by_address():
+    s = Setup([300, 40], 16, 512, 64, seed=19)
+    q, st = s.randn(2, 16, s.w), torch.cuda.Stream()
+    want = s.cache.decode(q, 0.07)
+    torch.cuda.synchronize()
+    got = s.cache.decode(q, 0.07, stream=st.cuda_stream)
+    st.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# --------------------------------------------------------------------------
+# a wait that runs out
+# --------------------------------------------------------------------------
+
+def test_waits_that_run_out_are_reported():
+    """The products' warp waits on a barrier that nothing arrives on: every wait
+    ends, the status says so, nothing is written, and the next call is as ever."""
+    s = Setup([2000, 30], 64, 512, 64, seed=21)
+    q = s.randn(2, 64, s.w)
+    want = [t.clone() for t in s.cache.decode(q, 0.07)]
+    e = Expanded([200, 3], [200, 50], 4, 128, 64, "bf16", seed=22)
+    ewant = [t.clone() for t in e.run(0.07)]
+    torch.cuda.synchronize()
+    out, lse = torch.full_like(want[0], 5), torch.full_like(want[1], 5)
+    eout, else_ = torch.full_like(e.out, 5), torch.full_like(e.lse, 5)
+    ta.set_wait_hooks(20_000_000, True)
+    try:
+        s.cache.decode(q, 0.07, out=out, lse=lse)
+        assert s.cache.device_status() == ta.TA_ERR_DEVICE_TIMEOUT
+        e.run(0.07, out=eout, lse=else_)
+        assert ta.device_status(e.ws) == ta.TA_ERR_DEVICE_TIMEOUT
+    finally:
+        ta.set_wait_hooks(0, False)
+    assert (out == 5).all() and (lse == 5).all() and (eout == 5).all() and (else_ == 5).all()
+    for _ in range(2):
+        got, egot = s.cache.decode(q, 0.07), e.run(0.07)
+        assert s.cache.device_status() == ta.TA_OK and ta.device_status(e.ws) == ta.TA_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(egot[0], ewant[0]) and torch.equal(egot[1], ewant[1])

@@ -861,8 +861,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  // after a wait ran out copies may still be on their way into shared memory
+  // after a wait ran out copies may still be on their way into shared memory, and
+  // there is nothing to join
   if (m.abort) {
+    if (tid == 0 && cta == 0) p.merge[pair] = LatentMerge{};
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
