@@ -571,6 +571,13 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
     x = combine(combine(e[0][rr], e[1][rr]), combine(e[2][rr], e[3][rr]));
     return true;
   };
+  // where the walk of the tree enters this thread's row's node
+  auto enter_of = [&](const Piece& x) {
+    const int row = 64 * (int)cta + rr;
+    if (x.start >= x.kv || row >= x.nrows) return 0;
+    return reinterpret_cast<const int2*>(p.tree_order)[x.m0 + x.node0 + (x.m_row + row) / p.h].x;
+  };
+  int enter_next = 0;
   for (;; ++n) {
     const int slot = n % kPieces;
     if (!cx.wait_warp(&m.piece_full[slot], (n / kPieces) & 1)) return;
@@ -581,8 +588,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
     const int row = 64 * (int)cta + rr;          // of the item's 128
     const bool work = 64 * (int)cta + (quarter & 1) * 32 < x.nrows;   // some row of the warp exists
     const int2* order = reinterpret_cast<const int2*>(p.tree_order) + x.m0;
-    int enter = 0;
-    if (x.start < x.kv && row < x.nrows) enter = order[x.node0 + (x.m_row + row) / p.h].x;
+    const int enter = n == 0 ? enter_of(x) : enter_next;
     // l: the sum of the weights, lr: as rounded for the product, which O is divided
     // by (a row that one weight dominates then keeps its value's bits)
     float ref = -FLT_MAX, l = 0.f, lr = 0.f;
@@ -664,6 +670,12 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       __syncwarp();
       if (lane == 0) arrive_remote(in_first_cta(&m.p_full));
     }
+    // the next piece's rows are looked up behind this one's last product
+    if (p.tree_order) {
+      const int after = (n + 1) % kPieces;
+      if (!cx.wait_warp(&m.piece_full[after], ((n + 1) / kPieces) & 1)) return;
+      enter_next = enter_of(m.piece[after]);
+    }
     // the piece's result
     if (!cx.wait_warp(&m.pv_done, (it - 1) & 1)) return;
     if (work) {
@@ -677,7 +689,8 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
         const float inv = lr == 0.f ? 0.f : 1.f / lr;
         const int four = lane & ~3;              // the rows whose vectors this lane stores
         uint16_t* out = p.out + (at - lane + four) * RANK + col0 + (lane & 3) * 8;
-        float odd = 0.f;
+        const float2 zero = make_float2(0.f, 0.f), by = make_float2(inv, inv);
+        float2 odd2 = zero;
 #pragma unroll 1
         for (int c = 0; c < C::kCols; c += 32) {
           float v[32];
@@ -689,8 +702,10 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              odd += v[8 * i + 2 * k] * 0.f + v[8 * i + 2 * k + 1] * 0.f;
-              w[k] = pack2<BF16>(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+              const float2 o = make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+              odd2 = ffma2(o, zero, odd2);
+              const float2 z = ffma2(o, by, zero);
+              w[k] = pack2<BF16>(z.x, z.y);
             }
             y[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -699,6 +714,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
           for (int j = 0; j < 4; ++j)
             if (row - lane + four + j < x.nrows) *reinterpret_cast<uint4*>(out + j * RANK + c) = y[j];
         }
+        const float odd = odd2.x + odd2.y;
         if (valid && part == 0) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
         // a value that is not finite, though the weights are: it may be one that does not count
         unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);

@@ -625,7 +625,8 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     const int four = lane & ~3;                  // the rows whose vectors this lane stores
     const int64_t step = (int64_t)p.h * D;       // from row to row
     uint16_t* out = p.out + (at + (four - lane) * (int64_t)p.h) * D + (lane & 3) * 8;
-    float odd = 0.f;
+    const float2 zero = make_float2(0.f, 0.f), by = make_float2(inv, inv);
+    float2 odd2 = zero;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float v[32];
@@ -637,8 +638,10 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
         uint32_t y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          odd += v[8 * i + 2 * k] * 0.f + v[8 * i + 2 * k + 1] * 0.f;
-          y[k] = pack2<BF16>(v[8 * i + 2 * k] * inv, v[8 * i + 2 * k + 1] * inv);
+          const float2 o = make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+          odd2 = ffma2(o, zero, odd2);
+          const float2 r = ffma2(o, by, zero);
+          y[k] = pack2<BF16>(r.x, r.y);
         }
         z[i] = make_uint4(y[0], y[1], y[2], y[3]);
       }
@@ -650,6 +653,7 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&m.o_free[w]);
+    const float odd = odd2.x + odd2.y;
     if (valid) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
     // a value that is not finite, though the weights are: it may be one not seen
     unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
