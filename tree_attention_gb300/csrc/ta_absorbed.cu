@@ -577,6 +577,10 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
     if (x.start >= x.kv || row >= x.nrows) return 0;
     return reinterpret_cast<const int2*>(p.tree_order)[x.m0 + x.node0 + (x.m_row + row) / p.h].x;
   };
+  // a scale of nothing is made one that leaves a score below 2^-20: times the infinity
+  // of what does not count it stays infinite
+  const float scale = p.scale_log2 == 0.f ? 1e-40f : p.scale_log2;
+  const float2 scale2 = make_float2(scale, scale);
   int enter_next = 0;
   for (;; ++n) {
     const int slot = n % kPieces;
@@ -615,19 +619,29 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       __syncwarp();
       if (lane == 0) arrive_remote(in_first_cta(&m.s_empty[b]));
       if (work) {
+        // the largest of the scores, times their scale afterwards, whose sign is known;
+        // what does not count is made the least there is
+        const float least = scale > 0.f ? -INFINITY : INFINITY;
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const int a = __shfl_sync(0xffffffffu, iv.x, j), e = __shfl_sync(0xffffffffu, iv.y, j);
-            s[j] = a <= enter && enter < e ? s[j] * p.scale_log2 : -INFINITY;
+            s[j] = a <= enter && enter < e ? s[j] : least;
           }
+        }
+        float top = s[0], top2 = s[1];
+        if (scale > 0.f) {
+#pragma unroll
+          for (int j = 2; j < 32; j += 2) {
+            top = fmaxf(top, s[j]);
+            top2 = fmaxf(top2, s[j + 1]);
+          }
+          top = fmaxf(top, top2);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] *= p.scale_log2;
+          for (int j = 1; j < 32; ++j) top = fminf(top, s[j]);
         }
-        float top = s[0];
-#pragma unroll
-        for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j]);
+        top = top == least ? -INFINITY : top * scale;
         if (!exchange(top, [](float a, float c) { return fmaxf(a, c); })) return;
         const bool move = top - ref > Ref<BF16>::kTop;
         // P's buffer is free, and O at rest, once the tile before is done
@@ -648,12 +662,14 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
           }
         }
         float2 sum = make_float2(0.f, 0.f), sum_r = sum;
+        const float2 shift = make_float2(-ref, -ref);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 e = make_float2(ex2_approx(s[8 * i + 2 * k] - ref), ex2_approx(s[8 * i + 2 * k + 1] - ref));
+            float2 e = ffma2(make_float2(s[8 * i + 2 * k], s[8 * i + 2 * k + 1]), scale2, shift);
+            e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
             w[k] = pack2<BF16>(e.x, e.y);
             sum = fadd2(sum, e);
             sum_r = fadd2(sum_r, unpack2<BF16>(w[k]));
