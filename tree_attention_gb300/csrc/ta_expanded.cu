@@ -546,10 +546,19 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
         for (int c = 0; c < 4; ++c) {
           tmem_wait_ld(s[c & 1]);
           if (c < 3) tmem_ld32(s_at + 32 * (c + 1), s[(c + 1) & 1]);
+          // of the scores before their scale, whose sign is known
+          if (p.scale_log2 >= 0.f) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], s[c & 1][j] * p.scale_log2);
+            for (int j = 0; j < 32; j += 4) {
+              top[0] = fmaxf(top[0], fmaxf(s[c & 1][j], s[c & 1][j + 1]));
+              top[1] = fmaxf(top[1], fmaxf(s[c & 1][j + 2], s[c & 1][j + 3]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], -s[c & 1][j]);
+          }
         }
-        refer(fmaxf(top[0], top[1]));
+        refer(fmaxf(top[0], top[1]) * fabsf(p.scale_log2));
         tmem_ld32(s_at, s[0]);
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
 #pragma unroll
