@@ -62,6 +62,15 @@ __device__ __forceinline__ void turn(uint4& u0, uint4& u1, const float2* cs, int
 // One CTA per token.  Its last warp looks up the token's cache row and moves the
 // latent and the rotary key, the others the heads' rotary queries, whose loads go
 // out before the angles are known.
+//
+//   c = x w / sqrt(mean x^2 + eps),  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+//
+// Bound by the memory for long calls: a token's W + h rope_dim elements once each way,
+// and its row once more where the rows are wanted.  10,406 tokens of 64 heads, rank
+// 512, rotary 64, with rows: 40.0 us, 5.2 TB/s (floor 30.9 us at the measured copy
+// rate).  With the row after the queries in the same warps, whose look-ups the queries
+// then waited for: 46.5.  32 tokens: 3.1 us, the chain of look-ups (4.5 with the row in
+// the queries' warps).
 template <bool BF16, int LAYOUT>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendParams p) {
   __shared__ float2 s_cs[32];
