@@ -108,12 +108,9 @@ __device__ __forceinline__ void tma_load_pair_4d(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
-// The same into L2 only.
-__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
+// Contiguous memory into L2: both multiples of 16 bytes.
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
 }
 // sw128_desc with any distance between groups of 8 rows
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -377,8 +374,8 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
   uint32_t n = 0, it = 0;
   auto prefetch = [&](int page) {
     if (lane < C::kPages && page < p.tab.num_pages) {
-      tma_prefetch_l2_4d(&maps.v, 0, 0, (int)cta * C::kHalf, page);
-      tma_prefetch_l2_3d(&maps.rot, RANK, 8 * (int)cta, page);
+      const int elements = kPageSize * (RANK + p.rope_dim);   // of a page: the bytes of a half
+      prefetch_l2(p.pages + (int64_t)page * elements + (int)cta * (elements / 2), elements);
     }
     __syncwarp();
   };
@@ -395,8 +392,10 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
       const int page = next;
       next = after;
       // K has room for one tile, so the memory's latency would be in every tile's way:
-      // this CTA's half of the latents and of the rotary keys of the tile after the next
-      // go into L2 ahead of it
+      // the tile after the next goes into L2 ahead of it, of each page half by each CTA.
+      // (As boxes of columns, two per page: decode of 64 sequences 75.4 instead of 74.5
+      // us.  Three, four and six tiles ahead: 76.1, 77.4 and 85.0; trees 137 to 142
+      // instead of 134.)
       if (t + kAhead < x.t1) {
         after = page_of(p, x, t + kAhead, lane);
         prefetch(after);
@@ -1015,9 +1014,11 @@ __device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMe
 // Bound by latency: 5 to 8 us, of which reading the parts (at most 2 x 76 of 264 KB,
 // mostly in L2) would be 3 to 6.  All items'
 // units are shared out over one resident wave of CTAs: large units where there are
-// enough of them (each costs its loads' latency once), small ones where not.
+// enough of them (each costs its loads' latency once), small ones where not.  Small
+// units have 12 parts in flight: one sequence of 4,096 rows in 32 parts 13.0 us, with 8
+// 14.0; with 16, which spill, 12.8, but 64 sequences 78.6 instead of 75.3.
 template <int RANK, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) absorbed_merge_kernel(const LatentParams p, int pairs) {
+__global__ void __launch_bounds__(kMergeThreads, 2) absorbed_merge_kernel(const LatentParams p, int pairs) {
   __shared__ int s_at[kMaxPairs + 1];          // groups of 32 rows before each item
   __shared__ LatentMerge s_rec[kMaxPairs];
   __shared__ uint2 s_out[32][33];
@@ -1057,7 +1058,7 @@ __global__ void __launch_bounds__(kMergeThreads) absorbed_merge_kernel(const Lat
     if (large)
       merge_unit<RANK, BF16, 4, 4>(p, s_rec[pair], pair, row0, u % slices, s_out);
     else
-      merge_unit<RANK, BF16, 1, 8>(p, s_rec[pair], pair, row0, u % slices,
+      merge_unit<RANK, BF16, 1, 12>(p, s_rec[pair], pair, row0, u % slices,
                                    reinterpret_cast<uint2(*)[9]>(s_out));
   }
 }
