@@ -453,8 +453,10 @@ typedef struct {
 /* Bytes of device workspace each call on a latent cache needs (a multiple of
  * 256; 0 on invalid or unsupported dims).  tree_attn_cache_workspace_size's
  * rules apply: 256-byte aligned, zero-filled once, one workspace per set of
- * calls that may overlap on the GPU, any dims may take turns on one that is
- * large enough.  It holds the device status word, a mark per page of the pool and
+ * calls that may overlap on the GPU, latent caches of any dims may take turns on
+ * one that is large enough.  It is not a workspace for calls of the other sections,
+ * nor theirs one for these: what has to be zero between calls has another place
+ * (zero-filled again, it may change sides).  It holds the device status word, a mark per page of the pool and
  * the partial states of sequences that several SMs share. */
 size_t tree_attn_latent_workspace_size(const ta_latent_dims* dims);
 

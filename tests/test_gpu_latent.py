@@ -792,6 +792,18 @@ def test_one_workspace_for_several_caches():
     assert shared.device_status() == ta.TA_OK
 
 
+def test_workspaces_of_the_two_kinds_of_cache_are_kept_apart():
+    """What one keeps at zero lies where the other has its partial states."""
+    s = Setup([900, 3], 4, 256, 16)
+    table = [i32(x) for x in s.table]
+    pool = torch.zeros(s.pool.shape[0], 2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="kind of cache"):
+        ta.PagedCache(pool, *table, h_q=4, workspace=s.cache.workspace)
+    other = ta.PagedCache(pool, *table, h_q=4)
+    with pytest.raises(ValueError, match="kind of cache"):
+        ta.LatentCache(s.pool, *table, h_q=4, rank=256, workspace=other.workspace)
+
+
 # --------------------------------------------------------------------------
 # the ends of what is allowed
 # --------------------------------------------------------------------------

@@ -598,6 +598,10 @@ class _Cache:
             _check_dev("workspace", workspace)
             if workspace.get_device() != self._dev:
                 raise ValueError("workspace must be on the device of pages")
+            # the two kinds keep what has to be zero between calls in different places
+            if getattr(workspace, "_tree_attn_kind", self._size_name) != self._size_name:
+                raise ValueError("workspace is one of the other kind of cache "
+                                 f"({workspace._tree_attn_kind}, not {self._size_name})")
         if workspace is None or workspace.numel() * workspace.element_size() < need:
             # zero-filled once, before a call on any stream: the library keeps its
             # counters consistent afterwards.  While a graph is captured the filling
@@ -608,6 +612,7 @@ class _Cache:
                 self._binding.zero_now(workspace)
             else:
                 torch.cuda.current_stream(self._dev).synchronize()
+        workspace._tree_attn_kind = self._size_name
         self.workspace = workspace
         # the addresses of these tensors are what the calls pass, so they stay
         self._held = (pages, page_indptr, page_values, length_info, workspace)
@@ -741,7 +746,8 @@ class LatentCache(_Cache):
     latent elements and a rotary key per token, which all heads share.
 
     ``pages [num_pages, 16, rank + rope_dim]``, the table and the workspace are
-    held as ``PagedCache`` holds its own; everything said there holds here."""
+    held as ``PagedCache`` holds its own; everything said there holds here.  A
+    workspace may be another ``LatentCache``'s, but not a ``PagedCache``'s."""
 
     _prefix, _size_name = "latent_", "tree_attn_latent_workspace_size"
     _names = ("tree_attn_compact_latent", "tree_attn_copy_pages_latent")
