@@ -25,13 +25,13 @@
 //
 // Measured, bf16, rank 512, rotary 64 (the memory copies at 6.69 TB/s, the tensor
 // cores reach 1,947 TFLOP/s; the merge included): 4 sequences of 33,000 rows with 128
-// heads 51 us, floor 23 (memory) and 19 (tensor cores) at once; 64 sequences of 16 to
-// 16,384 rows with 64 heads 75.4 us, floor 37; draft trees of 64 nodes with 32 heads
-// behind 4 x 32,768 rows 441 us, 1,325 TFLOP/s.  A pair's products for a tile take
+// heads 50.1 us, floor 23 (memory) and 19 (tensor cores) at once; 64 sequences of 16 to
+// 16,384 rows with 64 heads 74.7 us, floor 37; draft trees of 64 nodes with 32 heads
+// behind 4 x 32,768 rows 435 us, 1,340 TFLOP/s.  A pair's products for a tile take
 // 2,500 cycles, its rows from memory 3,475 when all pairs read; for trees a tile takes
 // 2,500 to 2,900, for decode 2,650 with the rows at hand and some 4,700 on average over
 // a long call.  A call of few tiles is its start (4.3 us: tables, the first page's
-// look-up), the first loads (3 us), the parts' stores (3 us) and the merge (5 to 8 us).
+// look-up), the first loads (3 us), the parts' stores (3 us) and the merge (4 to 8 us).
 // Joining the parts in this kernel, pair by pair, took longer for few long sequences
 // (decode of one of 4,096 rows 14.5 -> 29.5 us) than the merge as a kernel of its own,
 // which all SMs share.
@@ -1011,7 +1011,7 @@ __device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMe
 
 // Joins the parts of the items that several pairs share, in their order:
 //   m = max m_i,  O = sum 2^(m_i - m) O_i,  l = sum 2^(m_i - m) l_i.
-// Bound by latency: 5 to 8 us, of which reading the parts (at most 2 x 76 of 264 KB,
+// Bound by latency: 4 to 8 us, of which reading the parts (at most 2 x 76 of 264 KB,
 // mostly in L2) would be 3 to 6.  All items'
 // units are shared out over one resident wave of CTAs: large units where there are
 // enough of them (each costs its loads' latency once), small ones where not.  Small
