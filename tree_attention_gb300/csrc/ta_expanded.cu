@@ -21,8 +21,8 @@
 // * One softmax thread per q row.
 //
 // Measured: prompts of 16 to 512 tokens, 64 sequences, 64 heads of 128 + 64, bf16:
-// 174 us on one GPU, 223 on another (floor 109, the memory); 2,000 tokens each of two
-// prompts with 14,000 held, 32 heads, fp16: 783 us, 1,216 TFLOP/s (floor 489, the
+// 172 us on one GPU, 229 on another (floor 109, the memory); 2,000 tokens each of two
+// prompts with 14,000 held, 32 heads, fp16: 775 us, 1,228 TFLOP/s (floor 489, the
 // tensor cores).  The latter are 512 units for 152 SMs, so four rounds for 3.4, and a
 // pair of tiles takes some 3,100 cycles of the 2,600 that its products need: a tile's
 // softmax and its products follow one another, and the softmax of one tile (some 1,850
@@ -382,9 +382,10 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
   Item x;
   using A = std::integral_constant<int, 0>;
   using B = std::integral_constant<int, 1>;
-  // S of tile w and load s, of its kv tiles the first or the last; both in line, with
-  // w known, as descriptors that are not the warp's constants cost 40 cycles a product
-  auto qk = [&](auto wc, int s, bool first, bool last) __attribute__((always_inline)) -> bool {
+  // S of tile w and load s, of its kv tiles the first or the last (done: no tile uses
+  // the load after this one); both in line, with w known, as descriptors that are not
+  // the warp's constants cost 40 cycles a product
+  auto qk = [&](auto wc, int s, bool first, bool last, bool done) __attribute__((always_inline)) -> bool {
     constexpr int w = decltype(wc)::value;
     const uint32_t g = it + s;
     if (first && !cx.wait(&m.q_full[w], units[w] & 1)) return false;
@@ -411,11 +412,12 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
                    k[C::kC] + 2 * i, idesc_qk, 1u);
       umma_commit(&m.s_full[w]);
       if (last) umma_commit(&m.q_empty[w]);
+      if (done) umma_commit(&m.k_empty[g & 1]);
     }
     __syncwarp();
     return true;
   };
-  auto do_pv = [&](auto wc, int s, bool first, bool last) __attribute__((always_inline)) -> bool {
+  auto do_pv = [&](auto wc, int s, bool first, bool last, bool done) __attribute__((always_inline)) -> bool {
     constexpr int w = decltype(wc)::value;
     const uint32_t g = it + s;
     if (!cx.wait(&m.p_full[w], pv[w] & 1)) return false;
@@ -443,13 +445,10 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
         if (i < steps) umma_f16_tmem_a(tmem + C::kTmemO + 128 * w, tmem + C::kTmemS + 128 * w + 8 * i,
                         v[i >> 2] + ((i & 3) * 2048 >> 4), idesc_pv, i > 0 ? 1u : (uint32_t)!first);
       if (last) umma_commit(&m.o_full[w]);
+      if (done) umma_commit(&m.v_empty[g & 1]);
     }
     __syncwarp();
     return true;
-  };
-  auto release = [&](uint64_t* bars, int s) {
-    if (elect_one()) umma_commit(&bars[(it + s) & 1]);
-    __syncwarp();
   };
   for (uint32_t n = 0; ok && next_item(cx, n, lane, x); ++n) {
     const int loads = x.loads(), step = x.heads, na = x.na, nb = x.nb;
@@ -457,20 +456,16 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
     for (int t = 0; ok; ++t) {
       const int sa = t * step, sb = sa + step - 1;
       if (t > 0 && t - 1 < na) {
-        if (!(ok = do_pv(A{}, sa - step, t == 1, t == na))) break;
-        if (step == 2 || t - 1 >= nb) release(m.v_empty, sa - step);
+        if (!(ok = do_pv(A{}, sa - step, t == 1, t == na, step == 2 || t - 1 >= nb))) break;
       }
       if (t < na) {
-        if (!(ok = qk(A{}, sa, t == 0, t == na - 1))) break;
-        if (step == 2 || t >= nb) release(m.k_empty, sa);
+        if (!(ok = qk(A{}, sa, t == 0, t == na - 1, step == 2 || t >= nb))) break;
       }
       if (t > 0 && t - 1 < nb) {
-        if (!(ok = do_pv(B{}, sb - step, t == 1, t == nb))) break;
-        release(m.v_empty, sb - step);
+        if (!(ok = do_pv(B{}, sb - step, t == 1, t == nb, true))) break;
       }
       if (t < nb) {
-        if (!(ok = qk(B{}, sb, t == 0, t == nb - 1))) break;
-        release(m.k_empty, sb);
+        if (!(ok = qk(B{}, sb, t == 0, t == nb - 1, true))) break;
       }
       if (t >= na && t >= nb) break;
     }
