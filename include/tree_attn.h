@@ -660,8 +660,10 @@ ta_status tree_attn_device_status(void* workspace, void* stream);
  *   stall          1: the MMA thread of every pipeline first waits on a
  *                  barrier that nothing arrives on, so that this wait runs
  *                  out after wait_limit_ns and every other warp then gives up
- *                  its own waits; 0: normal operation
- * Returns TA_ERR_INVALID_ARGUMENT for stall outside {0, 1}.  Not for
+ *                  its own waits; 0: normal operation; -1 - i: as 1, of the i-th
+ *                  pair of SMs of the kernel of tree_attn_decode_latent and
+ *                  tree_attn_latent alone
+ * Returns TA_ERR_INVALID_ARGUMENT for stall > 1.  Not for
  * production use: a stalled call computes nothing. */
 ta_status tree_attn_set_wait_hooks(uint64_t wait_limit_ns, int32_t stall);
 

@@ -929,3 +929,28 @@ def test_waits_that_run_out_are_reported():
         assert s.cache.device_status() == ta.TA_OK and ta.device_status(e.ws) == ta.TA_OK
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert torch.equal(egot[0], ewant[0]) and torch.equal(egot[1], ewant[1])
+
+
+def test_parts_of_an_earlier_call_are_not_joined():
+    """One pair of SMs gives up: a sequence with a part of its is left as it was,
+    not joined from the part that the call before left in the workspace; the
+    others' results are those of any call."""
+    # one tile of 128 rows for almost every pair, in order: pair 20 works on the
+    # first sequence, pair 60 on the second
+    s = Setup([4500, 4500], 16, 512, 64, seed=23)
+    q, before = s.randn(2, 16, s.w), s.randn(2, 16, s.w)
+    want = [t.clone() for t in s.cache.decode(q, 0.07)]
+    for pair, left in ((60, 1), (20, 0)):
+        s.cache.decode(before, 0.07)
+        out, lse = torch.full_like(want[0], 5), torch.full_like(want[1], 5)
+        ta.set_wait_hooks(20_000_000, -1 - pair)
+        try:
+            s.cache.decode(q, 0.07, out=out, lse=lse)
+            assert s.cache.device_status() == ta.TA_ERR_DEVICE_TIMEOUT
+        finally:
+            ta.set_wait_hooks(0, False)
+        assert (out[left] == 5).all() and (lse[left] == 5).all()
+        assert torch.equal(out[1 - left], want[0][1 - left]) and torch.equal(lse[1 - left], want[1][1 - left])
+        got = s.cache.decode(q, 0.07)
+        assert s.cache.device_status() == ta.TA_OK
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
@@ -447,11 +447,12 @@ def noalloc_device_status(stream=None) -> int:
     return int(lib().tree_attn_noalloc_device_status(_stream_ptr(stream)))
 
 
-def set_wait_hooks(wait_limit_ns: int = 0, stall: bool = False) -> None:
+def set_wait_hooks(wait_limit_ns: int = 0, stall: Union[bool, int] = False) -> None:
     """Test hook: the bounded-wait limit of later calls on this thread (0:
     the default) and whether their MMA threads first wait on a barrier that
-    nothing arrives on (so that the wait runs out)."""
-    st = lib().tree_attn_set_wait_hooks(int(wait_limit_ns), 1 if stall else 0)
+    nothing arrives on (so that the wait runs out); ``-1 - i``: only that of the
+    ``i``-th pair of SMs in ``LatentCache``'s attention."""
+    st = lib().tree_attn_set_wait_hooks(int(wait_limit_ns), stall if stall < 0 else int(bool(stall)))
     if st != TA_OK:
         raise TreeAttnError(st, "tree_attn_set_wait_hooks")
 

@@ -434,7 +434,7 @@ __device__ void run_v_producer(const Ctx& cx, const LatentParams& p, const Absor
 // The products: QK(t + 1) goes before PV(t), so that the softmax of one tile
 // runs beside the products of another.
 template <int RANK, bool BF16>
-__device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem, int lane) {
+__device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem, int pair, int lane) {
   using C = Cfg<RANK>;
   Misc& m = *cx.m;
   constexpr uint32_t idesc_qk = umma_idesc_f16(BF16, 128, 128, false);
@@ -447,7 +447,7 @@ __device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem, int
   uint32_t n = 0, it = 0, qt = 0;   // pieces, tiles whose PV, whose QK was issued
   const int rot_steps = p.rope_dim / 16;
   bool ok = true, issued = false;
-  if (p.debug_stall) ok = cx.wait_warp(&m.stall, 0);
+  if (p.debug_stall == 1 || p.debug_stall == -1 - pair) ok = cx.wait_warp(&m.stall, 0);
   auto qk = [&]() -> bool {
     const int b = qt & 1;
     if (!cx.wait_warp(&m.s_empty[b], ((qt >> 1) & 1) ^ 1)) return false;
@@ -898,21 +898,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       run_v_producer<RANK>(cx, p, maps, cta, lane);
     else if (warp == 10) {
-      if (cta == 0) run_mma<RANK, BF16>(cx, p, m.tmem, lane);
+      if (cta == 0) run_mma<RANK, BF16>(cx, p, m.tmem, pair, lane);
     } else if (lane == 0)
       run_planner(cx, p, split, pair, cta == 0);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  // after a wait ran out copies may still be on their way into shared memory, and
-  // there is nothing to join
+  // after a wait ran out copies may still be on their way into shared memory
   if (m.abort) {
-    if (tid == 0 && cta == 0) p.merge[pair] = LatentMerge{};
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
   }
   cluster_sync();   // neither CTA leaves while the other's products or arrivals may reach it
+  if (tid == 0) p.merge[pair].gave_up[cta] = m.abort;   // behind the pair's record
   if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(m.tmem) : "memory");
@@ -1026,7 +1025,16 @@ __global__ void __launch_bounds__(kMergeThreads, 2) absorbed_merge_kernel(const 
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < pairs) s_rec[tid] = p.merge[tid];
-  __syncthreads();
+  // after a wait ran out, items with a part of that pair's are left as they are
+  if (__syncthreads_or(tid < pairs && (s_rec[tid].gave_up[0] | s_rec[tid].gave_up[1]))) {
+    bool lost = false;
+    if (tid < pairs)
+      for (int i = tid; i < min(pairs, tid + s_rec[tid].parts); ++i)
+        lost |= s_rec[i].gave_up[0] | s_rec[i].gave_up[1];
+    __syncthreads();
+    if (lost) s_rec[tid].parts = 0;
+    __syncthreads();
+  }
   if (tid < 32) {
     int sum = 0;
     for (int base = 0; base < pairs; base += 32) {

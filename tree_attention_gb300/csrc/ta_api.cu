@@ -422,7 +422,7 @@ ta_status launch_run_checked(const void* q, const void* k, const void* v, const 
   ap.max_records = L.max_records;
   ap.scale_log2 = sm_scale * 1.4426950408889634f;
   ap.timeout_ns = wait_limit_ns();
-  ap.debug_stall = g_stall;
+  ap.debug_stall = g_stall > 0;
   ap.sched_clc = g_sched;
   ap.part_o = w.part_o;
   ap.part_lse = w.part_lse;
@@ -578,7 +578,7 @@ ta_status tree_attn_device_status(void* workspace, void* stream) {
 const char* tree_attn_last_cuda_error(void) { return cudaGetErrorString(g_last_cuda_error); }
 
 ta_status tree_attn_set_wait_hooks(uint64_t wait_limit_ns, int32_t stall) {
-  if (stall != 0 && stall != 1) return TA_ERR_INVALID_ARGUMENT;
+  if (stall > 1) return TA_ERR_INVALID_ARGUMENT;
   g_wait_limit_ns = wait_limit_ns;
   g_stall = stall;
   return TA_OK;
@@ -843,7 +843,7 @@ ta_status tree_attn_paged(const void* q, const int32_t* q_indptr, const void* pa
   ap.max_records = L.max_records;
   ap.scale_log2 = sm_scale * 1.4426950408889634f;
   ap.timeout_ns = wait_limit_ns();
-  ap.debug_stall = g_stall;
+  ap.debug_stall = g_stall > 0;
   ap.sched_clc = g_sched;
   ap.part_o = nullptr;
   ap.part_lse = nullptr;
@@ -1451,7 +1451,7 @@ ta_status tree_attn_expanded(const void* q, int64_t q_token_stride, int64_t q_he
   const int nsm = sm_count();
   if (nsm <= 0) return cuda_failure();
   p.timeout_ns = wait_limit_ns();
-  p.debug_stall = g_stall;
+  p.debug_stall = g_stall > 0;
   ta::ExpandedMaps maps;
   const int64_t h = dims->heads, nq = dims->total_q, nk = dims->total_kv, rd = dims->rope_dim;
   if (!make_tiled_map<3>(&maps.q, q, dims->dtype, {dq, h, nq}, {q_head_stride, q_token_stride},

@@ -244,14 +244,15 @@ struct LatentParams {
   struct LatentMerge* merge;              // [pairs of SMs]
   float* parts;                           // [pairs][2] states, see ta_absorbed.cu
   unsigned long long timeout_ns;
-  int debug_stall;                        // as in AttnParams
+  int debug_stall;                        // as in AttnParams; -1 - i: of pair i alone
 };
 
 // The item of 128 packed rows that begins in one pair's range of tiles and ends
 // in another's: packed rows row0 .. row0 + nrows - 1 (of its sequence b: m_row
-// on), in ``parts`` parts; 0: there is none.
+// on), in ``parts`` parts; 0: there is none.  gave_up: of the pair's CTAs, whether
+// a wait ran out in this call, so that its parts may be an earlier call's.
 struct LatentMerge {
-  int b, row0, m_row, nrows, parts, pad[3];
+  int b, row0, m_row, nrows, parts, gave_up[2], pad;
 };
 
 // Tensor maps of absorbed attention, all with 128-byte swizzle: q [rows * h, W] (box
