@@ -900,6 +900,25 @@ def test_streams_given_by_address():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_the_longest_sequence():
+    """2^31 - 16 rows, one page over and over: its 16 rows' attention.  A pair of SMs
+    adds its 220,753 tiles one after the other; every addition may lose 2^-23 of the
+    sum, one a tile for the sums of the weights, eight (of 16 rows) for the output."""
+    n = (1 << 27) - 1
+    g = torch.Generator("cuda").manual_seed(30)
+    pool = torch.randn((2, 16, 272), generator=g, device="cuda").bfloat16()
+    pool[1] = NAN
+    values = torch.zeros(n, dtype=torch.int32, device="cuda")
+    c = ta.LatentCache(pool, i32([0, n]), values, i32([16]), h_q=1, rank=256)
+    q = torch.randn((1, 1, 272), generator=g, device="cuda").bfloat16()
+    out, lse = c.decode(q, 0.07, out=torch.full((1, 1, 256), NAN, dtype=torch.bfloat16, device="cuda"))
+    assert c.device_status() == ta.TA_OK
+    ro, rl, mag, _ = ref.absorbed(q.double(), pool.double(), ([0, 1], [0], [16]), 256, 0.07)
+    lost = -(-n // 8 // 76) * 2.0 ** -23
+    assert ((out.double() - ro).abs() <= 9 * lost * mag + 2.0 ** -7 * mag).all()
+    assert (lse.double() - rl - math.log2(n)).abs().max() <= -math.log2(1 - lost) + 2.0 ** -10
+
+
 # --------------------------------------------------------------------------
 # a wait that runs out
 # --------------------------------------------------------------------------

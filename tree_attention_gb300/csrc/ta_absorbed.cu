@@ -239,10 +239,10 @@ struct Split {
   }
 };
 
-__device__ __forceinline__ int tiles_of(const LatentSeq& s) { return (s.kv + kTile - 1) / kTile; }
-__device__ __forceinline__ int items_of(const LatentSeq& s, int h) {
-  return (s.qo * h + kTile - 1) / kTile;
-}
+// Rounded up without passing 2^31: a sequence may have 2^31 - 16 rows.
+__device__ __forceinline__ int tiles(int n) { return n / kTile + (n % kTile != 0); }
+__device__ __forceinline__ int tiles_of(const LatentSeq& s) { return tiles(s.kv); }
+__device__ __forceinline__ int items_of(const LatentSeq& s, int h) { return tiles(s.qo * h); }
 
 // ---------------------------------------------------------------------------
 // roles
@@ -612,7 +612,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       const int b = it & 1;
       // this thread's kv rows: of four pages the 8 that its half of the lanes has
       const int tok = t * kTile + wg * 64 + (lane >> 3) * kPageSize + half * 8 + (lane & 7);
-      const bool masked = (t + 1) * kTile > x.start;
+      const bool masked = t * kTile > x.start - kTile;
       int2 iv = make_int2(INT32_MIN, INT32_MAX);
       if (masked && work) {
         if (tok >= x.kv)
