@@ -71,13 +71,13 @@ __device__ __forceinline__ uint32_t in_first_cta(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
-// Arrives on a barrier of the pair's first CTA, releasing to this CTA only: what
-// the arrivals here announce is this CTA's own shared memory, behind a proxy fence,
-// and tensor memory, which this SM's own units read.  (A release to the cluster
-// waits for all that its thread has under way, 1,000 to 4,000 cycles a time: with it
-// a tile took 6,500 cycles, whoever executed it.)
+// Arrives on a barrier of the pair's first CTA, releasing this CTA's shared memory to
+// the cluster, which is what the arrivals here announce (tensor memory has fences of
+// its own).  (A release of all memory waits for all that its thread has under way,
+// 1,000 to 4,000 cycles a time: with it a tile took 6,500 cycles.)
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
