@@ -352,6 +352,56 @@ def test_tree_rows_that_others_see_may_hold_anything(h, dtype):
     assert free.sum() > 60 and base is not None
 
 
+def milliseconds(f, n=5):
+    """The median of ``n`` calls, timed on the GPU."""
+    e = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in range(n)]
+    f()
+    for a, b in e:
+        a.record()
+        f()
+        b.record()
+    torch.cuda.synchronize()
+    return sorted(a.elapsed_time(b) for a, b in e)[n // 2]
+
+
+@pytest.mark.parametrize("h,rank,dtype", [(1, 512, "bf16"), (8, 512, "fp16"), (24, 256, "bf16")])
+def test_rows_not_seen_have_no_part_behind_long_prefixes(h, rank, dtype):
+    """Draft rows that are not finite, in columns of either SM's half, behind 40,000
+    rows: for the nodes that do not see them not a bit differs from a call without
+    them, nor does the call take longer by more than a look at some tiles' values
+    (a second pass over 40,000 rows would)."""
+    spec = [(40000, 64, 64, "star"), (33000, 40, 40, "random")]
+    t = Trees(spec, h, rank, 64, dtype, seed=6)
+    base = [x.clone() for x in t.run(0.07)]
+    quick = milliseconds(lambda: t.run(0.07))
+    touched = torch.zeros(104, dtype=torch.bool, device="cuda")
+    at = 0
+    for b, (prefix, n, _, _) in enumerate(spec):
+        pid, sl = t.s.slots(b)
+        for i, c, x in ((n - 1, 5, NAN), (n - 2, rank - 1, INF), (n // 2, rank // 2 + 3, -INF),
+                        (n // 3, rank + 9, NAN), (n // 4, slice(None), NAN)):
+            t.s.pool[pid[prefix + i], sl[prefix + i], c] = x
+            for j in range(n):
+                k = j
+                while k > i:
+                    k = int(t.parents[b][k])
+                touched[at + j] |= k == i
+        at += n
+    out, lse = t.run(0.07)
+    assert t.s.cache.device_status() == ta.TA_OK
+    free = ~touched
+    assert free.sum() > 60
+    assert torch.equal(out[free], base[0][free]) and torch.equal(lse[free], base[1][free])
+    assert milliseconds(lambda: t.run(0.07)) < 2 * quick
+    # of the others, those whose scores are -inf there (a column of one sign) are as
+    # if the row were not there, all else is NaN
+    want = ref.absorbed(t.q.double(), t.s.pool.double(), t.s.table, rank, 0.07, t.rows, t.parents)
+    nan = torch.isnan(want[0]).any(-1)
+    assert torch.equal(torch.isnan(out).all(-1), nan) and torch.equal(torch.isnan(out).any(-1), nan)
+    assert torch.equal(torch.isnan(lse), nan)
+    check(t.s.dtype, t.s.w, 40000, 6.0, out[~nan], lse[~nan], [x[~nan] for x in want])
+
+
 def test_tree_is_decode_for_single_nodes():
     kv = [5, 130, 1, 2000, 16]
     s = Setup(kv, 24, 512, 64, seed=6)

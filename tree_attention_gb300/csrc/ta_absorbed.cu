@@ -19,6 +19,8 @@
 // * The tiles of all (sequence, 128 packed rows) in order are cut into equal
 //   ranges, one per pair of SMs; a range's first and last item may be parts,
 //   whose float32 states a second kernel merges.
+// * What is not finite in a row that does not count never meets its weight of zero:
+//   the rows' scores tell (see run_softmax), and such values are zeroed first.
 // * Roles: 8 warps of softmax, one that loads Q and K, one that loads V, one that
 //   issues the products (of the pair's first CTA), one that walks the tables ahead
 //   of all others.
@@ -173,7 +175,7 @@ struct Cfg {
 // An item's part that one pair works on: kv tiles t0 .. t1 - 1 of one
 // sequence, for packed rows from m_row on (nrows of them exist).
 struct Piece {
-  int b, p0, kv, start, m0, node0;   // start: of the tree's rows; node0: the first q row's node
+  int p0, kv, start, m0, node0;      // start: of the tree's rows; node0: the first q row's node
   int row0, m_row, nrows;            // row0: global packed row of m_row
   int t0, t1, slot;                  // t0 == t1: no more; slot -1: the whole item, else 0 or 1
 };
@@ -276,7 +278,6 @@ __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& s
         continue;
       }
       const int item = off / kt;
-      x.b = b;
       x.p0 = s.p0;
       x.kv = s.kv;
       x.start = s.kv - s.tree;
@@ -290,9 +291,7 @@ __device__ void run_planner(const Ctx& cx, const LatentParams& p, const Split& s
       x.slot = x.t0 == 0 && x.t1 == kt ? -1 : x.t0 == 0;
       if (x.slot == 1) {
         const int last = base + (item + 1) * kt - 1;
-        merge.b = b;
         merge.row0 = x.row0;
-        merge.m_row = x.m_row;
         merge.nrows = x.nrows;
         merge.parts = split.pair_of(last) - pair + 1;
       }
@@ -534,12 +533,12 @@ __device__ void run_mma(const Ctx& cx, const LatentParams& p, uint32_t tmem, int
 }
 
 // The exponent that a weight may reach over its reference, and where a moved
-// reference puts the largest: fp16 weights are held 2^7 higher than bf16 ones,
-// as what lies 2^-24 below a weight of one is the type's end and long sequences
-// have mass there.
+// reference puts the largest.  fp16 weights are held high, as what lies 2^-24 below
+// a weight of one is the type's end and long sequences have mass there; bf16 ones
+// are at most one, as values may be near the end of float32's range.
 template <bool BF16>
 struct Ref {
-  static constexpr float kTop = BF16 ? 8.f : 15.f, kPut = BF16 ? 0.f : 7.f;
+  static constexpr float kTop = BF16 ? 0.f : 15.f, kPut = BF16 ? -8.f : 7.f;
 };
 
 // O of this thread's lane and columns times f.
@@ -557,6 +556,31 @@ __device__ __noinline__ void rescale(uint32_t o, float f) {
   tmem_wait_st();
 }
 
+// The elements of this CTA's values that are infinite or NaN made zero, in the rows
+// of a tile that are set in ``rows``: eight of each of four pages from page0 on, row0
+// their first.  By a whole warp.
+template <int RANK, bool BF16>
+__device__ __noinline__ void clear_values(uint8_t* sv, uint32_t rows, int page0, int row0, int lane) {
+  using C = Cfg<RANK>;
+  constexpr uint32_t kEnd = BF16 ? 0x7f80u : 0x7c00u;   // the exponent of what is not finite
+  auto cleared = [](uint32_t w) {
+    if ((w & kEnd) == kEnd) w &= 0xffff0000u;
+    if ((w >> 16 & kEnd) == kEnd) w &= 0xffffu;
+    return w;
+  };
+  while (rows) {
+    const int j = __ffs(rows) - 1;
+    rows &= rows - 1;
+    uint8_t* row = sv + (page0 + (j >> 3)) * C::kVBox + (row0 + (j & 7)) * 128;
+    for (int i = lane; i < C::kHalf * 8; i += 32) {
+      uint4* at = reinterpret_cast<uint4*>(row + (i >> 3) * kPageSize * 128 + (i & 7) * 16);
+      const uint4 u = *at;
+      *at = make_uint4(cleared(u.x), cleared(u.y), cleared(u.z), cleared(u.w));
+    }
+  }
+  fence_proxy_async_smem();
+}
+
 template <int RANK, bool BF16>
 __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem, uint32_t cta,
                             int pair, int warp, int lane) {
@@ -566,6 +590,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
   const int half = quarter >> 1;                 // of every page's rows, of the latent's columns
   const int rr = (quarter & 1) * 32 + lane;      // packed row of this CTA's 64
   const int part = half * 2 + wg;                // of the row's four threads
+  const bool checks = (quarter & 1) == 0;        // this warp's kv rows, for both of their warps
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const uint32_t o_at = tmem + lanes + C::kTmemO + wg * C::kCols;
   uint8_t* p_row = cx.smem + C::kOffP + wg * kChunkBytes + rr * 128;
@@ -610,7 +635,8 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
     float ref = -FLT_MAX, l = 0.f, lr = 0.f;
     for (int t = x.t0; t < x.t1; ++t, ++it) {
       const int b = it & 1;
-      // this thread's kv rows: of four pages the 8 that its half of the lanes has
+      // this warp's kv rows: of four pages the 8 that its half of the lanes has; the
+      // j-th score is of lane j's
       const int tok = t * kTile + wg * 64 + (lane >> 3) * kPageSize + half * 8 + (lane & 7);
       const bool masked = t * kTile > x.start - kTile;
       int2 iv = make_int2(INT32_MIN, INT32_MAX);
@@ -623,13 +649,36 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
       if (!cx.wait_warp(&m.s_full[b], (it >> 1) & 1)) return;
       tc_fence_after();
       float s[32];
-      if (work) {
+      if (work || checks) {
         tmem_ld32(tmem + lanes + C::kTmemS + 64 * b + 32 * wg, s);
         tmem_wait_ld(s);
         tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) arrive_remote(in_first_cta(&m.s_empty[b]));
+      // A weight of zero times a value that is not finite is NaN.  Such a value is an
+      // element of its key too, so its scores are not finite, whatever the query (an
+      // infinity times zero is NaN): for a q row that sees it the score is -inf and it
+      // does not count, or the result is NaN whatever the values are.  For all rows
+      // the value may be zero, so where all 32 scores of a kv row are not finite, its
+      // values are looked through before their product.
+      if (checks) {
+        const float2 zero = make_float2(0.f, 0.f);
+        float2 odd2 = zero;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) odd2 = ffma2(make_float2(s[j], s[j + 1]), zero, odd2);
+        if (__all_sync(0xffffffffu, odd2.x + odd2.y != 0.f)) {
+          uint32_t rows = 0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            rows |= (uint32_t)(__all_sync(0xffffffffu, !(fabsf(s[j]) < INFINITY)) != 0) << j;
+          rows &= __ballot_sync(0xffffffffu, tok < x.kv);   // the others are zeroed already
+          if (rows) {
+            if (!cx.wait_warp(&m.v_full[wg], it & 1)) return;
+            clear_values<RANK, BF16>(cx.smem + C::kOffV, rows, 4 * wg, 8 * half, lane);
+          }
+        }
+      }
       if (work) {
         // the largest of the scores, times their scale afterwards, whose sign is known;
         // what does not count is made the least there is
@@ -718,7 +767,6 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
         const int four = lane & ~3;              // the rows whose vectors this lane stores
         uint16_t* out = p.out + (at - lane + four) * RANK + col0 + (lane & 3) * 8;
         const float2 zero = make_float2(0.f, 0.f), by = make_float2(inv, inv);
-        float2 odd2 = zero;
 #pragma unroll 1
         for (int c = 0; c < C::kCols; c += 32) {
           float v[32];
@@ -730,9 +778,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 o = make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-              odd2 = ffma2(o, zero, odd2);
-              const float2 z = ffma2(o, by, zero);
+              const float2 z = ffma2(make_float2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]), by, zero);
               w[k] = pack2<BF16>(z.x, z.y);
             }
             y[i] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -742,17 +788,7 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
           for (int j = 0; j < 4; ++j)
             if (row - lane + four + j < x.nrows) *reinterpret_cast<uint4*>(out + j * RANK + c) = y[j];
         }
-        const float odd = odd2.x + odd2.y;
         if (valid && part == 0) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
-        // a value that is not finite, though the weights are: it may be one that does not count
-        unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
-        while (again) {
-          const int i = __ffs(again) - 1;
-          again &= again - 1;
-          const int r = x.m_row + 64 * (int)cta + (quarter & 1) * 32 + i;
-          __syncwarp();
-          latent_row_exact<BF16>(p, x.b, r / p.h, r % p.h, col0, col0 + C::kCols);
-        }
       } else {
         float* st = p.parts + (int64_t)(2 * pair + x.slot) * kSlotFloats;
         float4* o = reinterpret_cast<float4*>(st) + (col0 / 4) * kTile + row;
@@ -979,14 +1015,11 @@ __device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMe
     }
   }
   const float inv = lr == 0.f ? 0.f : 1.f / lr;
-  float odd = 0.f;
   __syncthreads();                             // s_out is read from the unit before
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    odd += (o[j].x + o[j].y) * 0.f + (o[j].z + o[j].w) * 0.f;
+  for (int j = 0; j < V; ++j)
     s_out[lane][warp * V + j] =
         make_uint2(pack2<BF16>(o[j].x * inv, o[j].y * inv), pack2<BF16>(o[j].z * inv, o[j].w * inv));
-  }
   const int64_t first = (int64_t)r.row0 + row0;
   if (warp == 0 && slice == 0 && valid) p.lse[first + lane] = l == 0.f ? -INFINITY : top + log2f(l);
   __syncthreads();
@@ -996,15 +1029,6 @@ __device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMe
     const int i = tid + j * kMergeThreads, orow = i / (8 * V), c = i % (8 * V);
     if (row0 + orow < r.nrows)
       *reinterpret_cast<uint2*>(p.out + (first + orow) * RANK + (slice * 8 * V + c) * 4) = s_out[orow][c];
-  }
-  // a value that is not finite, though the weights are: it may be one that does not count
-  const unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
-  if (__syncthreads_or(again != 0)) {
-    for (int i = 0; i < 32; ++i) {
-      if (!(again >> i & 1)) continue;
-      const int x = r.m_row + row0 + i, e0 = ((slice * 8 + warp) * V * 4) & ~7;
-      latent_row_exact<BF16>(p, r.b, x / p.h, x % p.h, e0, e0 + (V > 1 ? 4 * V : 8));
-    }
   }
 }
 

@@ -248,11 +248,11 @@ struct LatentParams {
 };
 
 // The item of 128 packed rows that begins in one pair's range of tiles and ends
-// in another's: packed rows row0 .. row0 + nrows - 1 (of its sequence b: m_row
-// on), in ``parts`` parts; 0: there is none.  gave_up: of the pair's CTAs, whether
+// in another's: packed rows row0 .. row0 + nrows - 1, in ``parts`` parts; 0: there
+// is none.  gave_up: of the pair's CTAs, whether
 // a wait ran out in this call, so that its parts may be an earlier call's.
 struct LatentMerge {
-  int b, row0, m_row, nrows, parts, gave_up[2], pad;
+  int row0, nrows, parts, gave_up[2], pad[3];
 };
 
 // Tensor maps of absorbed attention, all with 128-byte swizzle: q [rows * h, W] (box
