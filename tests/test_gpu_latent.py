@@ -870,6 +870,34 @@ def test_scales_of_zero_and_below(sm):
     e.check(out, lse, sm)
 
 
+def test_a_scale_of_zero_weighs_large_rows_as_any_other():
+    """Products near the end of float32's range times zero are zero; an infinite one
+    is NaN, for the rows that see it."""
+    s = Setup([200, 40, 30], 5, 256, 64, seed=24)
+    q = s.randn(3, 5, s.w)
+    q[:, :, 256] = 1.5e19
+    pid, sl = s.slots(0)
+    s.pool[pid, sl, 256] = torch.where(torch.arange(200, device="cuda") % 2 == 0, 1.5e19, 0.0).to(s.dtype)
+    pid, sl = s.slots(1)
+    s.pool[pid[17], sl[17], 256] = -INF
+    out, lse = s.cache.decode(q, 0.0)
+    nan = torch.zeros((3, 5), dtype=torch.bool, device="cuda")
+    nan[1] = True
+    assert torch.equal(torch.isnan(out).all(-1), nan) and torch.equal(torch.isnan(lse), nan)
+    want = [t[~nan] for t in ref.absorbed(q.double(), s.pool.double(), s.table, 256, 0.0)]
+    assert (want[1] - torch.log2(torch.tensor([200.0, 30.0], device="cuda")).repeat_interleave(5)).abs().max() < 1e-6
+    check(s.dtype, s.w, 200, 6.0, out[~nan], lse[~nan], want)
+    # a tree's nodes do not see one another's branches at any scale
+    t = Trees([(20, 12, 12, "star")], 5, 256, 64, "bf16", seed=25)
+    pid, sl = t.s.slots(0)
+    t.s.pool[pid[30], sl[30], 7] = INF
+    out, lse = t.run(0.0)
+    keep = torch.arange(12, device="cuda") != 10
+    assert torch.isnan(out[10]).all() and torch.isnan(lse[10]).all()
+    want = ref.absorbed(t.q.double(), t.s.pool.double(), t.s.table, 256, 0.0, t.rows, t.parents)
+    check(t.s.dtype, t.s.w, 32, 6.0, out[keep], lse[keep], [x[keep] for x in want])
+
+
 def test_expanded_rows_head_by_head():
     """Queries, keys and values laid out with the heads outside the tokens."""
     e = Expanded([70, 130], [200, 130], 5, 128, 48, "fp16", seed=14)

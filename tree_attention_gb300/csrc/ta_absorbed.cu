@@ -614,9 +614,10 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
     if (x.start >= x.kv || row >= x.nrows) return 0;
     return reinterpret_cast<const int2*>(p.tree_order)[x.m0 + x.node0 + (x.m_row + row) / p.h].x;
   };
-  // a scale of nothing is made one that leaves a score below 2^-20: times the infinity
-  // of what does not count it stays infinite
-  const float scale = p.scale_log2 == 0.f ? 1e-40f : p.scale_log2;
+  // a scale of zero goes into the scores before those that do not count are made
+  // infinite, which it would make NaN
+  const bool flat = p.scale_log2 == 0.f;
+  const float scale = flat ? 1.f : p.scale_log2;
   const float2 scale2 = make_float2(scale, scale);
   int enter_next = 0;
   for (;; ++n) {
@@ -683,6 +684,10 @@ __device__ void run_softmax(const Ctx& cx, const LatentParams& p, uint32_t tmem,
         // the largest of the scores, times their scale afterwards, whose sign is known;
         // what does not count is made the least there is
         const float least = scale > 0.f ? -INFINITY : INFINITY;
+        if (flat) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] *= 0.f;
+        }
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
