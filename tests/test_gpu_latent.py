@@ -666,6 +666,74 @@ def test_expanded_rows_not_seen_may_hold_anything(dtype):
     assert torch.isnan(out[~free]).any(-1).all()
 
 
+def check_expanded_with_odd_values(e, out, lse, sm):
+    """Element by element: NaN and infinities where the reference has them, its
+    numbers elsewhere."""
+    want = ref.expanded(e.q.double(), e.k.double(), e.kr.double(), e.v.double(), e.new, e.kv, sm)
+    fin = torch.isfinite(want[0])
+    assert torch.equal(torch.isfinite(out), fin)
+    assert torch.equal(torch.nan_to_num(out[~fin].double(), nan=7.0, posinf=8.0, neginf=9.0),
+                       torch.nan_to_num(want[0][~fin], nan=7.0, posinf=8.0, neginf=9.0))
+    zero = lambda x: torch.where(fin, x, 0.0)
+    check(e.dtype, e.d + e.rope, max(e.kv), 6.0, zero(out.double()), lse, [zero(want[0]), *want[1:]])
+    return fin
+
+
+@pytest.mark.parametrize("h,d,rope,dtype", [(3, 128, 64, "bf16"), (5, 64, 32, "fp16")])
+def test_expanded_rows_not_seen_have_no_part_behind_long_prefixes(h, d, rope, dtype):
+    """Values that are not finite among the last rows of long sequences: for the q
+    rows that do not see them not a bit differs from a call without them; a second
+    look at all units is the most that they cost."""
+    new, kv = [300, 64, 150, 20], [40300, 33064, 150, 90]
+    e = Expanded(new, kv, h, d, rope, dtype, seed=30)
+    base = [x.clone() for x in e.run(0.07)]
+    quick = milliseconds(lambda: e.run(0.07))
+    first, seen_from = 0, torch.full((sum(new),), -1, device="cuda")
+    at = 0
+    for n, m in zip(new, kv):
+        odd = [(m - 1, slice(None), NAN), (m - 5, d - 1, INF), (m - 17, 0, -INF), (m - n // 2, 7, NAN)]
+        for j, c, x in odd:
+            e.v[first + j, :, c] = x
+        seen_from[at:at + n] = min(j for j, _, _ in odd) - (m - n)
+        first, at = first + m, at + n
+    own = torch.cat([torch.arange(n, device="cuda") for n in new])
+    free = own < seen_from
+    out, lse = e.run(0.07, out=torch.zeros_like(e.out), lse=torch.zeros_like(e.lse))
+    assert ta.device_status(e.ws) == ta.TA_OK
+    assert free.sum() > 200
+    assert torch.equal(out[free], base[0][free]) and torch.equal(lse, base[1])
+    assert milliseconds(lambda: e.run(0.07)) < 4 * quick
+    fin = check_expanded_with_odd_values(e, out, lse, 0.07)
+    assert (~fin).any() and torch.equal(out[fin], base[0][fin])
+
+
+@pytest.mark.parametrize("name", ["edges", "chunks", "empties", "many_short", "one_head_long"])
+def test_expanded_values_that_are_not_finite(name):
+    """Infinities and NaN all over the values, seen and not; with keys whose score is
+    -inf, whose rows count as if they were not there."""
+    e = Expanded(*EXPANDED[name], seed=31)
+    g = torch.Generator("cuda").manual_seed(5)
+    nk = sum(e.kv)
+    pick = lambda share: torch.rand(e.v.shape, generator=g, device="cuda") < share
+    e.v[pick(0.0007)] = NAN
+    e.v[pick(0.0007)] = INF
+    e.v[pick(0.0007)] = -INF
+    e.q[:, :, 1] = e.q[:, :, 1].abs() + 0.1
+    gone = torch.rand(nk, generator=g, device="cuda") < 0.1
+    e.k[gone, :, 1] = -INF
+    e.v[gone, :, :3] = NAN
+    out, lse = e.run(0.07)
+    assert ta.device_status(e.ws) == ta.TA_OK
+    check_expanded_with_odd_values(e, out, lse, 0.07)
+    again = e.run(0.07, out=torch.zeros_like(out), lse=torch.zeros_like(lse))
+    assert torch.equal(torch.nan_to_num(out, nan=7.0), torch.nan_to_num(again[0], nan=7.0))
+    # all of them, for one sequence after the other
+    e.v[:] = NAN
+    out, lse = e.run(0.07)
+    assert ta.device_status(e.ws) == ta.TA_OK
+    check_expanded_with_odd_values(e, out, lse, 0.07)
+
+
 def test_expanded_spare_rows_are_left_alone():
     """Buffers longer than the batch: behind the last sequence nothing is read or
     written.  (The totals are the batch's, the tensors views.)"""

@@ -19,6 +19,10 @@
 //   halves of 64 rows) pass through one ring of eight 16 KB slots, so that a tile's
 //   values arrive where the tile before had its keys.
 // * One softmax thread per q row.
+// * Masked value rows meet weights of zero in the products.  Where that, or an
+//   infinity, left a result that is not finite, the CTA goes over its units a second
+//   time, carefully: values that are not finite are zeroed before the products, and
+//   the softmax threads add what the rows that see them get.
 //
 // Measured: prompts of 16 to 512 tokens, 64 sequences, 64 heads of 128 + 64, bf16:
 // 172 us on one GPU, 229 on another (floor 109, the memory); 2,000 tokens each of two
@@ -64,12 +68,21 @@ struct Item {
   __device__ __forceinline__ int q_rows(int w) const { return min(kTile, nq - w * (2 - heads) * kTile); }
 };
 
+// How far a warp has come: what it counts of records, kv tiles loaded, and uses of
+// barriers, kept from the first pass over the units for the second (the cleaner's
+// are what others count from while it runs).
+struct Counts {
+  uint32_t n, it, use[4][2];
+};
+
 struct Misc {
   uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t v_short[2], v_clean[2];   // a sequence's last tile, which is cleaned before use
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2], item_full[kItems], item_empty[kItems];
   uint64_t stall, drain;
   Item item[kItems];
+  uint32_t odd_rows[2][4];           // of a kv tile: rows with values that are not finite
+  Counts counts[kThreads / 32];
   uint32_t tmem;
   int abort;
 };
@@ -126,57 +139,6 @@ __device__ __forceinline__ bool good_sequence(const ExpandedParams& p, int b) {
          (b < p.batch - 1 || (q1 == p.total_q && k1 == p.total_kv));
 }
 
-// One q row and head by one warp, kv row by kv row; a lane holds D / 32 elements
-// of a head's part and 2 of the rotary part (lanes below rope_dim / 2).  For rows in
-// which the matrix products met a value that is not finite in a row not seen.
-template <int D, bool BF16>
-__device__ __noinline__ void row_exact(const ExpandedParams& p, int b, int row, int h) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 31;
-  const int k0 = p.kv_indptr[b];
-  const int n = p.kv_indptr[b + 1] - k0 - (p.q_indptr[b + 1] - row) + 1;   // rows it sees
-  const uint32_t* qp = reinterpret_cast<const uint32_t*>(p.q + row * p.q_ts + h * p.q_hs);
-  const bool rot = lane < p.rope_dim / 2;
-  float2 q[E], qr = unpack2<BF16>(rot ? qp[D / 2 + lane] : 0u), o[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = unpack2<BF16>(qp[lane + 32 * i]);
-    o[i] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-  for (int j = 0; j < n; ++j) {
-    const int64_t at = k0 + j;
-    const uint32_t* kp = reinterpret_cast<const uint32_t*>(p.k + at * p.k_ts + h * p.k_hs);
-    const uint32_t* rp = reinterpret_cast<const uint32_t*>(p.k_rope + at * p.kr_ts);
-    const uint32_t* vp = reinterpret_cast<const uint32_t*>(p.v + at * p.v_ts + h * p.v_hs);
-    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc = ffma2(q[i], unpack2<BF16>(kp[lane + 32 * i]), acc);
-    if (rot) acc = ffma2(qr, unpack2<BF16>(rp[lane]), acc);
-    float s = acc.x + acc.y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale_log2;
-    if (s == -INFINITY) continue;
-    if (s > m) {
-      const float f = ex2_approx(m - s);
-      m = s;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = make_float2(o[i].x * f, o[i].y * f);
-    }
-    const float w = ex2_approx(s - m);
-    l += w;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = ffma2(make_float2(w, w), unpack2<BF16>(vp[lane + 32 * i]), o[i]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((int64_t)row * p.h + h) * D);
-#pragma unroll
-  for (int i = 0; i < E; ++i) out[lane + 32 * i] = pack2<BF16>(o[i].x * inv, o[i].y * inv);
-}
-
 // ---------------------------------------------------------------------------
 // roles
 // ---------------------------------------------------------------------------
@@ -194,7 +156,7 @@ __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) 
   long long u = blockIdx.x, base = 0;
   int b0 = -32, q0 = 0, qo = 0, k0 = 0, kv = 0;
   long long before = 0, units = 0, total = 0;
-  for (uint32_t n = 0;; ++n) {
+  for (uint32_t n = m.counts[11].n;; ++n) {
     while (u >= base + total && b0 + 32 < p.batch) {
       base += total;
       b0 += 32;
@@ -255,6 +217,7 @@ __device__ void run_scheduler(const Ctx& cx, const ExpandedParams& p, int lane) 
       if (lane == 0) {
         m.item[slot] = x;
         mbar_arrive(&m.item_full[slot]);
+        m.counts[11].n = n + 1;
       }
       return;
     }
@@ -271,13 +234,14 @@ __device__ __forceinline__ bool next_item(const Ctx& cx, uint32_t n, int lane, I
   return x.na > 0;
 }
 
-template <int D>
-__device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) {
+template <int D, bool CAREFUL>
+__device__ __forceinline__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) {
   using C = Cfg<D>;
   Misc& m = *cx.m;
-  uint32_t it = 0, chunk = 0, units[2] = {0, 0};
+  Counts& kept = m.counts[8];
+  uint32_t n = kept.n, it = kept.it, chunk = kept.use[0][0], units[2] = {kept.use[1][0], kept.use[1][1]};
   Item x;
-  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
+  for (; next_item(cx, n, lane, x); ++n) {
     auto load_q = [&](int tile) {
       if (!cx.wait(&m.q_empty[tile], (units[tile] & 1) ^ 1)) return false;
       ++units[tile];
@@ -307,7 +271,7 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
     const int loads = x.loads();
     for (int t = 0; t < loads; ++t, ++it) {
       const int row = x.kv0 + x.tile(t) * kTile, s = it & 1, head = x.head + (t & (x.heads - 1));
-      uint64_t* v_bar = x.is_short(t) ? &m.v_short[s] : &m.v_full[s];
+      uint64_t* v_bar = CAREFUL || x.is_short(t) ? &m.v_short[s] : &m.v_full[s];
       const int boxes = x.rows(t) > 64 ? 2 : 1;
       for (int c = 0; c <= C::kC; ++c) {
         uint8_t* to = slot();
@@ -335,37 +299,101 @@ __device__ void run_producer(const Ctx& cx, const ExpandedMaps& maps, int lane) 
       }
     }
   }
+  if (!CAREFUL && lane == 0) kept = Counts{n + 1, it, {{chunk, 0}, {units[0], units[1]}}};
 }
 
+// sum + 0 times eight elements: NaN where one is infinite or NaN.
+template <bool BF16>
+__device__ __forceinline__ void add_zero_times(uint32_t& sum, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if constexpr (BF16)
+      asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[i]), "r"(0u));
+    else
+      asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[i]), "r"(0u));
+}
+__device__ __forceinline__ bool has_nan(uint32_t sum) { return (sum & 0x7fff7fffu) != 0; }
+
 // Zeroes the value rows behind a sequence's last, up to the 16 of a product: what
-// does not count must not reach the products as NaN.
-template <int D>
-__device__ void run_cleaner(const Ctx& cx, int lane) {
+// does not count must not reach the products as NaN.  CAREFUL: of every tile also the
+// values that are not finite, whose rows it notes.
+template <int D, bool BF16, bool CAREFUL>
+__device__ __forceinline__ void run_cleaner(const Ctx& cx, int lane) {
   using C = Cfg<D>;
+  constexpr uint32_t kEnd = BF16 ? 0x7f80u : 0x7c00u;   // the exponent of what is not finite
+  constexpr int kVecs = C::kC * 8;                      // of a row
   Misc& m = *cx.m;
-  uint32_t it = 0, count[2] = {0, 0};
+  Counts& kept = m.counts[10];
+  uint32_t n = kept.n, it = kept.it, count[2] = {kept.use[0][0], kept.use[0][1]};
   Item x;
-  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
-    const int loads = x.loads(), valid = x.kv - x.tile(loads - 1) * kTile;
+  for (; next_item(cx, n, lane, x); ++n) {
+    const int loads = x.loads();
+    const bool ends = x.is_short(loads - 1);
+    const uint32_t it0 = it;
     it += loads;
-    if (valid >= kTile) continue;
-    for (uint32_t t = it - x.heads; t < it; ++t) {
+    if (!ends && !CAREFUL) continue;
+    for (uint32_t t = CAREFUL ? it0 : it - x.heads; t < it; ++t) {
       if (!cx.wait(&m.v_short[t & 1], count[t & 1]++ & 1)) return;
-      for (int i = lane; i < (-valid & 15) * C::kC * 8; i += 32) {
-        const int row = valid + i / (C::kC * 8), c = i / 8 % C::kC;
-        const uint32_t chunk = t * C::kPerTile + C::kC + 1 + row / 64;
-        *reinterpret_cast<uint4*>(cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes + c * 8192 +
-                                  row % 64 * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      auto half = [&](int h) {   // rows 64 h on
+        const uint32_t chunk = t * C::kPerTile + C::kC + 1 + h;
+        return cx.smem + C::kOffRing + chunk % kSlots * kSlotBytes;
+      };
+      const int valid = x.rows(t - it0);
+      if (CAREFUL) {
+        // of 32 rows, kVecs vectors per lane; a look at all of them, and at each where
+        // one is not finite
+        const int mine = lane / kVecs * 128 + lane / 8 % C::kC * 8192 + (lane & 7) * 16;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t rows = 0;
+          if (32 * g < valid) {
+            uint8_t* at = half(g >> 1) + (g & 1) * 32 * 128 + mine;
+            auto vec = [&](int k) { return reinterpret_cast<uint4*>(at + k * (32 / kVecs) * 128); };
+            uint4 u[kVecs];
+            uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) u[k] = *vec(k);
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) add_zero_times<BF16>(sum[k & 3], u[k]);
+            if (has_nan(sum[0]) || has_nan(sum[1]) || has_nan(sum[2]) || has_nan(sum[3])) {
+              auto cleared = [](uint32_t w) {
+                if ((w & kEnd) == kEnd) w &= 0xffff0000u;
+                if ((w >> 16 & kEnd) == kEnd) w &= 0xffffu;
+                return w;
+              };
+#pragma unroll 1
+              for (int k = 0; k < kVecs; ++k) {
+                const uint4 v = *vec(k);
+                uint32_t odd = 0;
+                add_zero_times<BF16>(odd, v);
+                if (has_nan(odd)) {
+                  *vec(k) = make_uint4(cleared(v.x), cleared(v.y), cleared(v.z), cleared(v.w));
+                  rows |= 1u << (k * (32 / kVecs) + lane / kVecs);
+                }
+              }
+            }
+            rows = __reduce_or_sync(0xffffffffu, rows);
+            if (valid < 32 * (g + 1)) rows &= (1u << (valid - 32 * g)) - 1;
+          }
+          if (lane == 0) m.odd_rows[t & 1][g] = rows;
+        }
+      }
+      for (int i = lane; i < (-valid & 15) * kVecs; i += 32) {
+        const int row = valid + i / kVecs;
+        *reinterpret_cast<uint4*>(half(row >> 6) + i / 8 % C::kC * 8192 + row % 64 * 128 + (i & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.v_clean[t & 1]);
     }
   }
+  if (!CAREFUL && lane == 0) kept = Counts{n + 1, it, {{count[0], count[1]}}};
 }
 
-template <int D, bool BF16>
-__device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int lane) {
+template <int D, bool BF16, bool CAREFUL>
+__device__ __forceinline__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   Misc& m = *cx.m;
   constexpr uint32_t idesc_qk = umma_idesc_f16(BF16, kTile, kTile, false);
@@ -374,8 +402,11 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
   const uint64_t dring = sw128_desc(smem_u32(cx.smem + C::kOffRing), 0);
   const uint64_t dv = sw128_desc(smem_u32(cx.smem + C::kOffRing), 8192);
   const int rot_steps = p.rope_dim / 16;
-  uint32_t it = 0, units[2] = {0, 0}, pv[2] = {0, 0};
-  uint32_t cleaned[2] = {0, 0}, full[2] = {0, 0};   // of v_clean, v_full
+  Counts& kept = m.counts[9];
+  uint32_t n = kept.n, it = kept.it, units[2] = {kept.use[0][0], kept.use[0][1]};
+  uint32_t pv[2] = {kept.use[1][0], kept.use[1][1]};
+  // of v_clean, v_full
+  uint32_t cleaned[2] = {kept.use[2][0], kept.use[2][1]}, full[2] = {kept.use[3][0], kept.use[3][1]};
   uint32_t k_seen = ~0u, v_seen = ~0u;              // the load last waited for
   bool ok = true, issued = false;
   if (p.debug_stall) ok = cx.wait(&m.stall, 0);
@@ -424,9 +455,9 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
     ++pv[w];
     if (v_seen != g) {
       // the sequence's last, short tile is cleaned first
-      const bool is_short = x.is_short(s);
-      const uint32_t uses = is_short ? cleaned[g & 1]++ : full[g & 1]++;
-      if (!cx.wait(is_short ? &m.v_clean[g & 1] : &m.v_full[g & 1], uses & 1)) return false;
+      const bool clean = CAREFUL || x.is_short(s);
+      const uint32_t uses = clean ? cleaned[g & 1]++ : full[g & 1]++;
+      if (!cx.wait(clean ? &m.v_clean[g & 1] : &m.v_full[g & 1], uses & 1)) return false;
       v_seen = g;
     }
     if (first) {
@@ -439,18 +470,19 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
     for (int i = 0; i < 2; ++i)
       v[i] = dv + (((g * C::kPerTile + C::kC + 1 + i) % kSlots * kSlotBytes) >> 4);
     const int steps = (x.rows(s) + 15) / 16;
+    const uint32_t begin = first && !CAREFUL ? 0u : 1u;   // CAREFUL: the softmax cleared O
     if (elect_one()) {
 #pragma unroll
       for (int i = 0; i < kTile / 16; ++i)
         if (i < steps) umma_f16_tmem_a(tmem + C::kTmemO + 128 * w, tmem + C::kTmemS + 128 * w + 8 * i,
-                        v[i >> 2] + ((i & 3) * 2048 >> 4), idesc_pv, i > 0 ? 1u : (uint32_t)!first);
+                        v[i >> 2] + ((i & 3) * 2048 >> 4), idesc_pv, i > 0 ? 1u : begin);
       if (last) umma_commit(&m.o_full[w]);
       if (done) umma_commit(&m.v_empty[g & 1]);
     }
     __syncwarp();
     return true;
   };
-  for (uint32_t n = 0; ok && next_item(cx, n, lane, x); ++n) {
+  for (; ok && next_item(cx, n, lane, x); ++n) {
     const int loads = x.loads(), step = x.heads, na = x.na, nb = x.nb;
     // kv tile t is load t of both tiles, or load 2 t of A and 2 t + 1 of B
     for (int t = 0; ok; ++t) {
@@ -477,14 +509,17 @@ __device__ void run_mma(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, i
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(&m.drain, 0) && globaltimer_ns() - t0 < 10000000ull) {}
   }
+  if (!CAREFUL && lane == 0)
+    kept = Counts{n + 1, it, {{units[0], units[1]}, {pv[0], pv[1]}, {cleaned[0], cleaned[1]}, {full[0], full[1]}}};
 }
 
-// Where a moved reference puts the largest weight, and how far one may exceed it:
-// fp16 weights are held 2^7 higher than bf16 ones, as what lies 2^-24 below a weight
-// of one is the type's end.
+// The exponent that a weight may reach over its reference, and where a moved
+// reference puts the largest.  fp16 weights are held high, as what lies 2^-24 below
+// a weight of one is the type's end; bf16 ones are at most one, as values may be
+// near the end of float32's range.
 template <bool BF16>
 struct Ref {
-  static constexpr float kTop = BF16 ? 8.f : 15.f, kPut = BF16 ? 0.f : 7.f;
+  static constexpr float kTop = BF16 ? 0.f : 15.f, kPut = BF16 ? -8.f : 7.f;
 };
 
 template <int D>
@@ -501,18 +536,70 @@ __device__ __noinline__ void rescale(uint32_t o, float f) {
   tmem_wait_st();
 }
 
+// What this warp's q rows get of a kv tile's values that are not finite, which the
+// products have as zeros: O += w v, of the rows of the tile that are set in ``rows``
+// and that a q row sees (up to ``lim``).  O is at rest.  ``dead``: of which 32 columns
+// of O all is NaN and stays so; returned as it is then.  kv_row: the tile's first.
 template <int D, bool BF16>
-__device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int warp, int lane) {
+__device__ __noinline__ uint32_t add_odd_values(const ExpandedParams& p, const uint32_t* rows,
+                                                int64_t kv_row, int head, uint32_t s_at,
+                                                uint32_t o_at, int lim, float ref, uint32_t dead) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint32_t left = rows[g];
+#pragma unroll 1
+    while (left) {
+      const int j = 32 * g + __ffs(left) - 1;
+      left &= left - 1;
+      const float s = tmem_ld1(s_at + j) * p.scale_log2;
+      const float w = ex2_approx(s - ref);
+      const bool counts = j <= lim && s != -INFINITY;
+      if (!__any_sync(0xffffffffu, counts)) continue;
+      const uint16_t* v = p.v + (kv_row + j) * p.v_ts + head * p.v_hs;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        if (dead >> c & 1) continue;
+        const float x = unpack2<BF16>(v[32 * c + lane]).x;
+        const uint32_t odd = __ballot_sync(0xffffffffu, !(fabsf(x) < INFINITY));
+        if (!odd) continue;
+        float o[32];
+        tmem_ld32(o_at + 32 * c, o);
+        tmem_wait_ld(o);
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float y = __shfl_sync(0xffffffffu, x, i);
+          if (counts && (odd >> i & 1)) o[i] = fmaf(w, y, o[i]);
+          all = all && o[i] != o[i];
+        }
+        tmem_st32(o_at + 32 * c, o);
+        tmem_wait_st();
+        if (__all_sync(0xffffffffu, all)) dead |= 1u << c;
+      }
+    }
+  }
+  return dead;
+}
+
+// Returns whether a result of this thread's may have to be computed carefully.
+template <int D, bool BF16, bool CAREFUL>
+__device__ __forceinline__ bool run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tmem, int warp,
+                                            int lane) {
   using C = Cfg<D>;
   Misc& m = *cx.m;
+  Counts& kept = m.counts[warp];
   const int w = warp >> 2;                       // tile A or B
   const int rr = (warp & 3) * 32 + lane;         // the tile's row
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_at = tmem + lanes + C::kTmemS + 128 * w, o_at = tmem + lanes + C::kTmemO + 128 * w;
-  uint32_t done = 0, units = 0;
+  uint32_t n = kept.n, it = kept.it, done = kept.use[0][0], units = kept.use[0][1];
+  bool odd_result = false;
   Item x;
-  for (uint32_t n = 0; next_item(cx, n, lane, x); ++n) {
+  for (; next_item(cx, n, lane, x); ++n) {
     const int tiles = w ? x.nb : x.na;
+    const uint32_t it0 = it;
+    it += x.loads();
     if (tiles == 0) continue;
     const int row = w * (2 - x.heads) * kTile + rr;          // of the unit's
     const int head = x.head + w * (x.heads - 1);
@@ -520,8 +607,9 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     const int low = see - lane;                  // the warp's first row's
     const bool work = row - lane < x.nq;
     float ref = -FLT_MAX, l = 0.f;
+    uint32_t dead = 0;
     for (int t = 0; t < tiles; ++t, ++done) {
-      if (!cx.wait(&m.s_full[w], done & 1)) return;
+      if (!cx.wait(&m.s_full[w], done & 1)) return false;
       if (!work) {                               // no row of the warp is the sequence's
         if (lane == 0) mbar_arrive(&m.p_full[w]);
         continue;
@@ -532,7 +620,25 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
       float s[2][32];
       const int lim = see - t * kTile, lim0 = low - t * kTile;
       float2 sum = make_float2(0.f, 0.f);
-      auto refer = [&](float most) {             // moves the reference where it has to be
+      bool ok = true;
+      // CAREFUL: of the tile's values, load g, those that are not finite
+      auto add_odd = [&]() {
+        const uint32_t g = it0 + t * x.heads + w * (x.heads - 1);
+        // the cleaner's counts at the start of this pass, in which it cleans every load
+        const Counts& then = m.counts[10];
+        const uint32_t uses = then.use[0][g & 1] + ((g - then.it) >> 1);
+        if (!(ok = cx.wait(&m.v_clean[g & 1], uses & 1))) return;
+        if (t == 0) {
+          const float zero[32] = {};
+          for (int c = 0; c < D; c += 32) tmem_st32(o_at + c, zero);
+          tmem_wait_st();
+        }
+        dead = add_odd_values<D, BF16>(p, m.odd_rows[g & 1], (int64_t)x.kv0 + t * kTile, head, s_at, o_at,
+                                       see - t * kTile, ref, dead);
+      };
+      // Moves the reference where it has to be.  (Products that no compiler joins with an
+      // addition: a careful pass gives the bits of the first.)
+      auto refer = [&](float most) {
         const bool move = most - ref > Ref<BF16>::kTop;
         if (!__any_sync(0xffffffffu, move)) return;
         float f = 1.f;
@@ -540,7 +646,7 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
           const float to = most - Ref<BF16>::kPut;
           f = ex2_approx(ref - to);
           ref = to;
-          l *= f;
+          l = __fmul_rn(l, f);
         }
         // the product before has been waited for with these scores: O is at rest
         if (t > 0) rescale<D>(o_at, f);
@@ -564,7 +670,11 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
             for (int j = 0; j < 32; ++j) top[j & 1] = fmaxf(top[j & 1], -s[c & 1][j]);
           }
         }
-        refer(fmaxf(top[0], top[1]) * fabsf(p.scale_log2));
+        refer(__fmul_rn(fmaxf(top[0], top[1]), fabsf(p.scale_log2)));
+        if (CAREFUL) {
+          add_odd();
+          if (!ok) return false;
+        }
         tmem_ld32(s_at, s[0]);
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
 #pragma unroll
@@ -600,6 +710,10 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
         }
         tmem_wait_ld(s[0]);
         refer(fmaxf(top[0], top[1]));
+        if (CAREFUL) {
+          add_odd();
+          if (!ok) return false;
+        }
         const float2 scale = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(-ref, -ref);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -627,7 +741,7 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.p_full[w]);
     }
-    if (!cx.wait(&m.o_full[w], units & 1)) return;
+    if (!cx.wait(&m.o_full[w], units & 1)) return false;
     ++units;
     if (!work) {
       if (lane == 0) mbar_arrive(&m.o_free[w]);
@@ -671,14 +785,33 @@ __device__ void run_softmax(const Ctx& cx, const ExpandedParams& p, uint32_t tme
     const float odd = odd2.x + odd2.y;
     if (valid) p.lse[at] = l == 0.f ? -INFINITY : ref + log2f(l);
     // a value that is not finite, though the weights are: it may be one not seen
-    unsigned again = __ballot_sync(0xffffffffu, valid && odd != 0.f && l < INFINITY);
-    while (again) {
-      const int i = __ffs(again) - 1;
-      again &= again - 1;
-      __syncwarp();
-      row_exact<D, BF16>(p, x.b, x.q0 + row - lane + i, head);
-    }
+    odd_result |= valid && odd != 0.f && l < INFINITY;
   }
+  if (!CAREFUL && lane == 0) kept = Counts{n + 1, it, {{done, units}}};
+  return odd_result;
+}
+
+// This CTA's units, once.  Returns whether a result of this thread's may have to be
+// computed carefully.
+template <int D, bool BF16, bool CAREFUL>
+__device__ __forceinline__ bool run_pass(const Ctx& cx, const ExpandedMaps& maps, const ExpandedParams& p,
+                                         int warp, int lane) {
+  const uint32_t tmem = cx.m->tmem;
+  if (warp < 8) return run_softmax<D, BF16, CAREFUL>(cx, p, tmem, warp, lane);
+  if (warp == 8)
+    run_producer<D, CAREFUL>(cx, maps, lane);
+  else if (warp == 9)
+    run_mma<D, BF16, CAREFUL>(cx, p, tmem, lane);
+  else if (warp == 10)
+    run_cleaner<D, BF16, CAREFUL>(cx, lane);
+  else
+    run_scheduler(cx, p, lane);
+  return false;
+}
+template <int D, bool BF16>
+__device__ __noinline__ void run_carefully(const Ctx& cx, const ExpandedMaps& maps, const ExpandedParams& p,
+                                           int warp, int lane) {
+  run_pass<D, BF16, true>(cx, maps, p, warp, lane);
 }
 
 template <int D, bool BF16>
@@ -709,6 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&m.stall, 1);
     mbar_init(&m.drain, 1);
+    for (int i = 0; i < kThreads / 32; ++i) m.counts[i] = Counts{};
     m.abort = 0;
     mbar_fence_init();
   }
@@ -731,17 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ctx cx{smem, &m, p.error, p.timeout_ns};
   if (stop) {
     if (tid == 0) atomicOr(p.error, DEVERR_BAD_INDPTR);
-  } else if (warp < 8) {
-    run_softmax<D, BF16>(cx, p, m.tmem, warp, lane);
   } else {
-    if (warp == 8)
-      run_producer<D>(cx, maps, lane);
-    else if (warp == 9)
-      run_mma<D, BF16>(cx, p, m.tmem, lane);
-    else if (warp == 10)
-      run_cleaner<D>(cx, lane);
-    else
-      run_scheduler(cx, p, lane);
+    const bool odd = run_pass<D, BF16, false>(cx, maps, p, warp, lane);
+    __syncwarp();
+    tc_fence_before();
+    const bool again = __syncthreads_or(odd);
+    tc_fence_after();
+    if (again && !m.abort) run_carefully<D, BF16>(cx, maps, p, warp, lane);
   }
   __syncwarp();
   tc_fence_before();
