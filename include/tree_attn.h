@@ -456,8 +456,9 @@ typedef struct {
  * calls that may overlap on the GPU, latent caches of any dims may take turns on
  * one that is large enough.  It is not a workspace for calls of the other sections,
  * nor theirs one for these: what has to be zero between calls has another place
- * (zero-filled again, it may change sides).  It holds the device status word, a mark per page of the pool and
- * the partial states of sequences that several SMs share. */
+ * (zero-filled again, it may change sides).  It holds the device status word, a
+ * mark per page of the pool and the partial states of sequences that several SMs
+ * share. */
 size_t tree_attn_latent_workspace_size(const ta_latent_dims* dims);
 
 /* Appends tokens to a latent cache.  The page table describes the cache after

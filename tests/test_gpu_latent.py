@@ -922,6 +922,67 @@ def test_workspaces_of_the_two_kinds_of_cache_are_kept_apart():
         ta.LatentCache(s.pool, *table, h_q=4, rank=256, workspace=other.workspace)
 
 
+def test_a_reset_workspace_serves_the_other_kind():
+    """Views are refused like the tensor itself; after a reset every call of the
+    other kind is as on a workspace of its own, copies by marks among them."""
+    s = Setup([3000, 40, 900], 64, 256, 16, seed=26)
+    table = [i32(x) for x in s.table]
+    q = s.randn(3, 64, s.w)
+    want = [t.clone() for t in s.cache.decode(q, 0.07)]
+    g = torch.Generator("cuda").manual_seed(27)
+    pool = torch.randn((6000, 2, 2, 16, 64), generator=g, device="cuda").bfloat16()
+    small = ta.PagedCache(pool, *table, h_q=4)
+    for ws in (s.cache.workspace[:], s.cache.workspace.view(torch.int32), s.cache.workspace[256:]):
+        with pytest.raises(ValueError, match="kind of cache"):
+            ta.PagedCache(pool, *table, h_q=4, workspace=ws)
+    with pytest.raises(ValueError, match="kind of cache"):
+        ta.LatentCache(s.pool, *table, h_q=64, rank=256, workspace=small.workspace[:])
+    ws = torch.zeros(max(s.cache.workspace.numel(), small.workspace.numel()), dtype=torch.uint8, device="cuda")
+    latent = ta.LatentCache(s.pool, *table, h_q=64, rank=256, workspace=ws)
+    latent.decode(q, 0.07)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ta.reset_workspace(ws, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    shared = ta.PagedCache(pool, *table, h_q=4, workspace=ws)
+    assert shared.workspace is ws
+    perm = torch.randperm(6000, generator=torch.Generator().manual_seed(1)).int().cuda()
+    src, dst = perm[:3000].contiguous(), perm[3000:].contiguous()
+    qp = torch.randn((3, 4, 64), generator=g, device="cuda").bfloat16()
+    for _ in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(shared.decode(qp, 0.1), small.decode(qp, 0.1)))
+        after = pool.clone()
+        after[dst.long()] = after[src.long()]
+        shared.copy_pages(src, dst)
+        assert shared.device_status() == ta.TA_OK and torch.equal(pool, after)
+    ta.reset_workspace(ws, stream=torch.cuda.current_stream().cuda_stream)
+    latent = ta.LatentCache(s.pool, *table, h_q=64, rank=256, workspace=ws)
+    got = latent.decode(q, 0.07)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_copies_by_marks_between_attention_on_one_workspace():
+    """Handles of other pools and ranks: what one call leaves in a workspace is not
+    in the way of another's marks."""
+    a = Setup([1700, 3, 900], 128, 512, 64, seed=1)
+    g = torch.Generator("cuda").manual_seed(2)
+    pool = torch.randn((7000, 16, 272), generator=g, device="cuda").bfloat16()
+    b = ta.LatentCache(pool, i32([0, 1]), i32([0]), i32([3]), h_q=1, rank=256)
+    a.cache = ta.LatentCache(a.pool, *[i32(x) for x in a.table], h_q=128, rank=512, workspace=b.workspace)
+    assert a.cache.workspace is b.workspace
+    q = a.randn(3, 128, a.w)
+    perm = torch.randperm(7000, generator=torch.Generator().manual_seed(3)).int().cuda()
+    src, dst = perm[:3500].contiguous(), perm[3500:].contiguous()
+    for _ in range(3):
+        out, lse = a.cache.decode(q, 0.07)
+        after = pool.clone()
+        after[dst.long()] = after[src.long()]
+        b.copy_pages(src, dst)
+        assert b.device_status() == ta.TA_OK and torch.equal(pool, after)
+        check_absorbed(a, q, out, lse, 0.07)
+        src, dst = dst, src
+
+
 # --------------------------------------------------------------------------
 # the ends of what is allowed
 # --------------------------------------------------------------------------

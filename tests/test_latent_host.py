@@ -265,3 +265,31 @@ def test_python_refusals(lib):
         ta.tree_attn_expanded(q, i, q[..., :128], z((4, 64)), q[..., :128], i, None, None, 0.1, None)
     with pytest.raises(ValueError):
         ta.tree_attn_expanded(q[0], i, q, q, q, i, None, None, 0.1, None)
+
+
+# --------------------------------------------------------------------------
+# workspaces of the two kinds of cache
+# --------------------------------------------------------------------------
+
+def test_claims_go_by_memory_until_reset():
+    """A view of a workspace is that workspace; parts of one buffer are not."""
+    a, b = "latent", "paged"
+    buf = torch.full((1000,), 7, dtype=torch.uint8)
+    ta._claim(buf[:400], a)
+    for view in (buf, buf[:400], buf[399:500], buf.view(-1)[100:200], buf.view(torch.int32)[:2]):
+        with pytest.raises(ValueError, match="kind of cache"):
+            ta._claim(view, b)
+        ta._claim(view, a, used=False)
+    ta._claim(buf[400:], b)
+    with pytest.raises(ValueError):
+        ta._claim(buf[300:500], a)
+    ta.reset_workspace(buf[:600])
+    assert (buf[:600] == 0).all() and (buf[600:] == 7).all()
+    ta._claim(buf[:600], a)
+    with pytest.raises(ValueError):
+        ta._claim(buf[599:601], a)            # the rest is still the other kind's
+    ta.reset_workspace(buf)
+    ta._claim(buf, b)
+    ta._claim(torch.zeros(1000, dtype=torch.uint8), a)
+    with pytest.raises(ValueError, match="contiguous"):
+        ta.reset_workspace(buf[::2])

@@ -30,7 +30,7 @@ __all__ = [
     "MAX_CHUNKS", "split_workspace_size", "tree_attn_split", "merge_states", "last_cuda_error",
     "folds_rotation", "noalloc_device_status", "set_wait_hooks", "auto_split_chunks",
     "set_scheduler", "CacheDims", "Rope", "PagedCache", "cache_workspace_size", "LatentDims",
-    "LatentCache", "latent_workspace_size", "ExpandedDims", "make_expanded_dims",
+    "LatentCache", "latent_workspace_size", "reset_workspace", "ExpandedDims", "make_expanded_dims",
     "expanded_workspace_size", "tree_attn_expanded",
 ]
 
@@ -570,6 +570,58 @@ def _compiled():
     return _binding_module
 
 
+def _bytes_of(workspace: torch.Tensor):
+    """Where a workspace lies in its storage, which all tensors on it share."""
+    storage = workspace.untyped_storage()
+    start = workspace.data_ptr() - storage.data_ptr()
+    return storage.__dict__, start, start + workspace.numel() * workspace.element_size()
+
+
+def _claim(workspace: torch.Tensor, kind: str, used: bool = True) -> None:
+    """Note that ``workspace`` is one of this kind of cache (if ``used``).  The two
+    kinds keep what has to be zero between calls in different places, so memory that
+    the other kind has had is refused, as whatever tensor it comes, until
+    ``reset_workspace``."""
+    notes, start, end = _bytes_of(workspace)
+    claims = notes.setdefault("_tree_attn_claims", set())   # (start, end, kind)
+    for a, b, other in claims:
+        if other != kind and a < end and start < b:
+            raise ValueError(f"workspace is one of the other kind of cache ({other}, not {kind})")
+    if used:
+        claims.add((start, end, kind))
+
+
+def _as_stream(stream, device):
+    """A stream object for a stream given as one or by address."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    address = int(getattr(stream, "cuda_stream", stream))
+    # 0 and 1 are CUDA's names of the legacy default stream
+    return (torch.cuda.ExternalStream(address, device=device) if address > 1
+            else torch.cuda.default_stream(device))
+
+
+def reset_workspace(workspace: torch.Tensor, stream=None) -> None:
+    """Zero-fill a cache's workspace on ``stream`` (default: torch's current one),
+    behind all calls on it, so that it may serve the other kind of cache.  Not while
+    a graph is captured, whose replays would fill it again."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.is_cuda and torch.cuda.is_current_stream_capturing():
+        raise ValueError("a workspace cannot be reset while a graph is captured")
+    if stream is None:
+        workspace.zero_()
+    else:
+        with torch.cuda.stream(_as_stream(stream, workspace.device)):
+            workspace.zero_()
+    notes, start, end = _bytes_of(workspace)
+    claims = notes.get("_tree_attn_claims", set())
+    for a, b, kind in list(claims):
+        if a < end and start < b:
+            claims.remove((a, b, kind))
+            claims.update((x, y, kind) for x, y in ((a, start), (end, b)) if x < y)
+
+
 class _Cache:
     """What ``PagedCache`` and ``LatentCache`` have in common: the pool, its page
     table and the workspace.  A subclass names its dims' size function and the
@@ -599,10 +651,7 @@ class _Cache:
             _check_dev("workspace", workspace)
             if workspace.get_device() != self._dev:
                 raise ValueError("workspace must be on the device of pages")
-            # the two kinds keep what has to be zero between calls in different places
-            if getattr(workspace, "_tree_attn_kind", self._size_name) != self._size_name:
-                raise ValueError("workspace is one of the other kind of cache "
-                                 f"({workspace._tree_attn_kind}, not {self._size_name})")
+            _claim(workspace, self._size_name, workspace.numel() * workspace.element_size() >= need)
         if workspace is None or workspace.numel() * workspace.element_size() < need:
             # zero-filled once, before a call on any stream: the library keeps its
             # counters consistent afterwards.  While a graph is captured the filling
@@ -613,7 +662,7 @@ class _Cache:
                 self._binding.zero_now(workspace)
             else:
                 torch.cuda.current_stream(self._dev).synchronize()
-        workspace._tree_attn_kind = self._size_name
+            _claim(workspace, self._size_name)
         self.workspace = workspace
         # the addresses of these tensors are what the calls pass, so they stay
         self._held = (pages, page_indptr, page_values, length_info, workspace)
@@ -626,12 +675,7 @@ class _Cache:
         """A new output, from the pool of the stream that the call runs on."""
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        if not isinstance(stream, torch.cuda.Stream):
-            address = int(getattr(stream, "cuda_stream", stream))
-            # 0 and 1 are CUDA's names of the legacy default stream
-            stream = (torch.cuda.ExternalStream(address, device=self.device) if address > 1
-                      else torch.cuda.default_stream(self.device))
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(_as_stream(stream, self.device)):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def compact(self, mn_indptr, accept_indptr, accept_nodes, *, new_page_indptr=None,
@@ -748,7 +792,8 @@ class LatentCache(_Cache):
 
     ``pages [num_pages, 16, rank + rope_dim]``, the table and the workspace are
     held as ``PagedCache`` holds its own; everything said there holds here.  A
-    workspace may be another ``LatentCache``'s, but not a ``PagedCache``'s."""
+    workspace may be another ``LatentCache``'s, but a ``PagedCache``'s only after
+    ``reset_workspace`` (and the other way round)."""
 
     _prefix, _size_name = "latent_", "tree_attn_latent_workspace_size"
     _names = ("tree_attn_compact_latent", "tree_attn_copy_pages_latent")
