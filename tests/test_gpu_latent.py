@@ -162,6 +162,24 @@ def test_decode_largest_batch():
     check_absorbed(s, q, out, lse, 0.1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_merges_in_large_units_of_the_small_rank(dtype):
+    """Enough sequences that several pairs of SMs share for the merge's large units
+    (32 rows by 128 columns: two CTAs' worth of them per SM and more)."""
+    kv = [int(x) for x in np.random.default_rng(28).integers(400, 2200, 70)]
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    tiles = np.cumsum([0] + [-(-n // 128) for n in kv])
+    per, extra = divmod(int(tiles[-1]), pairs)
+    starts = {i * per + min(i, extra) for i in range(pairs)}
+    cut = sum(any(u in starts for u in range(a + 1, b)) for a, b in zip(tiles[:-1], tiles[1:]))
+    assert cut * 4 * 2 * 2 >= 4 * 2 * pairs
+    s = Setup(kv, 128, 256, 64, dtype, seed=29)
+    q = s.randn(len(kv), 128, s.w)
+    out, lse = s.cache.decode(q, 0.07)
+    assert s.cache.device_status() == ta.TA_OK
+    check_absorbed(s, q, out, lse, 0.07)
+
+
 def test_decode_without_any_page():
     pool = torch.full((2, 16, 576), NAN, dtype=torch.bfloat16, device="cuda")
     c = ta.LatentCache(pool, i32([0, 0, 0]), i32([]), i32([0, 0]), h_q=4, rank=512)
