@@ -657,7 +657,9 @@ ta_status tree_attn_device_status(void* workspace, void* stream);
  * returns, and tree_attn_device_status reports it.  These hooks let a test
  * take that path on purpose, for the attention kernels launched by later
  * calls made on the calling host thread:
- *   wait_limit_ns  the limit of every bounded wait (0: the default 2 s)
+ *   wait_limit_ns  the limit of every bounded wait (0: the default 2 s); in the
+ *                  kernels of latent attention it counts from the last kv tile
+ *                  asked for, as a unit of work may take longer
  *   stall          1: the MMA thread of every pipeline first waits on a
  *                  barrier that nothing arrives on, so that this wait runs
  *                  out after wait_limit_ns and every other warp then gives up

@@ -1198,3 +1198,24 @@ def test_parts_of_an_earlier_call_are_not_joined():
         got = s.cache.decode(q, 0.07)
         assert s.cache.device_status() == ta.TA_OK
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_waits_are_limited_from_the_last_progress():
+    """Some warps wait for a whole unit of work: with a limit far below what one
+    takes, but far above what one of its tiles takes, nothing runs out."""
+    e = Expanded([1, 3], [200001, 150003], 1, 64, 16, "bf16", seed=40)
+    want = [t.clone() for t in e.run(0.1)]
+    # 12 or 13 items of 128 packed rows for a pair of SMs, 400 tiles of kv rows each
+    trees = Trees([(51000, 64, 64, "star")] * 30, 64, 256, 16, "bf16", seed=41)
+    twant = [t.clone() for t in trees.run(0.1)]
+    assert milliseconds(lambda: e.run(0.1), 1) > 2 and milliseconds(lambda: trees.run(0.1), 1) > 2
+    ta.set_wait_hooks(150_000, False)
+    try:
+        out, lse = e.run(0.1, out=torch.zeros_like(want[0]), lse=torch.zeros_like(want[1]))
+        assert ta.device_status(e.ws) == ta.TA_OK
+        tout, tlse = trees.run(0.1)
+        assert trees.s.cache.device_status() == ta.TA_OK
+    finally:
+        ta.set_wait_hooks(0, False)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.equal(tout, twant[0]) and torch.equal(tlse, twant[1])

@@ -189,7 +189,7 @@ struct Misc {
   long long scan[12];
   LatentSeq first;                   // the range's first sequence, its first tile
   int first_seq, first_unit;
-  uint32_t tmem;
+  uint32_t tmem, tiles;              // tiles: whose keys were asked for
   int abort;
 };
 
@@ -198,7 +198,8 @@ struct Ctx {
   Misc* m;
   unsigned int* error;
   uint64_t limit_ns;
-  // Waits for a phase, at most limit_ns, or until another thread gave up.
+  // Waits for a phase, at most limit_ns in which this CTA asks for no further tile of
+  // keys (a piece may take as long as it takes), or until another thread gave up.
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {   // by one thread
     if (try_wait_cluster(bar, parity)) return true;
     return wait_long(bar, parity);
@@ -208,25 +209,32 @@ struct Ctx {
     if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
     return wait_warp_long(bar, parity);
   }
-  __device__ __forceinline__ bool expired(uint64_t t0) const {
+  __device__ __forceinline__ bool expired(uint64_t& t0, uint32_t& tiles) const {
     if (*(volatile int*)&m->abort) return true;
+    const uint32_t now = *(volatile uint32_t*)&m->tiles;
+    if (now != tiles) {
+      tiles = now;
+      t0 = globaltimer_ns();
+    }
     if (globaltimer_ns() - t0 <= limit_ns) return false;
     atomicOr(error, DEVERR_TIMEOUT);
     *(volatile int*)&m->abort = 1;
     return true;
   }
   __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    uint32_t tiles = *(volatile uint32_t*)&m->tiles;
     for (uint32_t spins = 1;; ++spins) {
       if (try_wait_cluster(bar, parity)) return true;
-      if ((spins & 63u) == 0 && expired(t0)) return false;
+      if ((spins & 63u) == 0 && expired(t0, tiles)) return false;
     }
   }
   __device__ __noinline__ bool wait_warp_long(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    uint32_t tiles = *(volatile uint32_t*)&m->tiles;
     for (uint32_t spins = 1;; ++spins) {
       if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
-      if ((spins & 63u) == 0 && __any_sync(0xffffffffu, expired(t0))) return false;
+      if ((spins & 63u) == 0 && __any_sync(0xffffffffu, expired(t0, tiles))) return false;
     }
   }
 };
@@ -340,6 +348,7 @@ __device__ void run_k_producer(const Ctx& cx, const LatentParams& p, const Absor
     for (int t = x.t0; t < x.t1; ++t, ++it) {
       const int page = next;
       if (t + 1 < x.t1) next = page_of(p, x, t + 1, lane);
+      if (lane == 0) *(volatile uint32_t*)&m.tiles = it + 1;
 #pragma unroll
       for (int g = 0; g < 3; ++g) {
         if (!cx.wait_warp(&m.k_empty[g], (it & 1) ^ 1)) return;
@@ -854,6 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&m.stall, 1);
     mbar_init(&m.drain, 1);
     m.abort = 0;
+    m.tiles = 0;
     m.first_seq = 0;
     m.first_unit = 0;
     mbar_fence_init();

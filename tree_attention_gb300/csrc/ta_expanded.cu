@@ -83,7 +83,7 @@ struct Misc {
   Item item[kItems];
   uint32_t odd_rows[2][4];           // of a kv tile: rows with values that are not finite
   Counts counts[kThreads / 32];
-  uint32_t tmem;
+  uint32_t tmem, loads;              // loads: kv tiles that were asked for
   int abort;
 };
 
@@ -102,24 +102,31 @@ struct Ctx {
   Misc* m;
   unsigned int* error;
   uint64_t limit_ns;
-  __device__ __forceinline__ bool expired(uint64_t t0) const {
+  __device__ __forceinline__ bool expired(uint64_t& t0, uint32_t& loads) const {
     if (*(volatile int*)&m->abort) return true;
+    const uint32_t now = *(volatile uint32_t*)&m->loads;
+    if (now != loads) {
+      loads = now;
+      t0 = globaltimer_ns();
+    }
     if (globaltimer_ns() - t0 <= limit_ns) return false;
     atomicOr(error, DEVERR_TIMEOUT);
     *(volatile int*)&m->abort = 1;
     return true;
   }
-  // by a whole warp, with one answer for all lanes; at most limit_ns, or until
-  // another warp gave up
+  // by a whole warp, with one answer for all lanes; at most limit_ns in which no
+  // further kv tile is asked for (a unit may take as long as it takes), or until another
+  // warp gave up
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return wait_long(bar, parity);
   }
   __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity) const {
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
+    uint32_t loads = *(volatile uint32_t*)&m->loads;
     for (uint32_t spins = 1;; ++spins) {
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-      if ((spins & 63u) == 0 && __any_sync(0xffffffffu, expired(t0))) return false;
+      if ((spins & 63u) == 0 && __any_sync(0xffffffffu, expired(t0, loads))) return false;
     }
   }
 };
@@ -270,6 +277,7 @@ __device__ __forceinline__ void run_producer(const Ctx& cx, const ExpandedMaps& 
     if (!load_q(0)) return;
     const int loads = x.loads();
     for (int t = 0; t < loads; ++t, ++it) {
+      if (lane == 0) *(volatile uint32_t*)&m.loads = it + 1;
       const int row = x.kv0 + x.tile(t) * kTile, s = it & 1, head = x.head + (t & (x.heads - 1));
       uint64_t* v_bar = CAREFUL || x.is_short(t) ? &m.v_short[s] : &m.v_full[s];
       const int boxes = x.rows(t) > 64 ? 2 : 1;
@@ -844,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&m.drain, 1);
     for (int i = 0; i < kThreads / 32; ++i) m.counts[i] = Counts{};
     m.abort = 0;
+    m.loads = 0;
     mbar_fence_init();
   }
   if (warp == 8) {
