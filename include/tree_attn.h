@@ -504,7 +504,8 @@ ta_status tree_attn_append_latent(const void* latent, int64_t latent_stride, con
  * counts as if it were not there, one whose score is NaN or +inf makes its head's
  * out NaN.  Weights are rounded to dtype before they meet the values (and out is
  * divided by the sum of the rounded ones), all else is float32.  The result does
- * not depend on timing.
+ * not depend on timing.  Where sm_scale is 0, a score is 0 times the product: NaN
+ * where that is infinite.
  * Inconsistent page tables (or 2^31 pairs of 128 heads of q rows and 128 kv rows and
  * more) are reported by tree_attn_device_status and nothing is computed.  q, pages
  * and out 16-byte aligned.  Asynchronous on stream. */
@@ -520,7 +521,9 @@ ta_status tree_attn_decode_latent(const void* q, const void* pages, const int32_
  * of a sequence its nodes), with q [total_q, h_q, rank + rope_dim], out
  * [total_q, h_q, rank], lse [total_q, h_q]; all else is as for
  * tree_attn_decode_latent.  What a q row does not see has no part in its result,
- * whatever it holds.  total_q * h_q must fit an int32. */
+ * whatever it holds.  All pairs of q rows and of a sequence's rows are multiplied,
+ * also those in a tree of which nothing is seen (tree_attn_paged leaves them out).
+ * total_q * h_q must fit an int32. */
 ta_status tree_attn_latent(const void* q, const int32_t* q_indptr, int32_t total_q,
                            const void* pages, const int32_t* page_indptr,
                            const int32_t* page_values, const int32_t* length_info,
@@ -576,9 +579,12 @@ size_t tree_attn_expanded_workspace_size(const ta_expanded_dims* dims);
  *            rows merge with it (tree_attn_merge_states)
  * Every *_token_stride and *_head_stride in elements, multiples of 8, at least a
  * row, so that k and v may be views of one projection of the latents.  What a
- * q row does not see has no part in its result, whatever it holds.  Weights are
- * rounded to dtype before they meet the values, all else is float32.  A row whose score is -inf counts as if it were not
- * there; one of NaN or +inf makes the result NaN.  Inconsistent indptr arrays are
+ * q row does not see has no part in its result, whatever it holds (results that
+ * are not finite make their SM go over its share of the call twice).  Weights are
+ * rounded to dtype before they meet the values (out is divided by the sum of the
+ * unrounded ones), all else is float32.  A row whose score is -inf counts as if it
+ * were not there; one of NaN or +inf makes the result NaN.  Rows that a paged cache
+ * holds already have to be at hand as plain rows, gathered from its pages.  Inconsistent indptr arrays are
  * reported by tree_attn_device_status and nothing is computed.  Pointers 16-byte
  * aligned.  Asynchronous on stream. */
 ta_status tree_attn_expanded(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -27,16 +27,22 @@
 //
 // Measured, bf16, rank 512, rotary 64 (the memory copies at 6.69 TB/s, the tensor
 // cores reach 1,947 TFLOP/s; the merge included): 4 sequences of 33,000 rows with 128
-// heads 50.1 us, floor 23 (memory) and 19 (tensor cores) at once; 64 sequences of 16 to
-// 16,384 rows with 64 heads 74.7 us, floor 37; draft trees of 64 nodes with 32 heads
-// behind 4 x 32,768 rows 435 us, 1,340 TFLOP/s.  A pair's products for a tile take
-// 2,500 cycles, its rows from memory 3,475 when all pairs read; for trees a tile takes
-// 2,500 to 2,900, for decode 2,650 with the rows at hand and some 4,700 on average over
-// a long call.  A call of few tiles is its start (4.3 us: tables, the first page's
+// heads 49.6 us, floor 23 (memory) and 19 (tensor cores) at once; 64 sequences of 16 to
+// 16,384 rows with 64 heads 73.5 to 74.9 us, floor 37; draft trees of 64 nodes with 32
+// heads behind 4 x 32,768 rows 411 to 490 us, 1,420 to 1,190 TFLOP/s, by the state of
+// the GPU's power limit.  A pair's products for a tile take 2,500 cycles, its rows from
+// memory 3,475 when all pairs read; for trees a tile takes 2,500 to 2,900, for decode
+// 2,650 with the rows at hand and some 4,700 on average over a long call.  A call of few tiles is its start (4.3 us: tables, the first page's
 // look-up), the first loads (3 us), the parts' stores (3 us) and the merge (4 to 8 us).
 // Joining the parts in this kernel, pair by pair, took longer for few long sequences
 // (decode of one of 4,096 rows 14.5 -> 29.5 us) than the merge as a kernel of its own,
 // which all SMs share.
+//
+// Weights are rounded to the data's type for the product, as the tensor cores take both
+// operands in it: the error against 64 bits is 1.05 to 1.25 times that of float32
+// weights, as each output is rounded as well.  A second product with what the rounding
+// left would want 16 KB of shared memory, of which 3 KB are left, and two fifths of
+// the tensor cores' time.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -1051,10 +1057,11 @@ __device__ __forceinline__ void merge_unit(const LatentParams& p, const LatentMe
 //   m = max m_i,  O = sum 2^(m_i - m) O_i,  l = sum 2^(m_i - m) l_i.
 // Bound by latency: 4 to 8 us, of which reading the parts (at most 2 x 76 of 264 KB,
 // mostly in L2) would be 3 to 6.  All items'
-// units are shared out over one resident wave of CTAs: large units where there are
-// enough of them (each costs its loads' latency once), small ones where not.  Small
-// units have 12 parts in flight: one sequence of 4,096 rows in 32 parts 13.0 us, with 8
-// 14.0; with 16, which spill, 12.8, but 64 sequences 78.6 instead of 75.3.
+// units are shared out over four CTAs per SM, of which the registers let two be
+// resident: large units where there are two for each of them (a unit costs its loads'
+// latency once), small ones where not.  Small units have 12 parts in flight: one
+// sequence of 4,096 rows in 32 parts 13.0 us, with 8 14.0; with 16, which spill, 12.8,
+// but 64 sequences 78.6 instead of 75.3.
 template <int RANK, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads, 2) absorbed_merge_kernel(const LatentParams p, int pairs) {
   __shared__ int s_at[kMaxPairs + 1];          // groups of 32 rows before each item

@@ -25,15 +25,22 @@
 //   the softmax threads add what the rows that see them get.
 //
 // Measured: prompts of 16 to 512 tokens, 64 sequences, 64 heads of 128 + 64, bf16:
-// 172 us on one GPU, 229 on another (floor 109, the memory); 2,000 tokens each of two
-// prompts with 14,000 held, 32 heads, fp16: 775 us, 1,228 TFLOP/s (floor 489, the
-// tensor cores).  The latter are 512 units for 152 SMs, so four rounds for 3.4, and a
-// pair of tiles takes some 3,100 cycles of the 2,600 that its products need: a tile's
-// softmax and its products follow one another, and the softmax of one tile (some 1,850
-// cycles) takes longer than the other's products (1,300).  Two threads per q row, which
-// halve the softmax but have to agree on the maximum and get 96 registers, took 854
-// us (prompts 336); the last round's units as single tiles on two SMs each 843 (a tile
+// 175 to 200 us by the GPU (floor 109, the memory), up to 235 right behind a load at the
+// power limit; 2,000 tokens each of two prompts with 8,195 and 13,045 held, 32 heads,
+// fp16: 776 to 822 us, 1,227 to 1,158 TFLOP/s (floor 489, the tensor cores).  The latter
+// are 512 units of 67 to 118 kv tiles, of which the busiest of 152 SMs has 375 and the
+// average one 311, and a kv tile, for both tiles of q rows, takes 3,960 cycles of the
+// 2,600 that its products need: the period is one tile's softmax (some 1,850), its
+// products (1,300) and the hand-overs one after the other, beside which the other
+// tile's run.  Two threads per q row, which halve the softmax but have to agree on the
+// maximum and get 96 registers, took 854 instead of 783 us (prompts 336 instead of 174);
+// the last round's units as single tiles on two SMs each 843 instead of 815 (a tile
 // alone takes as long as two).
+//
+// Weights are rounded to the data's type for the product (the error against 64 bits is
+// 1.2 to 1.41 times that of float32 weights, as each output is rounded as well); the
+// result is divided by their unrounded sum, since that of the rounded ones was measured
+// to change the error by 1 % at most and the time by 2 % (prompts 10 %).
 #include <cuda_runtime.h>
 
 #include <atomic>
