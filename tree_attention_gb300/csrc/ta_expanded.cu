@@ -564,7 +564,7 @@ __device__ __noinline__ uint32_t add_odd_values(const ExpandedParams& p, const u
   for (int g = 0; g < 4; ++g) {
     uint32_t left = rows[g];
 #pragma unroll 1
-    while (left) {
+    while (left && dead != (1u << (D / 32)) - 1) {
       const int j = 32 * g + __ffs(left) - 1;
       left &= left - 1;
       const float s = tmem_ld1(s_at + j) * p.scale_log2;
